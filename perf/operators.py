@@ -214,8 +214,8 @@ def _run_own(st):
     if op == "combine_bwd":
         return nvq.moe_combine_bwd_bf16(st["dout"], st["y"], st["weights"], topk_ids=st["ids"], E=c["E"])
     if c["sigmoid"]:
-        return nvq.moe_router_sigmoid_topk_bwd(st["logits"], st["ids"], st["dweights"])
-    return nvq.moe_router_softmax_topk_bwd(st["logits"], st["ids"], st["dweights"])
+        return nvq.moe_router_sigmoid_topk_bwd(st["weights"], st["logits"], st["ids"], st["dweights"])
+    return nvq.moe_router_softmax_topk_bwd(st["weights"], st["ids"], st["dweights"], c["E"])
 
 
 def _act(z, act):
