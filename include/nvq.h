@@ -440,6 +440,128 @@ int moe_grouped_gemm_nvfp4_bwd(int mode, const uint8_t* a_codes, const uint8_t* 
                                void* ws, size_t ws_bytes, nvq_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* The expert layer in BF16: the unquantized form of the layer above, for    */
+/* the layers that keep full precision and as what both quantized forms are  */
+/* compared with ([AIC] "Key Takeaways", "Architecture highlights": only the */
+/* expert forward is 4-bit). Operands are bf16, products accumulate in fp32  */
+/* and are rounded once. In all calls of this section: outputs must not      */
+/* overlap inputs or the workspace (residual == out is allowed: each element  */
+/* is read by the thread that writes it), and infinities and NaN propagate   */
+/* as in the formulas.                                                       */
+/* ------------------------------------------------------------------------ */
+
+/* Products grouped by expert. Logical token rows r = 0 .. R-1 lie in expert
+ * segments [seg_offsets[e], seg_offsets[e+1]); rows from seg_offsets[E] on
+ * belong to no expert: they are not read, and their outputs are left as they
+ * were. Row r of an operand with a gather is its source row gather[r] / div
+ * (NULL: row r, which must exist: a_rows >= R).
+ *  NVQ_FWD:   out[dst(r)][n] = sum_{k<K} a[src(r)][k] * b[e][n][k]
+ *             (b [E, N, K]: the layout in which weights are stored)
+ *  NVQ_DGRAD: out[dst(r)][n] = sum_{k<K} a[src(r)][k] * b[e][k][n]
+ *             (b [E, K, N]: the same weights, whose rows are now contracted)
+ *             dst(r) = out_scatter[r] (NULL: r); out [*, N]
+ *  NVQ_WGRAD: out[e][m][n] = sum_{r in e} a[src_a(r)][m] * b[src_b(r)][n]
+ *             a [a_rows, M], b [b_rows, N], out [E, M, N]; an empty segment
+ *             gives zeros. accumulate != 0 adds to out instead (a 32-bit sum,
+ *             rounded once; an empty segment leaves its matrix as it was).
+ * M is used by WGRAD only, K by FWD and DGRAD only. out_dtype NVQ_OUT_BF16 or
+ * NVQ_OUT_F32. accumulate and b_gather need WGRAD, out_scatter FWD or DGRAD
+ * (else NVQ_ERR_UNSUPPORTED). Limits (else NVQ_ERR_DIM): M, N, K multiples of
+ * 8 up to 2^22, E <= 4096, R < 2^31 - 256, one expert's weights and the whole
+ * of a gathered operand below 4 GiB - 512, output tiles below 2^31. Not
+ * checked on the host: offsets (clamped to [0, R] on the device) and gather
+ * and scatter entries of rows before seg_offsets[E] (a gathered row outside
+ * its operand reads as zeros; out_scatter entries must be valid and distinct).
+ * The same sums in the same order whatever the launch: results are
+ * reproducible bit for bit. */
+size_t moe_grouped_gemm_bf16_workspace_size(int mode, int64_t E, int64_t R);
+int moe_grouped_gemm_bf16(int mode, const uint16_t* a, int64_t a_rows, const int32_t* a_gather, int32_t a_div,
+                          const uint16_t* b, int64_t b_rows, const int32_t* b_gather, int32_t b_div,
+                          const int32_t* seg_offsets, int64_t E, int64_t R, int64_t M, int64_t N, int64_t K,
+                          void* out, const int32_t* out_scatter, int out_dtype, int accumulate,
+                          void* ws, size_t ws_bytes, nvq_stream_t stream);
+
+/* fc1 + SwiGLU: per expert g, u = x[sorted2assign[r] / k] . w1_e^T (w1
+ * [E, 2*d_ff, d], gate rows first), h[r] = bf16(g * sigmoid(g) * u) from the
+ * fp32 accumulators, for the rows r < offsets[E]; gu (nullable) [T*k, 2*d_ff]
+ * receives bf16 g and u. offsets and sorted2assign as from moe_route.
+ * Limits: d, d_ff multiples of 8, k <= E; else as above. */
+size_t moe_fc1_bf16_workspace_size(int64_t A, int64_t E);
+int moe_fc1_swiglu_bf16(const uint16_t* x, int64_t T, int64_t d, const int32_t* offsets,
+                        const int32_t* sorted2assign, int k, int64_t E, int64_t d_ff, const uint16_t* w1,
+                        uint16_t* h, uint16_t* gu, void* ws, size_t ws_bytes, nvq_stream_t stream);
+
+/* The whole expert forward: route, fc1 + SwiGLU, fc2 (w2 [E, d, d_ff]) with
+ * the rows scattered back: y [T, k, d], unweighted. Rows of y whose expert id
+ * is out of range are left untouched. bufs (nullable): caller-owned offsets,
+ * sorted2assign, h and gu; its other fields must be NULL / 0 (else
+ * NVQ_ERR_UNSUPPORTED). */
+size_t moe_expert_fwd_bf16_workspace_size(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff);
+int moe_expert_fwd_bf16(const uint16_t* x, int64_t T, int64_t d, const int32_t* topk_ids, int k, int64_t E,
+                        int64_t d_ff, const uint16_t* w1, const uint16_t* w2, uint16_t* y,
+                        const nvq_moe_buffers* bufs, void* ws, size_t ws_bytes, nvq_stream_t stream);
+
+/* Dense product with its epilogue (the router's projection, a shared expert):
+ *   z = x . w^T + bias,  out = act(z) + residual
+ * x [M, K], w [N, K], bias [N] fp32 (nullable), residual [M, N] bf16
+ * (nullable), out [M, N] bf16 or fp32; z (nullable) [M, N] receives the
+ * pre-activation in bf16 for the backward; act sees the fp32 one.
+ * NVQ_ACT_SWIGLU: w [2*N, K], bias [2*N], z [M, 2*N] (gate half first),
+ * act(z) = silu(gate) * up. GELU is the exact one (erf), GELU_TANH the tanh
+ * form. Limits as for NVQ_FWD with one expert; M <= 65535 * 64. */
+enum {
+    NVQ_ACT_NONE = 0,
+    NVQ_ACT_RELU = 1,
+    NVQ_ACT_GELU = 2,
+    NVQ_ACT_GELU_TANH = 3,
+    NVQ_ACT_SILU = 4,
+    NVQ_ACT_SWIGLU = 5
+};
+size_t linear_act_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int act);
+int linear_act_bf16(const uint16_t* x, const uint16_t* w, const float* bias, const uint16_t* residual, int64_t M,
+                    int64_t N, int64_t K, int act, void* out, int out_dtype, uint16_t* z, void* ws, size_t ws_bytes,
+                    nvq_stream_t stream);
+
+/* Its backward, from dout [M, N] (bf16 or fp32) and the saved z (unused and
+ * nullable for NVQ_ACT_NONE): dz = dout * act'(z) in fp32,
+ *   dbias[n] = sum_m dz[m][n]  fp32, from the unrounded dz
+ *   dx = dz . w     bf16 [M, K]
+ *   dw = dz^T . x   bf16 or fp32, shape of w
+ * with dz rounded to bf16 as an operand of the two products. Any of dx, dw,
+ * dbias may be NULL (not all); x is needed for dw, w for dx. accumulate != 0
+ * adds to dw and dbias. The residual's gradient is dout. relu'(0) = 0. */
+size_t linear_act_bwd_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int act);
+int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, const uint16_t* w, const uint16_t* z,
+                        int64_t M, int64_t N, int64_t K, int act, uint16_t* dx, void* dw, int dw_dtype,
+                        int accumulate, float* dbias, void* ws, size_t ws_bytes, nvq_stream_t stream);
+
+/* Weighted combine of bf16 expert outputs y [T, k, C] (the unquantized form of
+ * rht32_dequant_combine): out[t] = residual[t] + sum_s w[t][s] * y[t][s],
+ * summed in fp32 in slot order, rounded to bf16. topk_ids (nullable) [T, k]: a
+ * slot whose id is outside [0, E) is dropped: its weight and its row of y are
+ * not used. residual (nullable) [T, C] bf16. Limits: C % 8 == 0, C <= 2^20,
+ * k <= 1024, T*k < 2^31, k*(256 + C/4)*16 below 4 GiB (else NVQ_ERR_DIM). */
+int moe_combine_bf16(const uint16_t* y, const float* w, const int32_t* topk_ids, int64_t E, const uint16_t* residual,
+                     int64_t T, int k, int64_t C, uint16_t* out, nvq_stream_t stream);
+/* Its backward: dy[t][s] = bf16(w[t][s] * dout[t]), dw[t][s] = <dout[t], y[t][s]>
+ * (fp32); dropped slots get zeros in both. The residual's gradient is dout. */
+int moe_combine_bwd_bf16(const uint16_t* dout, const uint16_t* y, const float* w, const int32_t* topk_ids, int64_t E,
+                         int64_t T, int k, int64_t C, uint16_t* dy, float* dw, nvq_stream_t stream);
+
+/* Backward of the routers: dlogits [T, E] fp32 (every element written) from
+ * the forward's weights w [T, k] and ids and the gradient dw [T, k]; with
+ * D = sum_i w_i * dw_i,
+ *   softmax: dlogits[t][id_j] = w_j * (dw_j - D)
+ *   sigmoid: dlogits[t][id_j] = w_j * (1 - sigmoid(logits[t][id_j])) * (dw_j - D)
+ * and zero elsewhere; ids outside [0, E) write nothing, a repeated id adds up.
+ * The bias only steers the choice and has no gradient. Limits as for the
+ * forward (k <= min(E, 64), E <= 1024, T*E < 2^31). */
+int moe_router_softmax_topk_bwd(const float* w, const int32_t* topk_ids, const float* dw, int64_t T, int64_t E,
+                                int k, float* dlogits, nvq_stream_t stream);
+int moe_router_sigmoid_topk_bwd(const float* w, const float* logits, const int32_t* topk_ids, const float* dw,
+                                int64_t T, int64_t E, int k, float* dlogits, nvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Converter checks. Every code, scale byte and bf16 output above comes from */
 /* a handful of gfx950 conversion instructions (and two software encoders);  */
 /* their exactness against the format rules (NVFP4 about 4.5 bits per value */

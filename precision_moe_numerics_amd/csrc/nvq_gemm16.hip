@@ -1,0 +1,124 @@
+// nvq_gemm16.hip -- tile tables and launches of the BF16 matrix products.
+#include "nvq_gemm16.hpp"
+
+#include <algorithm>
+
+namespace nvq {
+namespace g16 {
+
+constexpr int kTabThreads = 1024;
+constexpr int kMaxE = 4096;
+
+// The m-tiles of E expert segments, one entry each: expert, first row, end of
+// the expert's rows. One workgroup: prefix sums of the experts' tile counts in
+// LDS (four experts per thread), then every thread fills entries t, t + 1024,
+// ... by binary search. Offsets are clamped to [0, rows] and a decreasing one
+// counts as an empty segment, so no entry points outside the rows and none is
+// written past `cap`.
+__global__ __launch_bounds__(kTabThreads) void k_tile_table(const int32_t* __restrict__ seg, int E, int rows, int tm,
+                                                            int cap, int32_t* __restrict__ count,
+                                                            Tile* __restrict__ tiles) {
+    __shared__ int buf[kTabThreads];
+    __shared__ int first[kMaxE + 1];
+    const int t = threadIdx.x;
+    auto off = [&](int e) { return min(max(seg[e], 0), rows); };
+    int n[4], local = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int e = 4 * t + j;
+        n[j] = e < E ? (max(off(e + 1) - off(e), 0) + tm - 1) / tm : 0;
+        local += n[j];
+    }
+    int total;
+    int base = block_exclusive_scan(local, buf, &total);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (4 * t + j < E) first[4 * t + j] = base;
+        base += n[j];
+    }
+    total = min(total, cap);
+    if (t == 0) {
+        first[E] = total;
+        *count = total;
+    }
+    __syncthreads();
+    for (int i = t; i < total; i += kTabThreads) {
+        int lo = 0, hi = E;  // the last expert whose first tile is at or before i
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= i) lo = mid; else hi = mid;
+        }
+        Tile v;
+        v.e = lo;
+        v.row0 = off(lo) + (i - first[lo]) * tm;
+        v.row_end = max(off(lo + 1), off(lo));
+        v.pad = 0;
+        tiles[i] = v;
+    }
+}
+
+template <int MODE, int EPI, int TM, int TN, int WM, int WN>
+void run(Args p, int64_t m_tiles_cap, hipStream_t s) {
+    constexpr int TNO = EPI == kEpiGlu ? TN / 2 : TN;
+    p.n_tiles = (p.N + TNO - 1) / TNO;
+    const int64_t grid = m_tiles_cap * p.n_tiles;
+    hipLaunchKernelGGL((k_gemm16<MODE, EPI, TM, TN, WM, WN>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, p);
+}
+
+}  // namespace g16
+
+using namespace g16;
+
+constexpr int kMinTileM = 128;
+
+static int64_t tile_cap(int64_t rows, int64_t E, int tm) { return (rows + tm - 1) / tm + E; }
+
+size_t gemm16_ws_bytes(int64_t rows, int64_t E) {
+    Carver c(nullptr);
+    c.take<int32_t>(1);
+    c.take<Tile>((size_t)tile_cap(std::max<int64_t>(rows, 0), std::max<int64_t>(E, 1), kMinTileM));
+    return c.need;
+}
+
+bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int64_t N, int64_t K) {
+    const int64_t i31 = (int64_t)1 << 31;
+    if (rows < 0 || rows >= i31 - 256 || E < 1 || E > kMaxE || N < 8 || N % 8 != 0 || N > (1 << 22)) return false;
+    if (mode == kWgrad) {
+        if (M < 8 || M % 8 != 0 || M > (1 << 22)) return false;
+        return E * ((M + 127) / 128) * ((N + 127) / 128) < i31;
+    }
+    if (K < 8 || K % 8 != 0 || K > (1 << 22)) return false;
+    // one expert's weights are one buffer descriptor
+    if ((glu ? 2 : 1) * N * K * 2 > kMaxBytes) return false;
+    return tile_cap(rows, E, kMinTileM) * ((N + 63) / 64) < i31;
+}
+
+void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
+    constexpr int TM = 128;
+    int64_t mt;
+    if (mode == kWgrad) {
+        p.m_tiles = (p.M + TM - 1) / TM;
+        mt = (int64_t)p.m_tiles * p.E;
+        run<kWgrad, kEpiOut, TM, 128, 2, 2>(p, mt, s);
+        return;
+    }
+    if (p.rows == 0) return;
+    if (p.seg) {
+        Carver cv(ws);
+        int32_t* count = cv.take<int32_t>(1);
+        mt = tile_cap(p.rows, p.E, TM);
+        Tile* tiles = cv.take<Tile>((size_t)mt);
+        hipLaunchKernelGGL(k_tile_table, dim3(1), dim3(kTabThreads), 0, s, p.seg, p.E, p.rows, TM, (int)mt, count,
+                           tiles);
+        p.tiles = tiles;
+        p.tile_count = count;
+    } else {
+        mt = (p.rows + TM - 1) / TM;
+    }
+    if (mode == kDgrad) run<kDgrad, kEpiOut, TM, 128, 2, 2>(p, mt, s);
+    else if (epi == kEpiGlu) run<kFwd, kEpiGlu, TM, 128, 2, 2>(p, mt, s);
+    else if (epi == kEpiAct) run<kFwd, kEpiAct, TM, 128, 2, 2>(p, mt, s);
+    else run<kFwd, kEpiOut, TM, 128, 2, 2>(p, mt, s);
+}
+
+}  // namespace nvq

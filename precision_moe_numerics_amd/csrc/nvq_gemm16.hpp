@@ -1,0 +1,473 @@
+// nvq_gemm16.hpp -- BF16 matrix products on the gfx950 matrix pipe, shared by
+// the grouped products of the unquantized expert layer (nvq_moe16.hip) and the
+// dense product with its epilogue (nvq_linear.hip).
+//
+// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) for three operand
+// arrangements, with bf16 operands and fp32 accumulation:
+//   FWD    A rows and B rows hold k contiguously (x W^T);
+//   DGRAD  A as above, B holds n contiguously (g W, W as the forward keeps it);
+//   WGRAD  A and B hold m and n contiguously, k runs over token rows (g^T x).
+// Rows come in expert segments (or one dense block), may be gathered on the
+// way in and scattered on the way out.
+#pragma once
+
+#include "nvq_device.hpp"
+#include "nvq_host.hpp"
+
+namespace nvq {
+namespace g16 {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };   // operand arrangement
+enum { kEpiOut = 0, kEpiAct = 1, kEpiGlu = 2 };
+
+constexpr int kBK = 64;          // K per LDS stage
+constexpr int kWgradRows = 16;   // (unused rows of a segment cost at most a stage)
+
+// One m-tile of the row-segmented arrangements, written by k_tile_table.
+struct Tile {
+    int32_t e, row0, row_end, pad;
+};
+
+struct Args {
+    const uint16_t* a;
+    const uint16_t* b;
+    const int32_t* a_gather;  // source row of logical row r: a_gather[r] / a_div (NULL: r)
+    const int32_t* b_gather;  // WGRAD only
+    const int32_t* seg;       // [E + 1] (NULL: one segment [0, rows))
+    const Tile* tiles;        // FWD, DGRAD with segments: [count], count at tile_count
+    const int32_t* tile_count;
+    const int32_t* scatter;   // destination of logical row r (NULL: r)
+    void* out;
+    const float* bias;
+    const uint16_t* residual;
+    uint16_t* z;              // saved pre-activation
+    int64_t a_bytes, b_bytes; // gathered operands: bytes of the whole source (bounds the loads)
+    uint32_t a_div, b_div;
+    int32_t lda, ldb;         // row strides in elements
+    int32_t E, rows;          // experts; logical token rows
+    int32_t M, N, K;          // WGRAD: M x N outputs; FWD, DGRAD: N columns (GLU: N outputs), K
+    int32_t m_tiles, n_tiles;
+    int32_t out_f32, accumulate, act;
+};
+
+// ------------------------------------------------------------------ LDS staging
+// 16 bytes per lane from a buffer straight into LDS at lds_addr + 16 * lane.
+// A lane whose offset lies at or past the descriptor's byte count gets zeros
+// (kNowhere always does): ragged rows, columns and K tails need no branch and
+// contribute nothing. The instruction has no destination register; the caller
+// waits with wait_vm before the barrier that publishes the stage. It is
+// written out because a builtin load into LDS makes the compiler drain every
+// load in flight before the next LDS read of any stage.
+constexpr uint32_t kNowhere = 0xFFFFFFE0u;
+constexpr int64_t kMaxBytes = 0xFFFFFE00ll;  // largest descriptor: every real offset below kNowhere
+
+__device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t off, uint32_t lds_addr) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds"
+        :
+        : "s"(lds_addr), "v"(off), "s"(rsrc)
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Buffer descriptor over [p, p + bytes), bytes clamped to [0, kMaxBytes].
+__device__ __forceinline__ i32x4 make_rsrc(const void* p, int64_t bytes) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const int64_t n = bytes < 0 ? 0 : bytes > kMaxBytes ? kMaxBytes : bytes;
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)u);
+    r[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(u >> 32) & 0xFFFFu));
+    r[2] = __builtin_amdgcn_readfirstlane((int)(uint32_t)n);
+    r[3] = 0x00020000;
+    return r;
+}
+
+typedef const __attribute__((address_space(3))) s16x8 lds_s16x8;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+__device__ __forceinline__ uint32_t lds_off(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+__device__ __forceinline__ void stage_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Swizzle of a stage that holds n (or m) contiguously, R columns per k row:
+// 16-byte chunk c of k row k sits at slot c ^ rkey(k). The four k rows that one
+// transposing read touches per 16 lanes, and the next 16 lanes' four, then lie
+// in different 32-byte bank groups.
+__device__ __forceinline__ uint32_t rkey(uint32_t k) { return 2u * ((k & 3u) | ((k >> 1) & 4u)); }
+
+// MFMA operand of 16 rows starting at row `r0` of a stage that holds k
+// contiguously (128-byte rows, chunk c of row r at slot c ^ (r & 7)):
+// lane l gets row l % 16, k = 32 ks + 8 (l / 16) .. + 7.
+__device__ __forceinline__ bf16x8 frag_k(const uint8_t* st, int r0, int ks, int lane) {
+    const int r = r0 + (lane & 15);
+    const int c = ks * 4 + (lane >> 4);
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const s16x8*>(st + r * 128 + ((c ^ (r & 7)) << 4)));
+}
+
+// The same operand from a stage of R columns per k row: two transposing reads
+// of four k each. Lane i of a 16-lane group passes the address of k row i / 4,
+// columns 4 (i % 4) .. + 3 and receives column i of the four rows.
+template <int R>
+__device__ __forceinline__ bf16x8 frag_r(const uint8_t* st, int r0, int ks, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    const uint32_t k = ks * 32 + 8 * g + (i >> 2);
+    const uint32_t c = (uint32_t)(r0 >> 3) + ((i >> 1) & 1);
+    // k + 4 has the same key
+    const uint8_t* q = st + k * (R * 2) + ((c ^ rkey(k)) << 4) + ((i & 1) << 3);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)q);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(q + 4 * R * 2));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// ------------------------------------------------------------------ activations
+// In fp32. exp overflow gives inf and a reciprocal of 0, the limits wanted.
+__device__ __forceinline__ float sigmoidf(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
+__device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)); }
+// 0.5 (1 + tanh(t)) = sigmoid(2 t)
+__device__ __forceinline__ float gelu_tanh(float v) {
+    return v * sigmoidf(1.5957691216057308f * (v + 0.044715f * v * v * v));
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float v) {
+    if (ACT == NVQ_ACT_RELU) return v > 0.0f ? v : (v != v ? v : 0.0f);
+    if (ACT == NVQ_ACT_GELU) return gelu_erf(v);
+    if (ACT == NVQ_ACT_GELU_TANH) return gelu_tanh(v);
+    if (ACT == NVQ_ACT_SILU) return v * sigmoidf(v);
+    return v;
+}
+
+// ------------------------------------------------------------------ epilogue
+__device__ __forceinline__ f32x4 load4_bf16(const uint16_t* p) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+    return (f32x4){__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u), __uint_as_float(w[1] << 16),
+                   __uint_as_float(w[1] & 0xFFFF0000u)};
+}
+__device__ __forceinline__ void store4_bf16(uint16_t* p, f32x4 v) {
+    *reinterpret_cast<u32x2*>(p) = (u32x2){bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+}
+__device__ __forceinline__ void store4(void* out, int64_t idx, f32x4 v, bool f32) {
+    if (f32) *reinterpret_cast<f32x4*>(static_cast<float*>(out) + idx) = v;
+    else store4_bf16(static_cast<uint16_t*>(out) + idx, v);
+}
+
+// Output position of a wave: lane l holds, of its 16 x 16 block (i, j), row
+// row0 + 16 i + l % 16 and columns col0 + 16 j + 4 (l / 16) .. + 3 (the
+// operands are passed to the MFMA as B, A, so a lane's four values are
+// neighbours along n and are stored together).
+struct Pos {
+    int64_t out_base;  // WGRAD: first element of the expert's matrix
+    int row0, row_end, col0;
+};
+
+template <int EPI, int ACT, int MF, int NF>
+__device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[MF][NF], const Pos& o, int lane) {
+    const int N = p.N;
+    const int c4 = (lane >> 4) * 4;
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+        const int m = o.row0 + 16 * i + (lane & 15);
+        if (m >= o.row_end) continue;
+        if (EPI == kEpiOut) {
+            const int64_t r = p.scatter ? p.scatter[m] : m;
+            const int64_t base = o.out_base + r * N;
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const int n = o.col0 + 16 * j + c4;
+                if (n >= N) continue;
+                f32x4 v = acc[i][j];
+                if (p.accumulate)
+                    v += p.out_f32 ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.out) + base + n)
+                                   : load4_bf16(static_cast<const uint16_t*>(p.out) + base + n);
+                store4(p.out, base + n, v, p.out_f32);
+            }
+        } else if (EPI == kEpiAct) {
+            const int64_t base = (int64_t)m * N;
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const int n = o.col0 + 16 * j + c4;
+                if (n >= N) continue;
+                f32x4 v = acc[i][j];
+                if (p.bias) v += *reinterpret_cast<const f32x4*>(p.bias + n);
+                if (p.z) store4_bf16(p.z + base + n, v);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) v[t] = act_fwd<ACT>(v[t]);
+                if (p.residual) v += load4_bf16(p.residual + base + n);
+                store4(p.out, base + n, v, p.out_f32);
+            }
+        } else {
+            const int64_t base = (int64_t)m * N;
+#pragma unroll
+            for (int j = 0; j < NF / 2; ++j) {
+                const int n = o.col0 + 16 * j + c4;
+                if (n >= N) continue;
+                f32x4 g = acc[i][2 * j], u = acc[i][2 * j + 1];
+                if (p.bias) {
+                    g += *reinterpret_cast<const f32x4*>(p.bias + n);
+                    u += *reinterpret_cast<const f32x4*>(p.bias + N + n);
+                }
+                if (p.z) {
+                    store4_bf16(p.z + 2 * base + n, g);
+                    store4_bf16(p.z + 2 * base + N + n, u);
+                }
+                f32x4 v;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) v[t] = g[t] * sigmoidf(g[t]) * u[t];
+                if (p.residual) v += load4_bf16(p.residual + base + n);
+                store4(p.out, base + n, v, p.out_f32);
+            }
+        }
+    }
+}
+
+// One scalar branch on the activation, outside the unrolled stores.
+template <int EPI, int MF, int NF>
+__device__ __forceinline__ void epilogue(const Args& p, const f32x4 (&acc)[MF][NF], const Pos& o, int lane) {
+    if constexpr (EPI != kEpiAct) {
+        epilogue_act<EPI, NVQ_ACT_NONE>(p, acc, o, lane);
+    } else {
+        switch (p.act) {
+            case NVQ_ACT_RELU: epilogue_act<EPI, NVQ_ACT_RELU>(p, acc, o, lane); break;
+            case NVQ_ACT_GELU: epilogue_act<EPI, NVQ_ACT_GELU>(p, acc, o, lane); break;
+            case NVQ_ACT_GELU_TANH: epilogue_act<EPI, NVQ_ACT_GELU_TANH>(p, acc, o, lane); break;
+            case NVQ_ACT_SILU: epilogue_act<EPI, NVQ_ACT_SILU>(p, acc, o, lane); break;
+            default: epilogue_act<EPI, NVQ_ACT_NONE>(p, acc, o, lane); break;
+        }
+    }
+}
+
+// Scalar load of a table entry at a wave-uniform index.
+template <typename T>
+__device__ __forceinline__ T sload(const T* base, int64_t i) {
+    typedef const __attribute__((address_space(4))) T ct;
+    return ((ct*)base)[i];
+}
+
+// Offset of a source row, or kNowhere.
+__device__ __forceinline__ uint32_t row_off(bool ok, uint32_t row, uint32_t stride_bytes) {
+    return ok ? row * stride_bytes : kNowhere;
+}
+
+// ------------------------------------------------------------------ the kernel
+// Tile TM x TN, WM x WN waves; every wave holds (TM / WM) x (TN / WN) outputs
+// as 16 x 16 blocks. Two LDS stages of kBK: the next stage is in flight while
+// this one is multiplied.
+template <int MODE, int EPI, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
+    constexpr int NW = WM * WN;
+    constexpr int MF = TM / WM / 16, NF = TN / WN / 16;
+    constexpr bool A_R = MODE == kWgrad, B_R = MODE != kFwd;
+    constexpr int CA = TM * 8 / (64 * NW), CB = TN * 8 / (64 * NW);  // 16-byte loads per lane and stage
+    constexpr int kStage = (TM + TN) * 128;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kStage];
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int lane = threadIdx.x & 63;
+    const int wm = wave / WN, wn = wave % WN;
+    const uint32_t lds0 = lds_off(&lds[0][0]);
+
+    // consecutive virtual ids on one XCD (workgroups are dealt to the 8 XCDs round robin)
+    const int G = gridDim.x;
+    const int t = (G % 8 == 0) ? (int)((blockIdx.x % 8) * (G / 8) + blockIdx.x / 8) : (int)blockIdx.x;
+    const int nt = t % p.n_tiles, mt = t / p.n_tiles;
+    int e = 0, row0, row_end;  // FWD, DGRAD: token rows; WGRAD: output rows
+    int k0 = 0, kend = p.K;    // WGRAD: token rows
+    if (MODE == kWgrad) {
+        e = mt / p.m_tiles;
+        if (e >= p.E) return;
+        row0 = (mt % p.m_tiles) * TM;
+        row_end = p.M;
+        if (p.seg) {
+            k0 = min(max(sload(p.seg, e), 0), p.rows);
+            kend = min(max(sload(p.seg, e + 1), k0), p.rows);
+        } else {
+            kend = p.rows;
+        }
+    } else if (p.tiles) {
+        if (mt >= sload(p.tile_count, 0)) return;
+        e = sload(&p.tiles[mt].e, 0);
+        row0 = sload(&p.tiles[mt].row0, 0);
+        row_end = sload(&p.tiles[mt].row_end, 0);
+    } else {
+        row0 = mt * TM;
+        row_end = p.rows;
+        if (row0 >= row_end) return;
+    }
+    constexpr int TNO = EPI == kEpiGlu ? TN / 2 : TN;  // output columns of a tile
+    const int col0 = nt * TNO;
+
+    // ---- operand addressing: lane offsets (bytes) within a descriptor whose
+    // base advances along K
+    const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
+    uint32_t ao[CA], bo[CB];
+    const uint16_t *abase, *bbase;
+    int64_t a_lim, b_lim;       // bytes of the descriptor at k0
+    const int kc = ((lane & 7) ^ (lane >> 3)) * 8;  // k of this lane's chunk in K-contiguous stages
+    if constexpr (!A_R) {
+        const bool gat = p.a_gather != nullptr;
+        abase = gat ? p.a : p.a + (int64_t)row0 * p.lda;
+        a_lim = gat ? p.a_bytes : (int64_t)(row_end - row0) * lda2;
+#pragma unroll
+        for (int i = 0; i < CA; ++i) {
+            const int rl = (i * NW + wave) * 8 + (lane >> 3);
+            const bool ok = row0 + rl < row_end;
+            uint32_t src = rl;
+            if (gat) src = (uint32_t)p.a_gather[ok ? row0 + rl : row0] / p.a_div;
+            ao[i] = ok ? src * lda2 + kc * 2 : kNowhere;
+        }
+    } else {
+        abase = p.a_gather ? p.a : p.a + (int64_t)k0 * p.lda;
+        a_lim = p.a_gather ? p.a_bytes : (int64_t)(kend - k0) * lda2;
+    }
+    if constexpr (!B_R) {
+        constexpr int rows_per = EPI == kEpiGlu ? 2 : 1;
+        bbase = p.b + (int64_t)e * rows_per * p.N * p.ldb;
+        b_lim = (int64_t)rows_per * p.N * ldb2;
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+            const int r = (i * NW + wave) * 8 + (lane >> 3);
+            int n, src;
+            if (EPI == kEpiGlu) {  // blocks of 16: gate, up, gate, up, ...
+                n = col0 + (r >> 5) * 16 + (r & 15);
+                src = ((r >> 4) & 1) * p.N + n;
+            } else {
+                n = src = col0 + r;
+            }
+            bo[i] = n < p.N ? (uint32_t)src * ldb2 + kc * 2 : kNowhere;
+        }
+    } else if constexpr (MODE == kDgrad) {
+        bbase = p.b + (int64_t)e * p.K * p.ldb;
+        b_lim = (int64_t)p.K * ldb2;
+    } else {
+        bbase = p.b_gather ? p.b : p.b + (int64_t)k0 * p.ldb;
+        b_lim = p.b_gather ? p.b_bytes : (int64_t)(kend - k0) * ldb2;
+    }
+    // K-strided stages: 16-byte chunk id = k row * (R / 8) + slot
+    auto r_off = [&](int i, int R, int c0, int lim, uint32_t ld2, uint32_t* krow) {
+        const int id = (i * NW + wave) * 64 + lane;
+        const uint32_t k = (uint32_t)id / (uint32_t)(R / 8), slot = (uint32_t)id % (uint32_t)(R / 8);
+        const int c = c0 + (int)(slot ^ rkey(k)) * 8;
+        *krow = k;
+        return c < lim ? (uint32_t)c * 2u : kNowhere;
+    };
+    uint32_t ak[CA], bk[CB];
+    if constexpr (A_R) {
+#pragma unroll
+        for (int i = 0; i < CA; ++i) ao[i] = r_off(i, TM, row0, row_end, lda2, &ak[i]);
+    }
+    if constexpr (B_R) {
+#pragma unroll
+        for (int i = 0; i < CB; ++i) bo[i] = r_off(i, TN, col0, p.N, ldb2, &bk[i]);
+    }
+
+    const int klen = kend - k0;
+    const int nk = (klen + kBK - 1) / kBK;
+    auto issue = [&](int s, int buf) {
+        const uint32_t la = lds0 + buf * kStage, lb = la + TM * 128;
+        const int k = s * kBK;
+        if constexpr (!A_R) {
+            const i32x4 ra = make_rsrc(abase + k, a_lim - (int64_t)k * 2);
+            const bool ok = k + kc < klen;
+#pragma unroll
+            for (int i = 0; i < CA; ++i) dma16(ra, ok ? ao[i] : kNowhere, la + (i * NW + wave) * 1024);
+        } else {
+            const bool gat = p.a_gather != nullptr;
+            const i32x4 ra = gat ? make_rsrc(abase, a_lim)
+                                 : make_rsrc(abase + (int64_t)k * p.lda, a_lim - (int64_t)k * lda2);
+#pragma unroll
+            for (int i = 0; i < CA; ++i) {
+                const bool ok = k + (int)ak[i] < klen && ao[i] != kNowhere;
+                uint32_t row = ak[i];
+                if (gat) row = (uint32_t)p.a_gather[ok ? k0 + k + (int)ak[i] : k0] / p.a_div;
+                dma16(ra, ok ? row * lda2 + ao[i] : kNowhere, la + (i * NW + wave) * 1024);
+            }
+        }
+        if constexpr (!B_R) {
+            const i32x4 rb = make_rsrc(bbase + k, b_lim - (int64_t)k * 2);
+            const bool ok = k + kc < klen;
+#pragma unroll
+            for (int i = 0; i < CB; ++i) dma16(rb, ok ? bo[i] : kNowhere, lb + (i * NW + wave) * 1024);
+        } else {
+            const bool gat = MODE == kWgrad && p.b_gather != nullptr;
+            const i32x4 rb = gat ? make_rsrc(bbase, b_lim)
+                                 : make_rsrc(bbase + (int64_t)k * p.ldb, b_lim - (int64_t)k * ldb2);
+#pragma unroll
+            for (int i = 0; i < CB; ++i) {
+                const bool ok = k + (int)bk[i] < klen && bo[i] != kNowhere;
+                uint32_t row = bk[i];
+                if (gat) row = (uint32_t)p.b_gather[ok ? k0 + k + (int)bk[i] : k0] / p.b_div;
+                dma16(rb, ok ? row * ldb2 + bo[i] : kNowhere, lb + (i * NW + wave) * 1024);
+            }
+        }
+    };
+
+    f32x4 acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+
+    if (nk > 0) issue(0, 0);
+    for (int s = 0; s < nk; ++s) {
+        wait_vm<0>();
+        stage_barrier();
+        if (s + 1 < nk) issue(s + 1, (s + 1) & 1);
+        const uint8_t* sa = lds[s & 1];
+        const uint8_t* sb = sa + TM * 128;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 av[MF], bv[NF];
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                const int r0 = wm * (TM / WM) + 16 * i;
+                if constexpr (A_R) av[i] = frag_r<TM>(sa, r0, ks, lane);
+                else av[i] = frag_k(sa, r0, ks, lane);
+            }
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                const int r0 = wn * (TN / WN) + 16 * j;
+                if constexpr (B_R) bv[j] = frag_r<TN>(sb, r0, ks, lane);
+                else bv[j] = frag_k(sb, r0, ks, lane);
+            }
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], av[i], acc[i][j], 0, 0, 0);
+        }
+    }
+    Pos o;
+    o.out_base = MODE == kWgrad ? (int64_t)e * p.M * p.N : 0;
+    o.row0 = row0 + wm * (TM / WM);
+    o.row_end = row_end;
+    o.col0 = col0 + wn * (TNO / WN);
+    epilogue<EPI>(p, acc, o, lane);
+}
+
+}  // namespace g16
+
+// Launches the product described by `p` (operands, sizes, epilogue; tiles and
+// tile counts are filled in here). `ws` holds gemm16_ws_bytes for segmented
+// FWD and DGRAD. mode is g16::kFwd, kDgrad or kWgrad.
+void launch_gemm16(int mode, int epi, g16::Args p, void* ws, hipStream_t s);
+size_t gemm16_ws_bytes(int64_t rows, int64_t E);
+// Whether every tile count and lane offset of the product fits (see the limits in nvq.h).
+bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int64_t N, int64_t K);
+
+}  // namespace nvq
