@@ -1,5 +1,5 @@
 // nvq_gemm16.hip -- tile tables and launches of the BF16 matrix products.
-#include "nvq_gemm16.hpp"
+#include "nvq_gemm16_big.hpp"
 
 #include <algorithm>
 
@@ -65,6 +65,15 @@ void run(Args p, int64_t m_tiles_cap, hipStream_t s) {
     hipLaunchKernelGGL((k_gemm16<MODE, EPI, TM, TN, WM, WN>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, p);
 }
 
+template <int MODE, int EPI>
+void run_big(Args p, int64_t m_tiles_cap, hipStream_t s) {
+    constexpr int TNO = EPI == kEpiGlu ? kBigT / 2 : kBigT;
+    p.n_tiles = (p.N + TNO - 1) / TNO;
+    const int64_t total = m_tiles_cap * p.n_tiles;
+    const int64_t grid = std::min<int64_t>(total, device_cus());
+    hipLaunchKernelGGL((k_gemm16_big<MODE, EPI>), dim3((unsigned)grid), dim3(64 * kBigWaves), 0, s, p, (int)total);
+}
+
 }  // namespace g16
 
 using namespace g16;
@@ -94,31 +103,46 @@ bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int6
 }
 
 void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
-    constexpr int TM = 128;
-    int64_t mt;
+    const int64_t n_big = (p.N + (epi == kEpiGlu ? 127 : 255)) / (epi == kEpiGlu ? 128 : 256);
+    const int cus = device_cus();
     if (mode == kWgrad) {
-        p.m_tiles = (p.M + TM - 1) / TM;
-        mt = (int64_t)p.m_tiles * p.E;
-        run<kWgrad, kEpiOut, TM, 128, 2, 2>(p, mt, s);
+        const int64_t mb = (p.M + 255) / 256 * (int64_t)p.E;
+        if (mb * n_big >= cus) {
+            p.m_tiles = (p.M + 255) / 256;
+            run_big<kWgrad, kEpiOut>(p, mb, s);
+        } else {
+            p.m_tiles = (p.M + 127) / 128;
+            run<kWgrad, kEpiOut, 128, 128, 2, 2>(p, (int64_t)p.m_tiles * p.E, s);
+        }
         return;
     }
     if (p.rows == 0) return;
+    const bool big = p.rows / p.E >= 128 && (p.rows + 255) / 256 * n_big >= cus;
+    const int tm = big ? 256 : 128;
+    int64_t mt;
     if (p.seg) {
         Carver cv(ws);
         int32_t* count = cv.take<int32_t>(1);
-        mt = tile_cap(p.rows, p.E, TM);
+        mt = tile_cap(p.rows, p.E, tm);
         Tile* tiles = cv.take<Tile>((size_t)mt);
-        hipLaunchKernelGGL(k_tile_table, dim3(1), dim3(kTabThreads), 0, s, p.seg, p.E, p.rows, TM, (int)mt, count,
+        hipLaunchKernelGGL(k_tile_table, dim3(1), dim3(kTabThreads), 0, s, p.seg, p.E, p.rows, tm, (int)mt, count,
                            tiles);
         p.tiles = tiles;
         p.tile_count = count;
     } else {
-        mt = (p.rows + TM - 1) / TM;
+        mt = (p.rows + tm - 1) / tm;
     }
-    if (mode == kDgrad) run<kDgrad, kEpiOut, TM, 128, 2, 2>(p, mt, s);
-    else if (epi == kEpiGlu) run<kFwd, kEpiGlu, TM, 128, 2, 2>(p, mt, s);
-    else if (epi == kEpiAct) run<kFwd, kEpiAct, TM, 128, 2, 2>(p, mt, s);
-    else run<kFwd, kEpiOut, TM, 128, 2, 2>(p, mt, s);
+    if (big) {
+        if (mode == kDgrad) run_big<kDgrad, kEpiOut>(p, mt, s);
+        else if (epi == kEpiGlu) run_big<kFwd, kEpiGlu>(p, mt, s);
+        else if (epi == kEpiAct) run_big<kFwd, kEpiAct>(p, mt, s);
+        else run_big<kFwd, kEpiOut>(p, mt, s);
+        return;
+    }
+    if (mode == kDgrad) run<kDgrad, kEpiOut, 128, 128, 2, 2>(p, mt, s);
+    else if (epi == kEpiGlu) run<kFwd, kEpiGlu, 128, 128, 2, 2>(p, mt, s);
+    else if (epi == kEpiAct) run<kFwd, kEpiAct, 128, 128, 2, 2>(p, mt, s);
+    else run<kFwd, kEpiOut, 128, 128, 2, 2>(p, mt, s);
 }
 
 }  // namespace nvq

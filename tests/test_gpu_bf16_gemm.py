@@ -267,3 +267,53 @@ def test_streams_and_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, expect[r]), f"replay {r}"
+
+
+# ------------------------------------------------------------------ sizes that take the 256 x 256 tiles
+@pytest.mark.parametrize("mode", [nvq.FWD, nvq.DGRAD])
+@pytest.mark.parametrize("lens,N,K", [([257, 0, 64, 511, 1], 16392, 72), ([700], 22008, 40), ([300, 200], 22000, 8),
+                                      ([513, 129], 22016, 256), ([65, 320], 33000, 328)])
+def test_rows_large(mode, lens, N, K):
+    R, E = sum(lens), len(lens)
+    T = R // 2 + 1
+    a, b = rnd(101, T, K), rnd(102, E, *((N, K) if mode == nvq.FWD else (K, N)))
+    g = perm(103, 2 * R)[:R] % (2 * T)
+    dst = perm(104, R)
+    out = torch.full((R + 1, N), 77.0, dtype=BF16, device="cuda")
+    nvq.moe_grouped_gemm_bf16(mode, a, b, seg_of(lens), a_gather=g, a_div=2, out_scatter=dst, out=out)
+    ref, err = ref_rows(mode, a[(g // 2).long()], b, segments(lens), R)
+    check(out.cpu()[dst.long().cpu()], ref, out_bound(ref, err, False), "gathered and scattered")
+    assert (out[R] == 77.0).all()
+    plain = nvq.moe_grouped_gemm_bf16(mode, a[(g // 2).long()], b, seg_of(lens), out_dtype=F32)
+    check(plain, ref, out_bound(ref, err, True), "plain")
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("lens,M,N", [([40, 0, 0, 1, 300, 33, 0, 64, 95], 1032, 1544), ([31], 4104, 4096),
+                                      ([0, 5] * 40, 520, 264), ([0] * 300, 264, 8)])
+def test_wgrad_large(gather, lens, M, N):
+    R, E = sum(lens), len(lens)
+    T = R // 2 + 1
+    ga = perm(111, 2 * R)[:R] % (2 * T) if gather else None
+    a, b = rnd(112, T if gather else R, M), rnd(113, R, N)
+    start = rnd(114, E, M, N, dtype=F32)
+    out = start.clone()
+    nvq.moe_grouped_gemm_bf16(nvq.WGRAD, a, b, seg_of(lens), a_gather=ga, a_div=2 if gather else 1, out=out,
+                              accumulate=gather)
+    A, B, off = d64(a) if ga is None else d64(a)[(ga // 2).long().cpu()], d64(b), segments(lens)
+    for e in range(E):
+        ref, err = matmul_bound(A[off[e]:off[e + 1]].T, B[off[e]:off[e + 1]])
+        if gather:
+            ref = ref + d64(start[e])
+        check(out[e], ref, out_bound(ref, err + U(ref), True), f"expert {e}")
+
+
+def test_fc1_large():
+    T, d, E, k, f = 1100, 104, 5, 2, 3304
+    x, w1 = rnd(121, T, d), rnd(122, E, 2 * f, d, std=d ** -0.5)
+    _, ids, _ = routed(123, T, E, k, 1.0)
+    off, order, _ = nvq.moe_route(ids, E)
+    h, gu = nvq.moe_fc1_swiglu_bf16(x, off, order, k, w1, save_gu=True)
+    z, dz, hr, dh = ref_fc1(x, w1, off.tolist(), order, k)
+    check(gu, z, out_bound(z, dz, False), "gu")
+    check(h, hr, out_bound(hr, dh, False), "h")

@@ -54,6 +54,21 @@ def test_linear(act, M, N, K, bias, residual, f32):
 
 
 @pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("f32", [False, True])
+def test_linear_large(act, f32):
+    """Sizes that take the 256 x 256 tiles, with ragged edges on every side."""
+    M, N, K = 2090, 7240, 72
+    rows = 2 * N if act == SWIGLU else N
+    x, w = rnd(8, M, K), rnd(9, rows, K, std=2 * K ** -0.5)
+    b, r = rnd(3, rows, dtype=F32), rnd(4, M, N)
+    out, z = nvq.linear_act_bf16(x, w, bias=b, act=act, residual=r, out_dtype=F32 if f32 else BF16, save_z=True)
+    zr, dz = pre(x, w, b)
+    check(z, zr, out_bound(zr, dz, False), "z")
+    ref = act_ref(zr, act, N)[0] + d64(r)
+    check(out, ref, out_bound(ref, act_bound(zr, dz, act, N) + ref.abs() * U23, f32), "out")
+
+
+@pytest.mark.parametrize("act", ACTS)
 def test_linear_extreme_pre_activations(act):
     """Pre-activations from -300 to 300 set by the bias: no overflow where the limit is finite."""
     N = 64
