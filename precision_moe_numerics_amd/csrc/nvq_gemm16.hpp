@@ -139,7 +139,19 @@ __device__ __forceinline__ bf16x8 frag_r(const uint8_t* st, int r0, int ks, int 
 // ------------------------------------------------------------------ activations
 // In fp32. exp overflow gives inf and a reciprocal of 0, the limits wanted.
 __device__ __forceinline__ float sigmoidf(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
-__device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)); }
+// erf by Abramowitz and Stegun 7.1.26: for x >= 0, 1 - (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x),
+// within 1.5e-7 of erf. (The library's erff, exact to an ulp, is three times as many instructions, and an epilogue
+// of 128 of them per lane took 20 us of a 256 x 256 tile.)
+__device__ __forceinline__ float erf_as(float v) {
+    const float x = fabsf(v);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+    float q = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+    q = __builtin_fmaf(q, t, 1.421413741f);
+    q = __builtin_fmaf(q, t, -0.284496736f);
+    q = __builtin_fmaf(q, t, 0.254829592f);
+    return __builtin_copysignf(__builtin_fmaf(-q * t, __expf(-x * x), 1.0f), v);
+}
+__device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * (1.0f + erf_as(v * 0.70710678118654752f)); }
 // 0.5 (1 + tanh(t)) = sigmoid(2 t)
 __device__ __forceinline__ float gelu_tanh(float v) {
     return v * sigmoidf(1.5957691216057308f * (v + 0.044715f * v * v * v));
@@ -169,12 +181,16 @@ __device__ __forceinline__ void store4(void* out, int64_t idx, f32x4 v, bool f32
 }
 
 // Output position of a wave: lane l holds, of its 16 x 16 block (i, j), row
-// row0 + 16 i + l % 16 and columns col0 + 16 j + 4 (l / 16) .. + 3 (the
-// operands are passed to the MFMA as B, A, so a lane's four values are
-// neighbours along n and are stored together).
+// row(i) + l % 16 and columns col(j) + 4 (l / 16) .. + 3 (the operands are
+// passed to the MFMA as B, A, so a lane's four values are neighbours along n
+// and are stored together). Blocks come in groups of four along m, 128 rows
+// apart, and of two along n (one gate-up pair for GLU), col_step apart.
 struct Pos {
     int64_t out_base;  // WGRAD: first element of the expert's matrix
-    int row0, row_end, col0;
+    int row0, row_end, col0, col_step;
+    __device__ __forceinline__ int row(int i) const { return row0 + 16 * (i & 3) + 128 * (i >> 2); }
+    __device__ __forceinline__ int col(int j) const { return col0 + 16 * (j & 1) + col_step * (j >> 1); }
+    __device__ __forceinline__ int col_pair(int j) const { return col0 + col_step * j; }
 };
 
 template <int EPI, int ACT, int MF, int NF>
@@ -183,14 +199,14 @@ __device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[M
     const int c4 = (lane >> 4) * 4;
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-        const int m = o.row0 + 16 * i + (lane & 15);
+        const int m = o.row(i) + (lane & 15);
         if (m >= o.row_end) continue;
         if (EPI == kEpiOut) {
             const int64_t r = p.scatter ? p.scatter[m] : m;
             const int64_t base = o.out_base + r * N;
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
-                const int n = o.col0 + 16 * j + c4;
+                const int n = o.col(j) + c4;
                 if (n >= N) continue;
                 f32x4 v = acc[i][j];
                 if (p.accumulate)
@@ -202,7 +218,7 @@ __device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[M
             const int64_t base = (int64_t)m * N;
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
-                const int n = o.col0 + 16 * j + c4;
+                const int n = o.col(j) + c4;
                 if (n >= N) continue;
                 f32x4 v = acc[i][j];
                 if (p.bias) v += *reinterpret_cast<const f32x4*>(p.bias + n);
@@ -216,7 +232,7 @@ __device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[M
             const int64_t base = (int64_t)m * N;
 #pragma unroll
             for (int j = 0; j < NF / 2; ++j) {
-                const int n = o.col0 + 16 * j + c4;
+                const int n = o.col_pair(j) + c4;
                 if (n >= N) continue;
                 f32x4 g = acc[i][2 * j], u = acc[i][2 * j + 1];
                 if (p.bias) {
@@ -457,6 +473,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     o.row0 = row0 + wm * (TM / WM);
     o.row_end = row_end;
     o.col0 = col0 + wn * (TNO / WN);
+    o.col_step = EPI == kEpiGlu ? 16 : 32;
     epilogue<EPI>(p, acc, o, lane);
 }
 
