@@ -65,12 +65,26 @@ void run(Args p, int64_t m_tiles_cap, hipStream_t s) {
     hipLaunchKernelGGL((k_gemm16<MODE, EPI, TM, TN, WM, WN>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, p);
 }
 
+// Multiplier and shift of div_by.
+static void set_div(uint32_t d, uint32_t* mul, int32_t* shift) {
+    if (d <= 1) {
+        *mul = 0;
+        *shift = -1;
+        return;
+    }
+    int s = 0;
+    while ((1ull << s) < d) ++s;
+    *mul = (uint32_t)((1ull << (31 + s)) / d + 1);
+    *shift = s - 1;
+}
+
 template <int MODE, int EPI>
 void run_big(Args p, int64_t m_tiles_cap, hipStream_t s) {
     constexpr int TNO = EPI == kEpiGlu ? kBigT / 2 : kBigT;
     p.n_tiles = (p.N + TNO - 1) / TNO;
     const int64_t total = m_tiles_cap * p.n_tiles;
     const int64_t grid = std::min<int64_t>(total, device_cus());
+    set_div((uint32_t)(kGroupM * p.n_tiles), &p.group_mul, &p.group_shift);
     hipLaunchKernelGGL((k_gemm16_big<MODE, EPI>), dim3((unsigned)grid), dim3(64 * kBigWaves), 0, s, p, (int)total);
 }
 
@@ -103,6 +117,8 @@ bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int6
 }
 
 void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
+    set_div(p.a_div, &p.a_mul, &p.a_shift);
+    set_div(p.b_div, &p.b_mul, &p.b_shift);
     const int64_t n_big = (p.N + (epi == kEpiGlu ? 127 : 255)) / (epi == kEpiGlu ? 128 : 256);
     const int cus = device_cus();
     if (mode == kWgrad) {

@@ -50,6 +50,10 @@ struct Args {
     uint16_t* z;              // saved pre-activation
     int64_t a_bytes, b_bytes; // gathered operands: bytes of the whole source (bounds the loads)
     uint32_t a_div, b_div;
+    uint32_t a_mul, b_mul;    // source row of gather entry v < 2^31: div_by(v, mul, shift)
+    int32_t a_shift, b_shift;
+    uint32_t group_mul;       // the same for the 256 x 256 kernel's tile groups
+    int32_t group_shift;
     int32_t lda, ldb;         // row strides in elements
     int32_t E, rows;          // experts; logical token rows
     int32_t M, N, K;          // WGRAD: M x N outputs; FWD, DGRAD: N columns (GLU: N outputs), K
@@ -73,6 +77,17 @@ __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t off, uint32_t lds_add
         "s_mov_b32 m0, %0\n\t"
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %1, %2, 0 offen lds"
+        :
+        : "s"(lds_addr), "v"(off), "s"(rsrc)
+        : "memory");
+}
+
+// The same with 4 bytes per lane.
+__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t off, uint32_t lds_addr) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dword %1, %2, 0 offen lds"
         :
         : "s"(lds_addr), "v"(off), "s"(rsrc)
         : "memory");
@@ -139,19 +154,25 @@ __device__ __forceinline__ bf16x8 frag_r(const uint8_t* st, int r0, int ks, int 
 // ------------------------------------------------------------------ activations
 // In fp32. exp overflow gives inf and a reciprocal of 0, the limits wanted.
 __device__ __forceinline__ float sigmoidf(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
-// erf by Abramowitz and Stegun 7.1.26: for x >= 0, 1 - (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x),
-// within 1.5e-7 of erf. (The library's erff, exact to an ulp, is three times as many instructions, and an epilogue
-// of 128 of them per lane took 20 us of a 256 x 256 tile.)
-__device__ __forceinline__ float erf_as(float v) {
+// erfc(x) for x >= 0 by Abramowitz and Stegun 7.1.28, 1 / (1 + a1 x + .. + a6 x^6)^16, within 3e-7; here of
+// x = |v| / sqrt(2), the powers of which are in the coefficients. (The library's erff, exact to an ulp, is four times
+// as many instructions: 20 us of each 256 x 256 tile.) gelu(v) = max(v, 0) - |v| erfc / 2.
+__device__ __forceinline__ float erfc_sqrt2(float v) {
     const float x = fabsf(v);
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
-    float q = __builtin_fmaf(1.061405429f, t, -1.453152027f);
-    q = __builtin_fmaf(q, t, 1.421413741f);
-    q = __builtin_fmaf(q, t, -0.284496736f);
-    q = __builtin_fmaf(q, t, 0.254829592f);
-    return __builtin_copysignf(__builtin_fmaf(-q * t, __expf(-x * x), 1.0f), v);
+    float q = __builtin_fmaf(0.0000430638f / 8.0f, x, 0.0002765672f * 0.17677669529663688f);
+    q = __builtin_fmaf(q, x, 0.0001520143f / 4.0f);
+    q = __builtin_fmaf(q, x, 0.0092705272f * 0.35355339059327376f);
+    q = __builtin_fmaf(q, x, 0.0422820123f / 2.0f);
+    q = __builtin_fmaf(q, x, 0.0705230784f * 0.70710678118654752f);
+    float r = __builtin_amdgcn_rcpf(__builtin_fmaf(q, x, 1.0f));
+    r *= r;
+    r *= r;
+    r *= r;
+    return r * r;
 }
-__device__ __forceinline__ float gelu_erf(float v) { return 0.5f * v * (1.0f + erf_as(v * 0.70710678118654752f)); }
+__device__ __forceinline__ float gelu_erf(float v) {
+    return __builtin_fmaf(-0.5f * fabsf(v), erfc_sqrt2(v), v > 0.0f ? v : v != v ? v : 0.0f);
+}
 // 0.5 (1 + tanh(t)) = sigmoid(2 t)
 __device__ __forceinline__ float gelu_tanh(float v) {
     return v * sigmoidf(1.5957691216057308f * (v + 0.044715f * v * v * v));
@@ -172,82 +193,127 @@ __device__ __forceinline__ f32x4 load4_bf16(const uint16_t* p) {
     return (f32x4){__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u), __uint_as_float(w[1] << 16),
                    __uint_as_float(w[1] & 0xFFFF0000u)};
 }
-__device__ __forceinline__ void store4_bf16(uint16_t* p, f32x4 v) {
-    *reinterpret_cast<u32x2*>(p) = (u32x2){bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
-}
-__device__ __forceinline__ void store4(void* out, int64_t idx, f32x4 v, bool f32) {
-    if (f32) *reinterpret_cast<f32x4*>(static_cast<float*>(out) + idx) = v;
-    else store4_bf16(static_cast<uint16_t*>(out) + idx, v);
-}
-
 // Output position of a wave: lane l holds, of its 16 x 16 block (i, j), row
 // row(i) + l % 16 and columns col(j) + 4 (l / 16) .. + 3 (the operands are
-// passed to the MFMA as B, A, so a lane's four values are neighbours along n
-// and are stored together). Blocks come in groups of four along m, 128 rows
-// apart, and of two along n (one gate-up pair for GLU), col_step apart.
+// passed to the MFMA as B, A, so a lane's four values are neighbours along n).
+// Blocks come in groups of four along m, 128 rows apart, and in pairs of
+// adjacent ones along n, pair_step apart (GLU: of the outputs, whose gate and
+// up blocks alternate).
 struct Pos {
     int64_t out_base;  // WGRAD: first element of the expert's matrix
-    int row0, row_end, col0, col_step;
+    int row0, row_end, col0, pair_step;
     __device__ __forceinline__ int row(int i) const { return row0 + 16 * (i & 3) + 128 * (i >> 2); }
-    __device__ __forceinline__ int col(int j) const { return col0 + 16 * (j & 1) + col_step * (j >> 1); }
-    __device__ __forceinline__ int col_pair(int j) const { return col0 + col_step * j; }
+    __device__ __forceinline__ int col(int pair) const { return col0 + pair_step * pair; }
 };
+
+// Stores one row's values of an adjacent pair of blocks (columns n .. n + 31 of
+// the wave; v0, v1 this lane's four of each). bf16: lanes of neighbouring
+// 16-lane rows trade halves, so that each holds eight neighbouring columns: one
+// 16-byte store per lane, whole 64-byte pieces per row and instruction.
+// base: the row's first element. Must be called by all lanes of the four
+// 16-lane rows that share an output row.
+__device__ __forceinline__ void store_pair(void* out, int64_t base, int n, int N, f32x4 v0, f32x4 v1, bool f32,
+                                           int lane) {
+    const int g = lane >> 4;
+    if (f32) {
+        float* o = static_cast<float*>(out) + base;
+        if (n + 4 * g < N) *reinterpret_cast<f32x4*>(o + n + 4 * g) = v0;
+        if (n + 16 + 4 * g < N) *reinterpret_cast<f32x4*>(o + n + 16 + 4 * g) = v1;
+        return;
+    }
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const auto lo = __builtin_amdgcn_permlane16_swap(bf16x2_rne(v0[0], v0[1]), bf16x2_rne(v1[0], v1[1]), false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(bf16x2_rne(v0[2], v0[3]), bf16x2_rne(v1[2], v1[3]), false, false);
+    const int c = n + ((g & 1) ? 16 + 4 * (g - 1) : 4 * g);
+    if (c < N)
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + base + c) = (u32x4){lo[0], hi[0], lo[1], hi[1]};
+}
 
 template <int EPI, int ACT, int MF, int NF>
 __device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[MF][NF], const Pos& o, int lane) {
     const int N = p.N;
     const int c4 = (lane >> 4) * 4;
+    constexpr int NP = EPI == kEpiGlu ? NF / 4 : NF / 2;  // pairs of output blocks
+    constexpr int CH = MF < 4 ? MF : 4;                   // rows whose residual is loaded together
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-        const int m = o.row(i) + (lane & 15);
-        if (m >= o.row_end) continue;
-        if (EPI == kEpiOut) {
-            const int64_t r = p.scatter ? p.scatter[m] : m;
+    for (int i0 = 0; i0 < MF; i0 += CH) {
+        u32x2 res[CH][NP][2];
+        if (EPI != kEpiOut && p.residual) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int m = min(o.row(i0 + i) + (lane & 15), o.row_end - 1);
+#pragma unroll
+                for (int q = 0; q < NP; ++q)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        res[i][q][t] = *reinterpret_cast<const u32x2*>(p.residual + (int64_t)m * N +
+                                                                       min(o.col(q) + 16 * t + c4, N - 4));
+            }
+        }
+#pragma unroll
+        for (int ii = 0; ii < CH; ++ii) {
+            const int i = i0 + ii;
+            const int m = o.row(i) + (lane & 15);
+            if (m >= o.row_end) continue;
+            const int64_t r = EPI == kEpiOut && p.scatter ? p.scatter[m] : m;
             const int64_t base = o.out_base + r * N;
 #pragma unroll
-            for (int j = 0; j < NF; ++j) {
-                const int n = o.col(j) + c4;
-                if (n >= N) continue;
-                f32x4 v = acc[i][j];
-                if (p.accumulate)
-                    v += p.out_f32 ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.out) + base + n)
-                                   : load4_bf16(static_cast<const uint16_t*>(p.out) + base + n);
-                store4(p.out, base + n, v, p.out_f32);
-            }
-        } else if (EPI == kEpiAct) {
-            const int64_t base = (int64_t)m * N;
+            for (int q = 0; q < NP; ++q) {
+                const int n = o.col(q);
+                f32x4 v[2];
 #pragma unroll
-            for (int j = 0; j < NF; ++j) {
-                const int n = o.col(j) + c4;
-                if (n >= N) continue;
-                f32x4 v = acc[i][j];
-                if (p.bias) v += *reinterpret_cast<const f32x4*>(p.bias + n);
-                if (p.z) store4_bf16(p.z + base + n, v);
+                for (int t = 0; t < 2; ++t) {
+                    const int nn = n + 16 * t + c4;
+                    if (EPI == kEpiOut) {
+                        v[t] = acc[i][2 * q + t];
+                        if (p.accumulate && nn < N)
+                            v[t] += p.out_f32
+                                        ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.out) + base + nn)
+                                        : load4_bf16(static_cast<const uint16_t*>(p.out) + base + nn);
+                    } else if (EPI == kEpiAct) {
+                        v[t] = acc[i][2 * q + t];
+                        if (p.bias) v[t] += *reinterpret_cast<const f32x4*>(p.bias + min(nn, N - 4));
+                    } else {
+                        f32x4 g = acc[i][4 * q + 2 * t], u = acc[i][4 * q + 2 * t + 1];
+                        if (p.bias) {
+                            g += *reinterpret_cast<const f32x4*>(p.bias + min(nn, N - 4));
+                            u += *reinterpret_cast<const f32x4*>(p.bias + N + min(nn, N - 4));
+                        }
 #pragma unroll
-                for (int t = 0; t < 4; ++t) v[t] = act_fwd<ACT>(v[t]);
-                if (p.residual) v += load4_bf16(p.residual + base + n);
-                store4(p.out, base + n, v, p.out_f32);
-            }
-        } else {
-            const int64_t base = (int64_t)m * N;
-#pragma unroll
-            for (int j = 0; j < NF / 2; ++j) {
-                const int n = o.col_pair(j) + c4;
-                if (n >= N) continue;
-                f32x4 g = acc[i][2 * j], u = acc[i][2 * j + 1];
-                if (p.bias) {
-                    g += *reinterpret_cast<const f32x4*>(p.bias + n);
-                    u += *reinterpret_cast<const f32x4*>(p.bias + N + n);
+                        for (int e = 0; e < 4; ++e) v[t][e] = g[e] * sigmoidf(g[e]) * u[e];
+                    }
                 }
-                if (p.z) {
-                    store4_bf16(p.z + 2 * base + n, g);
-                    store4_bf16(p.z + 2 * base + N + n, u);
-                }
-                f32x4 v;
+                if (EPI == kEpiAct) {
+                    if (p.z) store_pair(p.z, base, n, N, v[0], v[1], false, lane);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) v[t] = g[t] * sigmoidf(g[t]) * u[t];
-                if (p.residual) v += load4_bf16(p.residual + base + n);
-                store4(p.out, base + n, v, p.out_f32);
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[t][e] = act_fwd<ACT>(v[t][e]);
+                }
+                if (EPI == kEpiGlu && p.z) {
+                    f32x4 g[2], u[2];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        g[t] = acc[i][4 * q + 2 * t];
+                        u[t] = acc[i][4 * q + 2 * t + 1];
+                        if (p.bias) {
+                            const int nn = min(n + 16 * t + c4, N - 4);
+                            g[t] += *reinterpret_cast<const f32x4*>(p.bias + nn);
+                            u[t] += *reinterpret_cast<const f32x4*>(p.bias + N + nn);
+                        }
+                    }
+                    store_pair(p.z, 2 * base, n, N, g[0], g[1], false, lane);
+                    store_pair(p.z, 2 * base + N, n, N, u[0], u[1], false, lane);
+                }
+                if (EPI != kEpiOut && p.residual) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const u32x2 w = res[ii][q][t];
+                        v[t] += (f32x4){__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
+                                        __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u)};
+                    }
+                }
+                store_pair(p.out, base, n, N, v[0], v[1], p.out_f32, lane);
             }
         }
     }
@@ -276,9 +342,10 @@ __device__ __forceinline__ T sload(const T* base, int64_t i) {
     return ((ct*)base)[i];
 }
 
-// Offset of a source row, or kNowhere.
-__device__ __forceinline__ uint32_t row_off(bool ok, uint32_t row, uint32_t stride_bytes) {
-    return ok ? row * stride_bytes : kNowhere;
+// v / d for 0 <= v < 2^31: with 2^(s-1) < d <= 2^s and mul = floor(2^(31+s) / d) + 1 < 2^32 (host), exactly
+// (v * mul) >> (31 + s); d = 1 is shift -1. (A hardware division is some twenty instructions.)
+__device__ __forceinline__ uint32_t div_by(uint32_t v, uint32_t mul, int shift) {
+    return shift < 0 ? v : __umulhi(v, mul) >> shift;
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -344,7 +411,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
             const int rl = (i * NW + wave) * 8 + (lane >> 3);
             const bool ok = row0 + rl < row_end;
             uint32_t src = rl;
-            if (gat) src = (uint32_t)p.a_gather[ok ? row0 + rl : row0] / p.a_div;
+            if (gat) src = div_by((uint32_t)p.a_gather[ok ? row0 + rl : row0], p.a_mul, p.a_shift);
             ao[i] = ok ? src * lda2 + kc * 2 : kNowhere;
         }
     } else {
@@ -410,7 +477,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
             for (int i = 0; i < CA; ++i) {
                 const bool ok = k + (int)ak[i] < klen && ao[i] != kNowhere;
                 uint32_t row = ak[i];
-                if (gat) row = (uint32_t)p.a_gather[ok ? k0 + k + (int)ak[i] : k0] / p.a_div;
+                if (gat) row = div_by((uint32_t)p.a_gather[ok ? k0 + k + (int)ak[i] : k0], p.a_mul, p.a_shift);
                 dma16(ra, ok ? row * lda2 + ao[i] : kNowhere, la + (i * NW + wave) * 1024);
             }
         }
@@ -427,7 +494,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
             for (int i = 0; i < CB; ++i) {
                 const bool ok = k + (int)bk[i] < klen && bo[i] != kNowhere;
                 uint32_t row = bk[i];
-                if (gat) row = (uint32_t)p.b_gather[ok ? k0 + k + (int)bk[i] : k0] / p.b_div;
+                if (gat) row = div_by((uint32_t)p.b_gather[ok ? k0 + k + (int)bk[i] : k0], p.b_mul, p.b_shift);
                 dma16(rb, ok ? row * ldb2 + bo[i] : kNowhere, lb + (i * NW + wave) * 1024);
             }
         }
@@ -473,7 +540,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     o.row0 = row0 + wm * (TM / WM);
     o.row_end = row_end;
     o.col0 = col0 + wn * (TNO / WN);
-    o.col_step = EPI == kEpiGlu ? 16 : 32;
+    o.pair_step = 32;
     epilogue<EPI>(p, acc, o, lane);
 }
 

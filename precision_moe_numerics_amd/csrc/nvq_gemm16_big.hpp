@@ -12,7 +12,7 @@ constexpr int kBigT = 256;                 // output tile: 256 x 256
 constexpr int kBigK = 64;                  // K of a stage: whole 128-byte lines of K-contiguous rows
 constexpr int kBigWaves = 8;               // 2 (m) x 4 (n)
 constexpr int kHalf = 128 * kBigK * 2;     // half an operand's stage (128 rows or columns): 16 KiB
-constexpr int kBigStage = 4 * kHalf;       // A0, A1, B0, B1
+constexpr int kSlots = 8;                  // halves in LDS
 constexpr int kGroupM = 4;                 // m-tiles that run side by side
 
 // A tile of the stream (wave-uniform).
@@ -20,46 +20,82 @@ struct BigTile {
     int e, row0, row_end, col0, k0, klen;
 };
 
-// Tile t. Tiles go in groups of kGroupM m-tiles, n outside m within a group:
-// the 32 workgroups of an XCD then hold 4 m-tiles x 8 n-tiles at a time, 12
-// operand panels instead of 33 for the same 32 tiles along a row.
+// Walks a workgroup's tiles v, v + G, ... and holds the next one's table entries
+// as they come from scalar loads issued a tile earlier: a tile of a weight
+// gradient lasts a few microseconds, and a chain of dependent loads and integer
+// divisions at its head would cost as much again.
+//
+// Tiles go in groups of kGroupM m-tiles, n outside m within a group: the 32
+// workgroups of an XCD then hold 4 m-tiles x 8 n-tiles at a time, 12 operand
+// panels instead of 33 for the same 32 tiles along a row.
 template <int MODE, int EPI>
-__device__ __forceinline__ BigTile big_tile(const Args& p, int t, int m_count) {
-    constexpr int TNO = EPI == kEpiGlu ? kBigT / 2 : kBigT;
-    BigTile T;
-    T.e = 0;
-    if (MODE == kWgrad) {
-        const int per = p.m_tiles * p.n_tiles;
-        T.e = t / per;
-        t -= T.e * per;
-        m_count = p.m_tiles;
+struct BigWalk {
+    int t;            // the tile
+    int e, r;         // WGRAD: its expert and number within the expert
+    int mt, nt;
+    int32_t q0, q1, q2;  // table entries
+
+    __device__ __forceinline__ void start(const Args& p, int t0, int total, int m_count) {
+        t = t0;
+        e = MODE == kWgrad ? t / (p.m_tiles * p.n_tiles) : 0;
+        r = t - e * (p.m_tiles * p.n_tiles);
+        load(p, total, m_count);
     }
-    const int g = t / (kGroupM * p.n_tiles);
-    const int rem = t - g * (kGroupM * p.n_tiles);
-    const int gm = min(kGroupM, m_count - g * kGroupM);
-    const int nt = rem / gm;
-    const int mt = g * kGroupM + (rem - nt * gm);
-    T.col0 = nt * TNO;
-    T.k0 = 0;
-    T.klen = p.K;
-    if (MODE == kWgrad) {
-        T.row0 = mt * kBigT;
-        T.row_end = p.M;
-        T.klen = p.rows;
-        if (p.seg) {
-            T.k0 = min(max(sload(p.seg, T.e), 0), p.rows);
-            T.klen = max(min(max(sload(p.seg, T.e + 1), 0), p.rows) - T.k0, 0);
+    __device__ __forceinline__ void next(const Args& p, int G, int total, int m_count) {
+        t += G;
+        if (MODE == kWgrad) {
+            r += G;
+            const int per = p.m_tiles * p.n_tiles;
+            while (r >= per) {
+                r -= per;
+                ++e;
+            }
         }
-    } else if (p.tiles) {
-        T.e = sload(&p.tiles[mt].e, 0);
-        T.row0 = sload(&p.tiles[mt].row0, 0);
-        T.row_end = sload(&p.tiles[mt].row_end, 0);
-    } else {
-        T.row0 = mt * kBigT;
-        T.row_end = p.rows;
+        load(p, total, m_count);
     }
-    return T;
-}
+    __device__ __forceinline__ void load(const Args& p, int total, int m_count) {
+        if (t >= total) return;
+        const int u = MODE == kWgrad ? r : t;
+        const int g = (int)div_by((uint32_t)u, p.group_mul, p.group_shift);  // kGroupM * n_tiles per group
+        const int rem = u - g * (kGroupM * p.n_tiles);
+        const int gm = min(kGroupM, (MODE == kWgrad ? p.m_tiles : m_count) - g * kGroupM);
+        nt = gm == 4 ? rem >> 2 : gm == 2 ? rem >> 1 : gm == 1 ? rem : (int)__umulhi((uint32_t)rem, 0x55555556u);
+        mt = g * kGroupM + (rem - nt * gm);
+        if (MODE == kWgrad) {
+            if (p.seg) {
+                q0 = sload(p.seg, e);
+                q1 = sload(p.seg, e + 1);
+            }
+        } else if (p.tiles) {
+            q0 = sload(&p.tiles[mt].e, 0);
+            q1 = sload(&p.tiles[mt].row0, 0);
+            q2 = sload(&p.tiles[mt].row_end, 0);
+        }
+    }
+    __device__ __forceinline__ BigTile get(const Args& p) const {
+        BigTile T;
+        T.e = e;
+        T.col0 = nt * (EPI == kEpiGlu ? kBigT / 2 : kBigT);
+        T.k0 = 0;
+        T.klen = p.K;
+        T.row0 = mt * kBigT;
+        if (MODE == kWgrad) {
+            T.row_end = p.M;
+            T.klen = p.rows;
+            if (p.seg) {
+                T.k0 = min(max(q0, 0), p.rows);
+                T.klen = max(min(max(q1, 0), p.rows) - T.k0, 0);
+            }
+        } else if (p.tiles) {
+            T.e = q0;
+            T.row0 = q1;
+            T.row_end = q2;
+        } else {
+            T.row_end = p.rows;
+        }
+        return T;
+    }
+};
 
 // The loader: the stage being fetched, as descriptor bases and byte counts at
 // its K offset and this lane's offsets within them. A stage is fetched in
@@ -78,6 +114,7 @@ struct BigLoad {
     uint32_t alim, blim;  // K-contiguous operands: descriptor bytes
     uint32_t ao[A_R ? 1 : 4], bo;
     int klen, k0, k;      // K extent and start of the tile, K offset of the stage
+    uint32_t ra[2], rb[2]; // WGRAD with gathers: byte offsets of this lane's source rows of the stage (A, B)
 
     // K-contiguous: a piece is 16 bytes of row 128 half + 64 i + 8 wave + lane / 8; rows of 128 bytes
     // in LDS, chunk c of row r at slot c ^ (r & 7)
@@ -89,7 +126,16 @@ struct BigLoad {
         return (int)((lane & 15) ^ rkey(row_r(wave, lane))) * 8;
     }
 
-    __device__ __forceinline__ void set(const Args& p, const BigTile& T, int wave, int lane) {
+    // Gather entries of a tile's rows (this wave's 32: row 64 i + 8 wave + j at 8 i + j) into LDS at dst, a tile before
+    // set() reads them there: a load into registers would wait for every stage in flight.
+    static __device__ __forceinline__ void fetch_rows(const Args& p, const BigTile& T, uint32_t dst, int wave,
+                                                      int lane) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // set()'s reads of the tile before
+        const int r = T.row0 + 64 * (lane >> 3) + 8 * wave + (lane & 7);
+        dma4(rsrc(reinterpret_cast<const uint16_t*>(p.a_gather + T.row0), (uint32_t)min(T.row_end - T.row0, kBigT) * 4u),
+             lane < 32 && r < T.row_end ? (uint32_t)(r - T.row0) * 4u : kNowhere, dst);
+    }
+    __device__ __forceinline__ void set(const Args& p, const BigTile& T, const int32_t* idx, int wave, int lane) {
         const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
         klen = T.klen;
         k0 = T.k0;
@@ -102,7 +148,7 @@ struct BigLoad {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t src = r + 64 * i;
-                if (ga) src = (uint32_t)p.a_gather[min(T.row0 + r + 64 * i, T.row_end - 1)] / p.a_div;
+                if (ga) src = div_by((uint32_t)idx[8 * i + (lane >> 3)], p.a_mul, p.a_shift);
                 ao[i] = src * lda2 + chunk_k(lane) * 16;
             }
         } else {
@@ -113,8 +159,9 @@ struct BigLoad {
             bbase = p.b + ((int64_t)T.e * (EPI == kEpiGlu ? 2 : 1) * p.N + T.col0) * p.ldb;
             blim = (uint32_t)(EPI == kEpiGlu ? 2 * p.N - T.col0 : min(p.N - T.col0, kBigT)) * ldb2;
             const int r = row_k(wave, lane);
-            // GLU: blocks of 16 rows: gate, up, gate, up, ...
-            const int src = EPI == kEpiGlu ? ((r >> 4) & 1) * p.N + (r >> 5) * 16 + (r & 15) : r;
+            // GLU: blocks of 16 rows: gate, up, gate, up, ..., each wave's pairs of both halves adjacent:
+            // rows 32 w .. 32 w + 31 of half h are gate and up of outputs 32 w + 16 h .. + 15
+            const int src = EPI == kEpiGlu ? ((r >> 4) & 1) * p.N + (r >> 5) * 32 + (r & 15) : r;
             bo = (uint32_t)src * ldb2 + chunk_k(lane) * 16;
         } else {
             const bool gb = MODE == kWgrad && p.b_gather != nullptr;
@@ -151,39 +198,60 @@ struct BigLoad {
                                             int lane) const {
         dma16(rsrc(base, klen > 0 ? lim : 0), k + chunk_k(lane) * 8 < klen ? o : kNowhere, dst);
     }
-    // K-strided piece i of half h
-    __device__ __forceinline__ void piece_r(const uint16_t* base, int64_t bytes, uint32_t o, const int32_t* gather,
-                                            uint32_t div, int ld, int h, int i, uint32_t dst, int wave,
-                                            int lane) const {
-        const uint32_t ld2 = (uint32_t)ld * 2u;
-        if (!gather) {
-            dma16(rsrc(base, (uint32_t)min(max(klen - k, 0), kBigK) * ld2), o + i * 32 * ld2 + h * 256, dst);
-            return;
-        }
-        uint32_t src = 0;
-        const int kl = k + 32 * i + 4 * wave;  // of lanes 0 .. 15; then the next rows
+    // Gather entries of the wave's k rows (32 i + 4 wave + q) of the stage at K offset kk, as scalar loads, issued
+    // well before rows() waits for them and picks this lane's.
+    typedef int32_t Entries __attribute__((ext_vector_type(8)));
+    __device__ __forceinline__ Entries entries(const int32_t* gather, int kk, int wave) const {
+        Entries r = {0, 0, 0, 0, 0, 0, 0, 0};
         if (klen > 0) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t s = (uint32_t)sload(gather, k0 + min(kl + q, klen - 1)) / div;
-                src = (lane >> 4) == q ? s : src;
-            }
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    r[4 * i + q] = sload(gather, k0 + min(kk + 32 * i + 4 * wave + q, klen - 1));
         }
-        dma16(rsrc(base, (uint32_t)bytes), kl + (lane >> 4) < klen ? src * ld2 + o + h * 256 : kNowhere, dst);
+        return r;
     }
-    // half (A0, A1, B0, B1), piece i of the stage, into the LDS stage at dst
+    static __device__ __forceinline__ void rows(uint32_t (&o)[2], Entries r, uint32_t mul, int shift, int ld,
+                                                int lane) {
+        const int q = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t v = (uint32_t)r[4 * i];
+#pragma unroll
+            for (int t = 1; t < 4; ++t) v = q == t ? (uint32_t)r[4 * i + t] : v;
+            o[i] = div_by(v, mul, shift) * ((uint32_t)ld * 2u);
+        }
+    }
+    // K-strided piece i of half h
+    __device__ __forceinline__ void piece_r(const uint16_t* base, uint32_t o, int ld, int h, int i, uint32_t dst) const {
+        const uint32_t ld2 = (uint32_t)ld * 2u;
+        dma16(rsrc(base, (uint32_t)min(max(klen - k, 0), kBigK) * ld2), o + i * 32 * ld2 + h * 256, dst);
+    }
+    __device__ __forceinline__ void piece_g(const uint16_t* base, int64_t bytes, uint32_t o, const uint32_t (&row)[2],
+                                            int h, int i, uint32_t dst, int wave, int lane) const {
+        const bool ok = k + 32 * i + 4 * wave + (lane >> 4) < klen;
+        dma16(rsrc(base, (uint32_t)bytes), ok ? row[i] + o + h * 256 : kNowhere, dst);
+    }
+    // half (A0, A1, B0, B1), piece i of the stage, into the LDS slot at dst
     __device__ __forceinline__ void piece(const Args& p, int half, int i, uint32_t dst, int wave, int lane) const {
         const int h = half & 1;
-        dst += half * kHalf + (i * kBigWaves + wave) * 1024;
+        dst += (i * kBigWaves + wave) * 1024;
         if (half < 2) {
-            if constexpr (A_R) piece_r(abase, p.a_bytes, ao[0], p.a_gather, p.a_div, p.lda, h, i, dst, wave, lane);
-            else piece_k(abase, alim, ao[2 * h + i], dst, lane);
+            if constexpr (A_R) {
+                if (p.a_gather)
+                    piece_g(abase, p.a_bytes, ao[0], ra, h, i, dst, wave, lane);
+                else piece_r(abase, ao[0], p.lda, h, i, dst);
+            } else {
+                piece_k(abase, alim, ao[2 * h + i], dst, lane);
+            }
         } else {
-            constexpr int step = EPI == kEpiGlu ? 32 : 64;  // rows of w between pieces
-            if constexpr (B_R)
-                piece_r(bbase, p.b_bytes, bo, MODE == kWgrad ? p.b_gather : nullptr, p.b_div, p.ldb, h, i, dst, wave,
-                        lane);
-            else piece_k(bbase, blim, bo + (2 * h + i) * step * ((uint32_t)p.ldb * 2u), dst, lane);
+            const int rows = EPI == kEpiGlu ? 64 * i + 16 * h : 64 * i + 128 * h;  // of w, from piece 0 of half 0
+            if constexpr (B_R) {
+                if (MODE == kWgrad && p.b_gather)
+                    piece_g(bbase, p.b_bytes, bo, rb, h, i, dst, wave, lane);
+                else piece_r(bbase, bo, p.ldb, h, i, dst);
+            } else piece_k(bbase, blim, bo + rows * ((uint32_t)p.ldb * 2u), dst, lane);
         }
     }
 };
@@ -240,27 +308,31 @@ __device__ __forceinline__ void big_mul(f32x4 (*acc)[4], int i0, int j0, const F
 }
 
 // Persistent kernel over the tiles v, v + G, ...: the K stages of a workgroup's
-// tiles form one stream through two LDS stages of four halves, so a tile's
-// first stages arrive while the tile before it is finished and stored.
+// tiles form one stream through LDS, so a tile's first stages arrive while the
+// tile before it is finished and stored.
 //
 // A K step of stage q has four quarters of 16 products a wave: A0 B0, A0 B1,
 // A1 B1, A1 B0, each in two halves of K. Fragments are read while earlier
 // products run, into registers whose last use has been issued: A's K halves
-// alternate, B0 and B1 swap places from step to step. As soon as a half has
-// been read by every wave (barrier) the same half two stages on is fetched into
-// its place: B0 in quarter 0, A0 in 1, B1 in 2, A1 in 3. It is first read six or
-// seven quarters later, so at the barriers before quarters 3, 0 and 1, the ones
-// whose reads need a new half, everything but the newest five halves (10 loads
-// of the wave) has landed; five quarters are 2560 matrix cycles of the SIMD.
+// alternate, B0 and B1 swap places from step to step. The operand halves B0,
+// A0, B1, A1 of stage 0, 1, .. are one sequence that goes round eight LDS slots:
+// half n is read in quarters n - 2 to n - 1 (of quarters counted through), so at
+// the barrier that opens quarter n its slot is free and half n + 8 is fetched
+// into it. At the barriers before quarters 3, 0 and 1, whose reads need a new
+// half, everything but the newest five halves (10 loads of the wave) has
+// landed; a half has six quarters, 3072 matrix cycles of the SIMD, to arrive.
+// (Ten slots, the whole LDS and eight quarters, measured no faster.)
 template <int MODE, int EPI>
 __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p, int total_cap) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kBigStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kHalf];
+    __shared__ int32_t rows_lds[kBigWaves][64];
+    __shared__ __attribute__((aligned(16))) int32_t ring[kBigWaves][4][4];
     using Load = BigLoad<MODE, EPI>;
-    constexpr int kNew = 10;
+    constexpr int kNew = 2 * (kSlots - 3);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63;
     const int wm = wave >> 2, wn = wave & 3;
-    const uint32_t lds0 = lds_off(&lds[0][0]);
+    const uint32_t lds0 = lds_off(&lds[0]);
     const int G = gridDim.x;
     const int v = (G % 8 == 0) ? (int)((blockIdx.x % 8) * (G / 8) + blockIdx.x / 8) : (int)blockIdx.x;
     const int m_count = MODE == kWgrad ? p.m_tiles : p.tiles ? sload(p.tile_count, 0) : (p.rows + kBigT - 1) / kBigT;
@@ -268,33 +340,86 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p, int to
     if (v >= total) return;
 
     Load ld;
-    int lt = v;  // the loader's tile
-    ld.set(p, big_tile<MODE, EPI>(p, lt, m_count), wave, lane);
-    // past the last tile the same number of loads goes out, none with anything to read
-    auto settle = [&]() {
-        while (ld.k >= ld.klen && lt < total) {
-            lt += G;
-            if (lt < total) ld.set(p, big_tile<MODE, EPI>(p, lt, m_count), wave, lane);
-            else ld.klen = 0;
+    BigWalk<MODE, EPI> lw;  // the tile after the one fetched
+    lw.start(p, v, total, m_count);
+    // The tiles between the loader and the products. A weight gradient's loader
+    // may pass any number of empty segments at once and the products follow
+    // with a walk of their own; otherwise every tile has a stage, the loader is
+    // at most three tiles ahead, and it leaves them in a ring.
+    BigWalk<MODE, EPI> cw;
+    if (MODE == kWgrad) cw = lw;
+    int pushed = 0, popped = 0;
+    const bool gat_r = MODE != kWgrad && p.a_gather;
+    const int32_t* idx = &rows_lds[wave][0];
+    const uint32_t idx0 = lds_off(idx);
+    if (gat_r) {
+        Load::fetch_rows(p, lw.get(p), idx0, wave, lane);
+        wait_vm<0>();
+    }
+    // moves the loader to its next tile; past the last one the same number of
+    // loads goes out, none with anything to read
+    auto next_tile = [&]() {
+        if (lw.t >= total) {
+            ld.klen = 0;
+            return;
         }
+        const BigTile T = lw.get(p);
+        ld.set(p, T, idx, wave, lane);
+        if (MODE != kWgrad) {
+            int32_t* q = ring[wave][pushed++ & 3];
+            if (lane == 0) {
+                q[0] = T.row0;
+                q[1] = T.row_end;
+                q[2] = T.col0;
+            }
+        }
+        lw.next(p, G, total, m_count);
+        if (gat_r && lw.t < total) Load::fetch_rows(p, lw.get(p), idx0, wave, lane);
     };
-    settle();
-#pragma unroll 1
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) ld.piece(p, h, i, lds0 + s * kBigStage, wave, lane);
-        ld.advance(p);
+    bool done = false;
+    auto settle = [&]() {
+        bool moved = false;
+        while (ld.k >= ld.klen && !done) {
+            done = lw.t >= total;
+            next_tile();
+            moved = true;
+        }
+        return moved;
+    };
+    const bool gat_a = MODE == kWgrad && p.a_gather, gat_b = MODE == kWgrad && p.b_gather;
+    auto rows_a = [&](typename Load::Entries e) { Load::rows(ld.ra, e, p.a_mul, p.a_shift, p.lda, lane); };
+    auto rows_b = [&](typename Load::Entries e) { Load::rows(ld.rb, e, p.b_mul, p.b_shift, p.ldb, lane); };
+    next_tile();
+    auto start_stage = [&]() {
         settle();
+        if (gat_r) wait_vm<0>();  // (before the loop several tiles may start with no wait between them)
+        if (gat_a) rows_a(ld.entries(p.a_gather, ld.k, wave));
+        if (gat_b) rows_b(ld.entries(p.b_gather, ld.k, wave));
+    };
+    start_stage();
+    // the halves of a stage in the order they are used
+    auto fetch = [&](int half, int slot, int i) { ld.piece(p, half, i, lds0 + slot * kHalf, wave, lane); };
+    constexpr int kOrder[4] = {kB0, kA0, kB1, kA1};
+#pragma unroll
+    for (int n = 0; n < kSlots; ++n) {
+        fetch(kOrder[n & 3], n, 0);
+        fetch(kOrder[n & 3], n, 1);
+        if ((n & 3) == 3) {
+            ld.advance(p);
+            start_stage();
+        }
     }
     wait_vm<0>();
     stage_barrier();
-    int slot = 0;  // LDS stage of the step
+    int base = 0;  // slot of the step's B0
+    auto slot_of = [&](int j) {
+        const int x = base + j;
+        return x >= kSlots ? x - kSlots : x;
+    };
     FragA a;
     FragB bx, by;
-    big_read_a<Load::A_R>(a, lds[0] + kA0 * kHalf, 0, wave, lane);
-    big_read_b<Load::B_R>(bx, lds[0] + kB0 * kHalf, wave, lane);
+    big_read_a<Load::A_R>(a, lds + kHalf, 0, wave, lane);
+    big_read_b<Load::B_R>(bx, lds, wave, lane);
 
     // One tile of a wave with NA active A halves (0, 1 or 2): separate loops
     // rather than a branch inside one, so that the accumulators never cross a
@@ -312,44 +437,54 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p, int to
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
         auto step = [&](int s, FragB& b0, FragB& b1) {
-            const uint8_t* cur = lds[slot];
-            const uint8_t* nxt = lds[slot ^ 1];
-            const uint32_t dst = lds0 + slot * kBigStage;
+            const uint8_t* A0 = lds + slot_of(1) * kHalf;
+            const uint8_t* B1 = lds + slot_of(2) * kHalf;
+            const uint8_t* A1 = lds + slot_of(3) * kHalf;
+            const uint8_t* nB0 = lds + slot_of(4) * kHalf;
+            const uint8_t* nA0 = lds + slot_of(5) * kHalf;
             // quarter 0
             if (s > 1) wait_vm<kNew>();
             stage_barrier();
-            ld.piece(p, kB0, 0, dst, wave, lane);
-            if (NA > 0) big_read_a<Load::A_R>(a, cur + kA0 * kHalf, 1, wave, lane);
+            fetch(kB0, base, 0);
+            if (NA > 0) big_read_a<Load::A_R>(a, A0, 1, wave, lane);
             big_mul<(NA > 0), RA>(acc, 0, 0, a, b0, 0);
-            ld.piece(p, kB0, 1, dst, wave, lane);
-            if (NA > 0) big_read_b<Load::B_R>(b1, cur + kB1 * kHalf, wave, lane);
+            fetch(kB0, base, 1);
+            if (NA > 0) big_read_b<Load::B_R>(b1, B1, wave, lane);
             big_mul<(NA > 0), RB>(acc, 0, 0, a, b0, 1);
             // quarter 1
             if (s > 1) wait_vm<kNew>();
             stage_barrier();
-            ld.piece(p, kA0, 0, dst, wave, lane);
+            fetch(kA0, slot_of(1), 0);
             big_mul<(NA > 0), 0>(acc, 0, 2, a, b1, 0);
-            ld.piece(p, kA0, 1, dst, wave, lane);
-            if (NA > 1) big_read_a<Load::A_R>(a, cur + kA1 * kHalf, 0, wave, lane);
+            fetch(kA0, slot_of(1), 1);
+            if (NA > 1) big_read_a<Load::A_R>(a, A1, 0, wave, lane);
             big_mul<(NA > 0), (NA > 1 ? RA : 0)>(acc, 0, 2, a, b1, 1);
-            // quarter 2 (nothing new is needed and B1 was read before the last barrier)
-            ld.piece(p, kB1, 0, dst, wave, lane);
-            if (NA > 1) big_read_a<Load::A_R>(a, cur + kA1 * kHalf, 1, wave, lane);
+            // quarter 2 (nothing new is needed, and B1 was read before the last barrier)
+            typename Load::Entries ea = {0, 0, 0, 0, 0, 0, 0, 0}, eb = ea;
+            if (gat_a) ea = ld.entries(p.a_gather, ld.k + kBigK, wave);  // for the next stage
+            fetch(kB1, slot_of(2), 0);
+            if (NA > 1) big_read_a<Load::A_R>(a, A1, 1, wave, lane);
             big_mul<(NA > 1), RA>(acc, 4, 2, a, b1, 0);
-            ld.piece(p, kB1, 1, dst, wave, lane);
+            fetch(kB1, slot_of(2), 1);
             big_mul<(NA > 1), 0>(acc, 4, 2, a, b1, 1);
             // quarter 3
             if (s > 0) wait_vm<kNew>();
             stage_barrier();
-            ld.piece(p, kA1, 0, dst, wave, lane);
-            big_read_b<Load::B_R>(b1, nxt + kB0 * kHalf, wave, lane);
+            if (gat_b) eb = ld.entries(p.b_gather, ld.k + kBigK, wave);
+            fetch(kA1, slot_of(3), 0);
+            big_read_b<Load::B_R>(b1, nB0, wave, lane);
             big_mul<(NA > 1), RB>(acc, 4, 0, a, b0, 0);
-            ld.piece(p, kA1, 1, dst, wave, lane);
-            big_read_a<Load::A_R>(a, nxt + kA0 * kHalf, 0, wave, lane);
+            fetch(kA1, slot_of(3), 1);
+            big_read_a<Load::A_R>(a, nA0, 0, wave, lane);
             big_mul<(NA > 1), RA>(acc, 4, 0, a, b0, 1);
             ld.advance(p);
-            settle();
-            slot ^= 1;
+            if (settle()) {
+                if (gat_a) ea = ld.entries(p.a_gather, ld.k, wave);
+                if (gat_b) eb = ld.entries(p.b_gather, ld.k, wave);
+            }
+            if (gat_a) rows_a(ea);
+            if (gat_b) rows_b(eb);
+            base = slot_of(4);
         };
 #pragma unroll 1
         for (int s = 0; s < nk; s += 2) {
@@ -363,13 +498,24 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p, int to
             o.out_base = MODE == kWgrad ? (int64_t)T.e * p.M * p.N : 0;
             o.row0 = T.row0 + wm * 64;
             o.row_end = T.row_end;
-            o.col0 = T.col0 + wn * (EPI == kEpiGlu ? 16 : 32);
-            o.col_step = EPI == kEpiGlu ? 64 : 128;
+            o.col0 = T.col0 + wn * 32;
+            o.pair_step = 128;
             epilogue<EPI>(p, acc, o, lane);
         }
     };
     for (int t = v; t < total; t += G) {
-        const BigTile T = big_tile<MODE, EPI>(p, t, m_count);
+        BigTile T;
+        if (MODE == kWgrad) {
+            T = cw.get(p);
+            cw.next(p, G, total, m_count);
+        } else {
+            const int32_t* q = ring[wave][popped++ & 3];
+            T.row0 = __builtin_amdgcn_readfirstlane(q[0]);
+            T.row_end = __builtin_amdgcn_readfirstlane(q[1]);
+            T.col0 = __builtin_amdgcn_readfirstlane(q[2]);
+            T.klen = p.K;
+            T.e = T.k0 = 0;
+        }
         const int rows = T.row_end - (T.row0 + wm * 64);
         if (rows > 128) tile(T, std::integral_constant<int, 2>{});
         else if (rows > 0) tile(T, std::integral_constant<int, 1>{});

@@ -14,7 +14,7 @@ template <int ACT>
 __device__ __forceinline__ float act_bwd(float dout, float z) {
     if (ACT == NVQ_ACT_RELU) return z > 0.0f ? dout : 0.0f;
     if (ACT == NVQ_ACT_GELU)
-        return dout * (0.5f * (1.0f + erf_as(z * 0.70710678118654752f)) +
+        return dout * ((z > 0.0f ? __builtin_fmaf(-0.5f, erfc_sqrt2(z), 1.0f) : 0.5f * erfc_sqrt2(z)) +
                        z * (0.39894228040143268f * __expf(-0.5f * z * z)));
     if (ACT == NVQ_ACT_GELU_TANH) {
         const float q = sigmoidf(1.5957691216057308f * (z + 0.044715f * z * z * z));
