@@ -1,5 +1,6 @@
 // nvq_gemm16.hip -- tile tables and launches of the BF16 matrix products.
 #include "nvq_gemm16_big.hpp"
+#include "nvq_gemm16_skinny.hpp"
 
 #include <algorithm>
 
@@ -88,6 +89,20 @@ void run_big(Args p, int64_t m_tiles_cap, hipStream_t s) {
     hipLaunchKernelGGL((k_gemm16_big<MODE, EPI>), dim3((unsigned)grid), dim3(64 * kBigWaves), 0, s, p, (int)total);
 }
 
+template <int EPI, int MB>
+void run_skinny(Args p, hipStream_t s) {
+    p.n_tiles = EPI == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
+    int64_t mt = (p.rows + 16 * MB - 1) / (16 * MB);
+    if (p.seg) mt = std::min<int64_t>(p.rows, mt + p.E);
+    hipLaunchKernelGGL((k_gemm16_skinny<EPI, MB>), dim3((unsigned)(mt * p.n_tiles)), dim3(64 * kSkWaves), 0, s, p);
+}
+template <int EPI>
+void run_skinny_rows(int rows, const Args& p, hipStream_t s) {
+    if (rows <= 16) run_skinny<EPI, 1>(p, s);
+    else if (rows <= 32) run_skinny<EPI, 2>(p, s);
+    else run_skinny<EPI, 4>(p, s);
+}
+
 }  // namespace g16
 
 using namespace g16;
@@ -133,6 +148,14 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
         return;
     }
     if (p.rows == 0) return;
+    // rows that most of the experts stay within
+    const int few = p.seg ? 4 * ((p.rows + p.E - 1) / p.E) : p.rows;
+    if (mode == kFwd && few <= 64) {
+        if (epi == kEpiGlu) run_skinny_rows<kEpiGlu>(few, p, s);
+        else if (epi == kEpiAct) run_skinny_rows<kEpiAct>(few, p, s);
+        else run_skinny_rows<kEpiOut>(few, p, s);
+        return;
+    }
     const bool big = p.rows / p.E >= 128 && (p.rows + 255) / 256 * n_big >= cus;
     const int tm = big ? 256 : 128;
     int64_t mt;
