@@ -470,8 +470,9 @@ int moe_grouped_gemm_nvfp4_bwd(int mode, const uint8_t* a_codes, const uint8_t* 
  * 8 up to 2^22, E <= 4096, R < 2^31 - 256, one expert's weights and the whole
  * of a gathered operand below 4 GiB - 512, output tiles below 2^31. Not
  * checked on the host: offsets (clamped to [0, R] on the device) and gather
- * and scatter entries of rows before seg_offsets[E] (a gathered row outside
- * its operand reads as zeros; out_scatter entries must be valid and distinct).
+ * and scatter entries of rows before seg_offsets[E] (non-negative; a gathered
+ * row outside its operand reads unspecified values, never memory outside the
+ * operand; out_scatter entries must be rows of out, each at most once).
  * The same sums in the same order whatever the launch: results are
  * reproducible bit for bit. */
 size_t moe_grouped_gemm_bf16_workspace_size(int mode, int64_t E, int64_t R);
@@ -517,10 +518,8 @@ enum {
     NVQ_ACT_SILU = 4,
     NVQ_ACT_SWIGLU = 5
 };
-size_t linear_act_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int act);
 int linear_act_bf16(const uint16_t* x, const uint16_t* w, const float* bias, const uint16_t* residual, int64_t M,
-                    int64_t N, int64_t K, int act, void* out, int out_dtype, uint16_t* z, void* ws, size_t ws_bytes,
-                    nvq_stream_t stream);
+                    int64_t N, int64_t K, int act, void* out, int out_dtype, uint16_t* z, nvq_stream_t stream);
 
 /* Its backward, from dout [M, N] (bf16 or fp32) and the saved z (unused and
  * nullable for NVQ_ACT_NONE): dz = dout * act'(z) in fp32,

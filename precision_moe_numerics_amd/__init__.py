@@ -108,8 +108,7 @@ _OPTIONAL = {
     "moe_fc1_swiglu_bf16": ([_vp, _i64, _i64, _vp, _vp, C.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp], C.c_int),
     "moe_expert_fwd_bf16_workspace_size": ([_i64, _i64, C.c_int, _i64, _i64], _sz),
     "moe_expert_fwd_bf16": ([_vp, _i64, _i64, _vp, C.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp], C.c_int),
-    "linear_act_bf16_workspace_size": ([_i64, _i64, _i64, C.c_int], _sz),
-    "linear_act_bf16": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, C.c_int, _vp, _vp, _sz, _vp], C.c_int),
+    "linear_act_bf16": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, C.c_int, _vp, _vp], C.c_int),
     "linear_act_bwd_bf16_workspace_size": ([_i64, _i64, _i64, C.c_int], _sz),
     "linear_act_bwd_bf16": ([_vp, C.c_int, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, _vp, C.c_int, C.c_int, _vp,
                              _vp, _sz, _vp], C.c_int),
@@ -605,45 +604,65 @@ def moe_grouped_gemm_nvfp4_bwd(mode, a, b, seg_offsets, M=0, N=None, K=0, a_gath
 
 
 # ------------------------------------------------------------------ the expert layer in BF16
+# These calls serve single tokens, where the host's part of a call counts: each
+# argument is checked once, its address taken in the same step.
 def _arg(t, dtype, name, shape, device):
-    """t is a contiguous CUDA tensor of this type, shape and device (a size of None: any; None: not given)."""
+    """Address of t (None for None), a contiguous tensor of this type and shape on `device`."""
     if t is None:
-        return
+        return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _need(t, dtype, name)
     if t.device != device:
         raise NvqError(f"{name} is on {t.device}, not on {device}")
-    if len(shape) != t.dim() or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise NvqError(f"{name} has shape {tuple(t.shape)}, not {tuple('*' if w is None else w for w in shape)}")
+    raise NvqError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
 def _main(t, dtype, name, dim):
-    """The tensor that fixes the call's device."""
+    """(device, sizes) of the tensor that fixes the call's device."""
     _need(t, dtype, name)
     if t.dim() != dim:
         raise NvqError(f"{name} must have {dim} dimensions, not {t.dim()}")
-    return t.device
+    return t.device, t.shape
+
+
+def _dims(t, dim, name):
+    """Sizes of a tensor that _arg checks later, which must have `dim` dimensions."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dim:
+        raise NvqError(f"{name} must be a tensor of {dim} dimensions")
+    return t.shape
 
 
 def _float_mode(dtype, name):
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise NvqError(f"{name} must be torch.bfloat16 or torch.float32, not {dtype}")
-    return OUT_BF16 if dtype == torch.bfloat16 else OUT_F32
+    if dtype is torch.bfloat16:
+        return OUT_BF16
+    if dtype is torch.float32:
+        return OUT_F32
+    raise NvqError(f"{name} must be torch.bfloat16 or torch.float32, not {dtype}")
 
 
-def _run16(name, device, args, ws_bytes=None, ws=None):
-    """One library call on `device` and its current stream, with a workspace of ws_bytes where the call takes one
-    (the caller's if it is large enough)."""
-    L = lib()
-    with torch.cuda.device(device):
-        tail = ()
-        if ws_bytes is not None:
-            if ws is not None:
-                _need(ws, torch.uint8, "ws")
-                if ws.device != device:
-                    raise NvqError(f"ws is on {ws.device}, not on {device}")
-            w = _ws(ws_bytes, device, ws)
-            tail = (_ptr(w), w.numel())
-        _check(getattr(L, name)(*args, *tail, C.c_void_p(torch.cuda.current_stream(device).cuda_stream)), name)
+def _scratch(nbytes, device, ws):
+    """(workspace, its address, its size): the caller's if it is large enough, else a new one."""
+    if ws is not None:
+        _need(ws, torch.uint8, "ws")
+        if ws.device != device:
+            raise NvqError(f"ws is on {ws.device}, not on {device}")
+    w = _ws(nbytes, device, ws)
+    return w, w.data_ptr(), w.numel()
+
+
+def _launch(name, device, *args):
+    """One library call on `device`'s current stream, with that device current."""
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(name, device, *args)
+    rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check(rc, name)
 
 
 def moe_grouped_gemm_bf16(mode, a, b, seg_offsets, a_gather=None, a_div=1, b_gather=None, b_div=1, out_scatter=None,
@@ -653,59 +672,56 @@ def moe_grouped_gemm_bf16(mode, a, b, seg_offsets, a_gather=None, a_div=1, b_gat
     WGRAD: a [*, M], b [*, N] -> out [E, M, N], added to `out` with accumulate.
     R is the length of a gather, else a's rows. Rows of no expert are left as they were (undefined in a new `out`)."""
     wg = mode == WGRAD
-    dev = _main(a, torch.bfloat16, "a", 2)
-    _arg(b, torch.bfloat16, "b", (None, None) if wg else (None, None, None), dev)
-    _arg(seg_offsets, torch.int32, "seg_offsets", (None,), dev)
-    E = seg_offsets.numel() - 1
+    dev, (a_rows, a_cols) = _main(a, torch.bfloat16, "a", 2)
+    E = _dims(seg_offsets, 1, "seg_offsets")[0] - 1
+    R = a_rows
+    if a_gather is not None:
+        R = _dims(a_gather, 1, "a_gather")[0]
+    elif b_gather is not None:
+        R = _dims(b_gather, 1, "b_gather")[0]
     if wg:
-        R = a_gather.numel() if a_gather is not None else b_gather.numel() if b_gather is not None else a.shape[0]
-        M, N, K = a.shape[1], b.shape[1], 0
-        shape = (E, M, N)
+        b_rows, N = _dims(b, 2, "b")
+        M, K = a_cols, 0
+        b_shape, shape = (b_rows, N), (E, M, N)
+        if b_gather is None and b_rows < R:
+            raise NvqError(f"b has {b_rows} rows for {R} rows of the segments")
     else:
-        R = a.shape[0] if a_gather is None else a_gather.numel()
-        M, K = 0, a.shape[1]
-        N = b.shape[1] if mode == FWD else b.shape[2]
-        _arg(b, torch.bfloat16, "b", (E, N, K) if mode == FWD else (E, K, N), dev)
-        shape = (R, N)
-    for t, name in ((a_gather, "a_gather"), (b_gather, "b_gather"), (out_scatter, "out_scatter")):
-        _arg(t, torch.int32, name, (R,), dev)
-    if wg and b_gather is None and b.shape[0] < R:
-        raise NvqError(f"b has {b.shape[0]} rows for {R} rows of the segments")
+        b_rows, M, K = 0, 0, a_cols
+        N = _dims(b, 3, "b")[1 if mode == FWD else 2]
+        b_shape, shape = ((E, N, K) if mode == FWD else (E, K, N)), (R, N)
     od = _float_mode(out_dtype if out is None else out.dtype, "out_dtype")
     if out is None:
         if accumulate:
             raise NvqError("accumulate needs out")
         out = torch.empty(shape, dtype=out_dtype, device=dev)
     elif out_scatter is not None:
-        _arg(out, out.dtype, "out", (None, N), dev)
-    else:
-        _arg(out, out.dtype, "out", shape, dev)
-    _run16("moe_grouped_gemm_bf16", dev,
-           (mode, _ptr(a), a.shape[0], _ptr(a_gather), a_div, _ptr(b), b.shape[0] if wg else 0, _ptr(b_gather), b_div,
-            _ptr(seg_offsets), E, R, M, N, K, _ptr(out), _ptr(out_scatter), od, int(accumulate)),
-           lib().moe_grouped_gemm_bf16_workspace_size(mode, E, R), ws)
+        shape = (_dims(out, 2, "out")[0], N)
+    i32 = torch.int32
+    w, wp, wn = _scratch(lib().moe_grouped_gemm_bf16_workspace_size(mode, E, R), dev, ws)
+    _launch("moe_grouped_gemm_bf16", dev, mode, a.data_ptr(), a_rows, _arg(a_gather, i32, "a_gather", (R,), dev), a_div,
+            _arg(b, torch.bfloat16, "b", b_shape, dev), b_rows, _arg(b_gather, i32, "b_gather", (R,), dev), b_div,
+            _arg(seg_offsets, i32, "seg_offsets", (E + 1,), dev), E, R, M, N, K,
+            _arg(out, out.dtype, "out", shape, dev), _arg(out_scatter, i32, "out_scatter", (R,), dev), od,
+            int(accumulate), wp, wn)
     return out
 
 
 def moe_fc1_swiglu_bf16(x, offsets, sorted2assign, k, w1, save_gu=False, h=None, gu=None, ws=None):
     """x bf16 [T, d], w1 bf16 [E, 2 d_ff, d] -> (h bf16 [T*k, d_ff] in sorted order, gu bf16 [T*k, 2 d_ff] or None).
-    Rows from offsets[E] on are left as they were."""
-    dev = _main(x, torch.bfloat16, "x", 2)
-    _main(w1, torch.bfloat16, "w1", 3)
-    T, d = x.shape
-    E, d_ff = w1.shape[0], w1.shape[1] // 2
-    A = T * k
-    _arg(w1, torch.bfloat16, "w1", (E, 2 * d_ff, d), dev)
-    _arg(offsets, torch.int32, "offsets", (E + 1,), dev)
-    _arg(sorted2assign, torch.int32, "sorted2assign", (A,), dev)
+    Rows from offsets[E] on are left as they were (undefined in new tensors)."""
+    bf = torch.bfloat16
+    dev, (T, d) = _main(x, bf, "x", 2)
+    E, rows, _ = _dims(w1, 3, "w1")
+    d_ff, A = rows // 2, T * k
     if h is None:
-        h = torch.empty((A, d_ff), dtype=torch.bfloat16, device=dev)
+        h = torch.empty((A, d_ff), dtype=bf, device=dev)
     if gu is None and save_gu:
-        gu = torch.empty((A, 2 * d_ff), dtype=torch.bfloat16, device=dev)
-    _arg(h, torch.bfloat16, "h", (A, d_ff), dev)
-    _arg(gu, torch.bfloat16, "gu", (A, 2 * d_ff), dev)
-    _run16("moe_fc1_swiglu_bf16", dev, (_ptr(x), T, d, _ptr(offsets), _ptr(sorted2assign), k, E, d_ff, _ptr(w1),
-                                        _ptr(h), _ptr(gu)), lib().moe_fc1_bf16_workspace_size(A, E), ws)
+        gu = torch.empty((A, 2 * d_ff), dtype=bf, device=dev)
+    w, wp, wn = _scratch(lib().moe_fc1_bf16_workspace_size(A, E), dev, ws)
+    _launch("moe_fc1_swiglu_bf16", dev, x.data_ptr(), T, d, _arg(offsets, torch.int32, "offsets", (E + 1,), dev),
+            _arg(sorted2assign, torch.int32, "sorted2assign", (A,), dev), k, E, d_ff,
+            _arg(w1, bf, "w1", (E, 2 * d_ff, d), dev), _arg(h, bf, "h", (A, d_ff), dev),
+            _arg(gu, bf, "gu", (A, 2 * d_ff), dev), wp, wn)
     return h, gu
 
 
@@ -713,57 +729,54 @@ def moe_expert_fwd_bf16(x, topk_ids, w1, w2, export=False, save_gu=False, y=None
     """BF16 expert forward. x bf16 [T, d]; topk_ids int32 [T, k]; w1 bf16 [E, 2 d_ff, d]; w2 bf16 [E, d, d_ff]
     -> y bf16 [T, k, d] (unweighted; rows of dropped assignments untouched, undefined in a new `y`), plus a dict of
     the intermediates (offsets, sorted2assign, h; gu with save_gu) when export or save_gu is set."""
-    dev = _main(x, torch.bfloat16, "x", 2)
-    _main(topk_ids, torch.int32, "topk_ids", 2)
-    _main(w1, torch.bfloat16, "w1", 3)
-    T, d = x.shape
-    k = topk_ids.shape[1]
-    E, d_ff = w1.shape[0], w1.shape[1] // 2
-    A = T * k
-    _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev)
-    _arg(w1, torch.bfloat16, "w1", (E, 2 * d_ff, d), dev)
-    _arg(w2, torch.bfloat16, "w2", (E, d, d_ff), dev)
+    bf = torch.bfloat16
+    dev, (T, d) = _main(x, bf, "x", 2)
+    k = _dims(topk_ids, 2, "topk_ids")[1]
+    E, rows, _ = _dims(w1, 3, "w1")
+    d_ff, A = rows // 2, T * k
     if y is None:
-        y = torch.empty((T, k, d), dtype=torch.bfloat16, device=dev)
-    _arg(y, torch.bfloat16, "y", (T, k, d), dev)
+        y = torch.empty((T, k, d), dtype=bf, device=dev)
     inter, bufs = {}, None
     if export or save_gu:
         inter = dict(offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
                      sorted2assign=torch.full((A,), -1, dtype=torch.int32, device=dev),
-                     h=torch.zeros((A, d_ff), dtype=torch.bfloat16, device=dev))
+                     h=torch.zeros((A, d_ff), dtype=bf, device=dev))
         if save_gu:
-            inter["gu"] = torch.zeros((A, 2 * d_ff), dtype=torch.bfloat16, device=dev)
+            inter["gu"] = torch.zeros((A, 2 * d_ff), dtype=bf, device=dev)
         bufs = MoeBuffers(**{f: (inter[f].data_ptr() if f in inter else None) for f, _ in MoeBuffers._fields_[:-1]},
                           gemm_workgroups=0)
-    _run16("moe_expert_fwd_bf16", dev, (_ptr(x), T, d, _ptr(topk_ids), k, E, d_ff, _ptr(w1), _ptr(w2), _ptr(y),
-                                        C.byref(bufs) if bufs is not None else None),
-           lib().moe_expert_fwd_bf16_workspace_size(T, d, k, E, d_ff), ws)
+    w, wp, wn = _scratch(lib().moe_expert_fwd_bf16_workspace_size(T, d, k, E, d_ff), dev, ws)
+    _launch("moe_expert_fwd_bf16", dev, x.data_ptr(), T, d, _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev), k, E,
+            d_ff, _arg(w1, bf, "w1", (E, 2 * d_ff, d), dev), _arg(w2, bf, "w2", (E, d, d_ff), dev),
+            _arg(y, bf, "y", (T, k, d), dev), C.byref(bufs) if bufs is not None else None, wp, wn)
     return (y, inter) if inter else y
 
 
+def _linear_sizes(w, act):
+    """(rows of w, outputs) of a dense product."""
+    rows = _dims(w, 2, "w")[0]
+    if act != ACT_SWIGLU:
+        return rows, rows
+    if rows % 2:
+        raise NvqError("ACT_SWIGLU needs an even number of rows in w")
+    return rows, rows // 2
+
+
 def linear_act_bf16(x, w, bias=None, act=ACT_NONE, residual=None, out_dtype=torch.bfloat16, save_z=False, out=None,
-                    z=None, ws=None):
+                    z=None):
     """act(x @ w.T + bias) + residual (include/nvq.h): x bf16 [M, K], w bf16 [N, K] (ACT_SWIGLU: [2N, K]), bias fp32,
     residual bf16 [M, N] -> out [M, N] in out_dtype, or (out, z) with save_z or z (the bf16 pre-activation)."""
-    dev = _main(x, torch.bfloat16, "x", 2)
-    _main(w, torch.bfloat16, "w", 2)
-    M, K = x.shape
-    rows = w.shape[0]
-    if act == ACT_SWIGLU and rows % 2:
-        raise NvqError("ACT_SWIGLU needs an even number of rows in w")
-    N = rows // 2 if act == ACT_SWIGLU else rows
-    _arg(w, torch.bfloat16, "w", (rows, K), dev)
-    _arg(bias, torch.float32, "bias", (rows,), dev)
-    _arg(residual, torch.bfloat16, "residual", (M, N), dev)
+    bf = torch.bfloat16
+    dev, (M, K) = _main(x, bf, "x", 2)
+    rows, N = _linear_sizes(w, act)
     od = _float_mode(out_dtype if out is None else out.dtype, "out_dtype")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     if z is None and save_z:
-        z = torch.empty((M, rows), dtype=torch.bfloat16, device=dev)
-    _arg(out, out.dtype, "out", (M, N), dev)
-    _arg(z, torch.bfloat16, "z", (M, rows), dev)
-    _run16("linear_act_bf16", dev, (_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), M, N, K, act, _ptr(out), od, _ptr(z)),
-           lib().linear_act_bf16_workspace_size(M, N, K, act), ws)
+        z = torch.empty((M, rows), dtype=bf, device=dev)
+    _launch("linear_act_bf16", dev, x.data_ptr(), _arg(w, bf, "w", (rows, K), dev),
+            _arg(bias, torch.float32, "bias", (rows,), dev), _arg(residual, bf, "residual", (M, N), dev), M, N, K, act,
+            _arg(out, out.dtype, "out", (M, N), dev), od, _arg(z, bf, "z", (M, rows), dev))
     return out if z is None else (out, z)
 
 
@@ -771,97 +784,75 @@ def linear_act_bwd_bf16(dout, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=
                         dw_dtype=torch.float32, dx=None, dw=None, dbias=None, accumulate=False, ws=None):
     """Backward of linear_act_bf16 from dout (bf16 or fp32 [M, N]) and the saved z: (dx bf16 [M, K], dw [shape of w],
     dbias fp32 [rows of w]), None where not needed. accumulate adds to the given dw and dbias."""
-    dev = _main(x, torch.bfloat16, "x", 2)
-    _main(w, torch.bfloat16, "w", 2)
-    M, K = x.shape
-    rows = w.shape[0]
-    if act == ACT_SWIGLU and rows % 2:
-        raise NvqError("ACT_SWIGLU needs an even number of rows in w")
-    N = rows // 2 if act == ACT_SWIGLU else rows
-    _arg(w, torch.bfloat16, "w", (rows, K), dev)
-    if not isinstance(dout, torch.Tensor):
-        raise NvqError("dout must be a tensor")
-    _arg(dout, torch.float32 if dout.dtype == torch.float32 else torch.bfloat16, "dout", (M, N), dev)
-    _arg(z, torch.bfloat16, "z", (M, rows), dev)
+    bf, f32 = torch.bfloat16, torch.float32
+    dev, (M, K) = _main(x, bf, "x", 2)
+    rows, N = _linear_sizes(w, act)
+    _dims(dout, 2, "dout")
     need_dx, need_dw, need_dbias = need_dx or dx is not None, need_dw or dw is not None, need_dbias or dbias is not None
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         raise NvqError("accumulate needs dw and dbias to add to")
+    gd = _float_mode(dout.dtype, "dout")
     wd = _float_mode(dw_dtype if dw is None else dw.dtype, "dw_dtype")
     if dx is None and need_dx:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dx = torch.empty((M, K), dtype=bf, device=dev)
     if dw is None and need_dw:
         dw = torch.empty((rows, K), dtype=dw_dtype, device=dev)
     if dbias is None and need_dbias:
-        dbias = torch.empty((rows,), dtype=torch.float32, device=dev)
-    _arg(dx, torch.bfloat16, "dx", (M, K), dev)
-    if dw is not None:
-        _arg(dw, dw.dtype, "dw", (rows, K), dev)
-    _arg(dbias, torch.float32, "dbias", (rows,), dev)
-    _run16("linear_act_bwd_bf16", dev,
-           (_ptr(dout), OUT_F32 if dout.dtype == torch.float32 else OUT_BF16, _ptr(x), _ptr(w), _ptr(z), M, N, K, act,
-            _ptr(dx), _ptr(dw), wd, int(accumulate), _ptr(dbias)),
-           lib().linear_act_bwd_bf16_workspace_size(M, N, K, act), ws)
+        dbias = torch.empty((rows,), dtype=f32, device=dev)
+    ws, wp, wn = _scratch(lib().linear_act_bwd_bf16_workspace_size(M, N, K, act), dev, ws)
+    _launch("linear_act_bwd_bf16", dev, _arg(dout, dout.dtype, "dout", (M, N), dev), gd, x.data_ptr(),
+            _arg(w, bf, "w", (rows, K), dev), _arg(z, bf, "z", (M, rows), dev), M, N, K, act,
+            _arg(dx, bf, "dx", (M, K), dev), _arg(dw, f32 if wd == OUT_F32 else bf, "dw", (rows, K), dev), wd,
+            int(accumulate), _arg(dbias, f32, "dbias", (rows,), dev), wp, wn)
     return dx, dw, dbias
 
 
 def moe_combine_bf16(y, weights, topk_ids=None, E=0, residual=None, out=None):
     """out[t] = residual[t] + sum_s weights[t, s] y[t, s]: y bf16 [T, k, C], weights fp32 [T, k] -> bf16 [T, C].
     With topk_ids (int32 [T, k]) and E, slots whose id is outside [0, E) are dropped."""
-    dev = _main(y, torch.bfloat16, "y", 3)
-    T, k, Cdim = y.shape
-    _arg(weights, torch.float32, "weights", (T, k), dev)
-    _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev)
-    _arg(residual, torch.bfloat16, "residual", (T, Cdim), dev)
+    bf = torch.bfloat16
+    dev, (T, k, Cdim) = _main(y, bf, "y", 3)
     if out is None:
-        out = torch.empty((T, Cdim), dtype=torch.bfloat16, device=dev)
-    _arg(out, torch.bfloat16, "out", (T, Cdim), dev)
-    _run16("moe_combine_bf16", dev, (_ptr(y), _ptr(weights), _ptr(topk_ids), E, _ptr(residual), T, k, Cdim, _ptr(out)))
+        out = torch.empty((T, Cdim), dtype=bf, device=dev)
+    _launch("moe_combine_bf16", dev, y.data_ptr(), _arg(weights, torch.float32, "weights", (T, k), dev),
+            _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev), E, _arg(residual, bf, "residual", (T, Cdim), dev), T, k,
+            Cdim, _arg(out, bf, "out", (T, Cdim), dev))
     return out
 
 
 def moe_combine_bwd_bf16(dout, y, weights, topk_ids=None, E=0, dy=None, dw=None):
     """Backward of moe_combine_bf16: dout bf16 [T, C] -> (dy bf16 [T, k, C], dw fp32 [T, k]); zeros for dropped slots."""
-    dev = _main(y, torch.bfloat16, "y", 3)
-    T, k, Cdim = y.shape
-    _arg(dout, torch.bfloat16, "dout", (T, Cdim), dev)
-    _arg(weights, torch.float32, "weights", (T, k), dev)
-    _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev)
+    bf, f32 = torch.bfloat16, torch.float32
+    dev, (T, k, Cdim) = _main(y, bf, "y", 3)
     if dy is None:
-        dy = torch.empty((T, k, Cdim), dtype=torch.bfloat16, device=dev)
+        dy = torch.empty((T, k, Cdim), dtype=bf, device=dev)
     if dw is None:
-        dw = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _arg(dy, torch.bfloat16, "dy", (T, k, Cdim), dev)
-    _arg(dw, torch.float32, "dw", (T, k), dev)
-    _run16("moe_combine_bwd_bf16", dev, (_ptr(dout), _ptr(y), _ptr(weights), _ptr(topk_ids), E, T, k, Cdim, _ptr(dy),
-                                         _ptr(dw)))
+        dw = torch.empty((T, k), dtype=f32, device=dev)
+    _launch("moe_combine_bwd_bf16", dev, _arg(dout, bf, "dout", (T, Cdim), dev), y.data_ptr(),
+            _arg(weights, f32, "weights", (T, k), dev), _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev), E, T, k,
+            Cdim, _arg(dy, bf, "dy", (T, k, Cdim), dev), _arg(dw, f32, "dw", (T, k), dev))
     return dy, dw
 
 
 def moe_router_softmax_topk_bwd(weights, topk_ids, dweights, E, dlogits=None):
     """Gradient of moe_router_softmax_topk's weights: (weights fp32, topk_ids int32, dweights fp32) [T, k] -> fp32 [T, E]."""
-    dev = _main(weights, torch.float32, "weights", 2)
-    T, k = weights.shape
-    _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev)
-    _arg(dweights, torch.float32, "dweights", (T, k), dev)
+    f32 = torch.float32
+    dev, (T, k) = _main(weights, f32, "weights", 2)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
-    _arg(dlogits, torch.float32, "dlogits", (T, E), dev)
-    _run16("moe_router_softmax_topk_bwd", dev, (_ptr(weights), _ptr(topk_ids), _ptr(dweights), T, E, k, _ptr(dlogits)))
+        dlogits = torch.empty((T, E), dtype=f32, device=dev)
+    _launch("moe_router_softmax_topk_bwd", dev, weights.data_ptr(), _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev),
+            _arg(dweights, f32, "dweights", (T, k), dev), T, E, k, _arg(dlogits, f32, "dlogits", (T, E), dev))
     return dlogits
 
 
 def moe_router_sigmoid_topk_bwd(weights, logits, topk_ids, dweights, dlogits=None):
     """Gradient of moe_router_sigmoid_topk's weights, from the forward's weights and logits [T, E] -> fp32 [T, E]."""
-    dev = _main(logits, torch.float32, "logits", 2)
-    T, E = logits.shape
-    _main(weights, torch.float32, "weights", 2)
-    k = weights.shape[1]
-    _arg(weights, torch.float32, "weights", (T, k), dev)
-    _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev)
-    _arg(dweights, torch.float32, "dweights", (T, k), dev)
+    f32 = torch.float32
+    dev, (T, E) = _main(logits, f32, "logits", 2)
+    k = _dims(weights, 2, "weights")[1]
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
-    _arg(dlogits, torch.float32, "dlogits", (T, E), dev)
-    _run16("moe_router_sigmoid_topk_bwd", dev, (_ptr(weights), _ptr(logits), _ptr(topk_ids), _ptr(dweights), T, E, k,
-                                                _ptr(dlogits)))
+        dlogits = torch.empty((T, E), dtype=f32, device=dev)
+    _launch("moe_router_sigmoid_topk_bwd", dev, _arg(weights, f32, "weights", (T, k), dev), logits.data_ptr(),
+            _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev), _arg(dweights, f32, "dweights", (T, k), dev), T, E, k,
+            _arg(dlogits, f32, "dlogits", (T, E), dev))
     return dlogits

@@ -161,17 +161,20 @@ __global__ __launch_bounds__(256) void k_combine16_bwd(const uint16_t* __restric
 // dlogits of the top-k weights. With D = sum_i w_i dw_i:
 //   softmax over the chosen logits: g_j = w_j (dw_j - D);
 //   w_j = s_j / S, s_j = sigmoid(logit_j): g_j = w_j (1 - s_j) (dw_j - D).
-// One wave per token, lane j the j-th chosen expert. Every lane then fills the
-// columns lane, lane + 64, ... of the token's row, comparing each against the
-// k ids (broadcast as scalars): the row is written once, coalesced, and an id
-// that occurs twice adds up in slot order. Ids outside [0, E) match no column.
-template <bool SIGMOID>
+// One wave per token, lane j the j-th chosen expert. The token's row is laid
+// out in LDS (zeros, then the k gradients; ids that occur twice have been added
+// up in slot order, so both lanes write the same sum) and written once, 16
+// bytes a lane where rows start on 16 bytes. Ids outside [0, E) write nothing.
+constexpr int kRouterE = 1024;
+template <bool SIGMOID, bool V4>
 __global__ __launch_bounds__(256) void k_router_bwd(const float* __restrict__ w, const float* __restrict__ logits,
                                                     const int32_t* __restrict__ ids, const float* __restrict__ dw,
                                                     int64_t T, int E, int k, float* __restrict__ dlogits) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (int)(threadIdx.x >> 6);
-    if (t >= T) return;
+    __shared__ __attribute__((aligned(16))) float rows[4][kRouterE];
+    const int lane = threadIdx.x & 63, wave = (int)(threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    if (t >= T) return;  // whole waves; no barrier below
+    float* row = rows[wave];
     int id = -1;
     float wj = 0.0f, dj = 0.0f, f = 1.0f;
     if (lane < k) {
@@ -181,17 +184,37 @@ __global__ __launch_bounds__(256) void k_router_bwd(const float* __restrict__ w,
         if (SIGMOID && (uint32_t)id < (uint32_t)E)  // 1 - sigmoid(v) = 1 / (1 + exp(v))
             f = 1.0f / (1.0f + __expf(logits[t * E + id]));
     }
+    for (int c = lane * 4; c < E; c += 256) *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float D = wave_sum(wj * dj);
     const float g = wj * f * (dj - D);
-    for (int c = lane; c < E; c += 64) {
-        float v = 0.0f;
-        for (int j = 0; j < k; ++j) {
-            const int idj = __builtin_amdgcn_readlane(id, j);
-            const float gj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(g), j));
-            v += idj == c ? gj : 0.0f;
-        }
-        dlogits[t * E + c] = v;
+    float sum = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        const int idj = __builtin_amdgcn_readlane(id, j);
+        const float gj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(g), j));
+        sum += idj == id ? gj : 0.0f;
     }
+    __builtin_amdgcn_wave_barrier();  // one wave's LDS accesses complete in order
+    if (lane < k && (uint32_t)id < (uint32_t)E) row[id] = sum;
+    __builtin_amdgcn_wave_barrier();
+    float* out = dlogits + t * E;
+    if (V4) {
+        for (int c = lane * 4; c < E; c += 256)
+            *reinterpret_cast<float4*>(out + c) = *reinterpret_cast<const float4*>(row + c);
+    } else {
+        for (int c = lane; c < E; c += 64) out[c] = row[c];
+    }
+}
+
+template <bool SIGMOID>
+void launch_router_bwd(const float* w, const float* logits, const int32_t* ids, const float* dw, int64_t T, int64_t E,
+                       int k, float* dlogits, hipStream_t s) {
+    const dim3 grid((unsigned)((T + 3) / 4));
+    if (E % 4 == 0 && aligned16(dlogits))
+        hipLaunchKernelGGL((k_router_bwd<SIGMOID, true>), grid, dim3(256), 0, s, w, logits, ids, dw, T, (int)E, k,
+                           dlogits);
+    else
+        hipLaunchKernelGGL((k_router_bwd<SIGMOID, false>), grid, dim3(256), 0, s, w, logits, ids, dw, T, (int)E, k,
+                           dlogits);
 }
 
 // The rows of y that one workgroup addresses from its descriptor's base (the
@@ -250,8 +273,7 @@ int moe_router_softmax_topk_bwd(const float* w, const int32_t* topk_ids, const f
     if (!router_dims_ok(T, E, k)) return NVQ_ERR_DIM;
     if (T > 0 && (!w || !topk_ids || !dw || !dlogits)) return NVQ_ERR_NULL;
     if (T == 0) return NVQ_OK;
-    hipLaunchKernelGGL(k_router_bwd<false>, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, as_stream(stream), w,
-                       nullptr, topk_ids, dw, T, (int)E, k, dlogits);
+    launch_router_bwd<false>(w, nullptr, topk_ids, dw, T, E, k, dlogits, as_stream(stream));
     return launch_status();
 }
 
@@ -260,8 +282,7 @@ int moe_router_sigmoid_topk_bwd(const float* w, const float* logits, const int32
     if (!router_dims_ok(T, E, k)) return NVQ_ERR_DIM;
     if (T > 0 && (!w || !logits || !topk_ids || !dw || !dlogits)) return NVQ_ERR_NULL;
     if (T == 0) return NVQ_OK;
-    hipLaunchKernelGGL(k_router_bwd<true>, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, as_stream(stream), w, logits,
-                       topk_ids, dw, T, (int)E, k, dlogits);
+    launch_router_bwd<true>(w, logits, topk_ids, dw, T, E, k, dlogits, as_stream(stream));
     return launch_status();
 }
 

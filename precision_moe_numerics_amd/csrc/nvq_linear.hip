@@ -29,6 +29,7 @@ __device__ __forceinline__ float act_bwd(float dout, float z) {
 
 constexpr int kBwdCols = 512;  // columns of a workgroup: 64 lanes x 8
 constexpr int kBwdRows = 64;   // rows of a workgroup: 4 waves x 16
+constexpr int kFoldWaves = 16; // row blocks folded side by side
 
 __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
     const uint4 w = *reinterpret_cast<const uint4*>(p);
@@ -105,14 +106,23 @@ __global__ __launch_bounds__(256) void k_act_bwd(const void* __restrict__ dout, 
     }
 }
 
-// dbias[c] (+)= sum of part[b][c] over the row blocks, in order.
-__global__ __launch_bounds__(256) void k_fold_bias(const float* __restrict__ part, int64_t nb, int64_t R,
-                                                   int accumulate, float* __restrict__ dbias) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= R) return;
-    float s = accumulate ? dbias[c] : 0.0f;
-    for (int64_t b = 0; b < nb; ++b) s += part[b * R + c];
-    dbias[c] = s;
+// dbias[c] (+)= sum of part[b][c] over the row blocks: wave w of the workgroup
+// adds blocks w, w + 16, .. of 64 columns, then the waves' sums are added in
+// order.
+__global__ __launch_bounds__(64 * kFoldWaves) void k_fold_bias(const float* __restrict__ part, int64_t nb, int64_t R,
+                                                               int accumulate, float* __restrict__ dbias) {
+    __shared__ float red[kFoldWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.0f;
+    if (c < R)
+        for (int64_t b = wave; b < nb; b += kFoldWaves) s += part[b * R + c];
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c >= R) return;
+#pragma unroll
+    for (int w = 1; w < kFoldWaves; ++w) s += red[w][lane];
+    dbias[c] = accumulate ? dbias[c] + s : s;
 }
 
 template <int ACT>
@@ -129,10 +139,9 @@ bool linear_dims_ok(int64_t M, int64_t N, int64_t K, int act) {
     return gemm16_dims_ok(kFwd, glu, M, 1, 0, N, K) && M <= (int64_t)65535 * kBwdRows;
 }
 
-size_t bwd_carve(Carver& c, int64_t M, int64_t R, uint16_t** dz, float** part, void** gws) {
+size_t bwd_carve(Carver& c, int64_t M, int64_t R, uint16_t** dz, float** part) {
     *dz = c.take<uint16_t>((size_t)(M * R));
     *part = c.take<float>((size_t)((M + kBwdRows - 1) / kBwdRows * R));
-    *gws = c.take<uint8_t>(gemm16_ws_bytes(M, 1));
     return c.need;
 }
 
@@ -143,21 +152,14 @@ using namespace nvq;
 
 extern "C" {
 
-size_t linear_act_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int act) {
-    (void)N; (void)K; (void)act;
-    return gemm16_ws_bytes(M, 1);
-}
-
 int linear_act_bf16(const uint16_t* x, const uint16_t* w, const float* bias, const uint16_t* residual, int64_t M,
-                    int64_t N, int64_t K, int act, void* out, int out_dtype, uint16_t* z, void* ws, size_t ws_bytes,
-                    nvq_stream_t stream) {
+                    int64_t N, int64_t K, int act, void* out, int out_dtype, uint16_t* z, nvq_stream_t stream) {
     if (!act_ok(act) || (out_dtype != NVQ_OUT_BF16 && out_dtype != NVQ_OUT_F32)) return NVQ_ERR_UNSUPPORTED;
     if (!linear_dims_ok(M, N, K, act)) return NVQ_ERR_DIM;
-    if (!w || !ws || (M > 0 && (!x || !out))) return NVQ_ERR_NULL;
+    if (!w || (M > 0 && (!x || !out))) return NVQ_ERR_NULL;
     if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(out) ||
-        !aligned16(z) || !aligned256(ws))
+        !aligned16(z))
         return NVQ_ERR_ALIGN;
-    if (ws_bytes < linear_act_bf16_workspace_size(M, N, K, act)) return NVQ_ERR_WORKSPACE;
     Args p{};
     p.a = x; p.b = w;
     p.a_div = p.b_div = 1;
@@ -166,7 +168,7 @@ int linear_act_bf16(const uint16_t* x, const uint16_t* w, const float* bias, con
     p.E = 1; p.rows = (int32_t)M; p.N = (int32_t)N; p.K = (int32_t)K;
     p.out_f32 = out_dtype == NVQ_OUT_F32;
     p.act = act;
-    launch_gemm16(kFwd, act == NVQ_ACT_SWIGLU ? kEpiGlu : kEpiAct, p, ws, as_stream(stream));
+    launch_gemm16(kFwd, act == NVQ_ACT_SWIGLU ? kEpiGlu : kEpiAct, p, nullptr, as_stream(stream));
     return launch_status();
 }
 
@@ -175,9 +177,8 @@ size_t linear_act_bwd_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int a
     Carver c(nullptr);
     uint16_t* dz;
     float* part;
-    void* g;
     return bwd_carve(c, std::max<int64_t>(M, 0), std::max<int64_t>(N, 0) * (act == NVQ_ACT_SWIGLU ? 2 : 1), &dz,
-                     &part, &g);
+                     &part);
 }
 
 int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, const uint16_t* w, const uint16_t* z,
@@ -201,8 +202,7 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
     Carver cv(ws);
     uint16_t* dz;
     float* part;
-    void* gws;
-    bwd_carve(cv, M, R, &dz, &part, &gws);
+    bwd_carve(cv, M, R, &dz, &part);
     // without an activation a bf16 dout is dz itself
     const bool same = act == NVQ_ACT_NONE && dout_dtype == NVQ_OUT_BF16;
     const bool need_dz = !same && (dx || dw);
@@ -221,7 +221,7 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
         NVQ_CHECK_LAUNCH();
     }
     if (dbias)
-        hipLaunchKernelGGL(k_fold_bias, dim3((unsigned)((R + 255) / 256)), dim3(256), 0, s, part,
+        hipLaunchKernelGGL(k_fold_bias, dim3((unsigned)((R + 63) / 64)), dim3(64 * kFoldWaves), 0, s, part,
                            (M + kBwdRows - 1) / kBwdRows, R, accumulate, dbias);
     const uint16_t* dzp = same ? static_cast<const uint16_t*>(dout) : dz;
     Args p{};
@@ -232,7 +232,7 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
         p.b = w; p.out = dx;
         p.lda = (int32_t)R; p.ldb = (int32_t)K;
         p.N = (int32_t)K; p.K = (int32_t)R;
-        launch_gemm16(kDgrad, kEpiOut, p, gws, s);
+        launch_gemm16(kDgrad, kEpiOut, p, nullptr, s);
     }
     if (dw) {
         p.b = x; p.out = dw;
@@ -240,7 +240,7 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
         p.M = (int32_t)R; p.N = (int32_t)K; p.K = 0;
         p.out_f32 = dw_dtype == NVQ_OUT_F32;
         p.accumulate = accumulate != 0;
-        launch_gemm16(kWgrad, kEpiOut, p, gws, s);
+        launch_gemm16(kWgrad, kEpiOut, p, nullptr, s);
     }
     return launch_status();
 }

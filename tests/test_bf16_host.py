@@ -79,14 +79,14 @@ def test_layer_refusals():
 def test_linear_refusals():
     L = nvq.lib()
 
-    def lin(x=_p(0), w=_p(1), b=None, r=None, M=16, N=64, K=64, act=0, out=_p(2), dt=0, z=None, ws=_p(3), wsb=BIG):
-        return L.linear_act_bf16(x, w, b, r, M, N, K, act, out, dt, z, ws, wsb, None)
+    def lin(x=_p(0), w=_p(1), b=None, r=None, M=16, N=64, K=64, act=0, out=_p(2), dt=0, z=None):
+        return L.linear_act_bf16(x, w, b, r, M, N, K, act, out, dt, z, None)
 
     def bwd(g=_p(0), gt=0, x=_p(1), w=_p(2), z=_p(3), M=16, N=64, K=64, act=4, dx=_p(4), dw=_p(5), wt=1, acc=0,
             db=_p(6), ws=_p(7), wsb=BIG):
         return L.linear_act_bwd_bf16(g, gt, x, w, z, M, N, K, act, dx, dw, wt, acc, db, ws, wsb, None)
 
-    for fn, nulls, mis in ((lin, ("x", "w", "out", "ws"), ("x", "w", "b", "r", "out", "z", "ws")),
+    for fn, nulls, mis in ((lin, ("x", "w", "out"), ("x", "w", "b", "r", "out", "z")),
                            (bwd, ("g", "x", "w", "z", "ws"), ("g", "x", "w", "z", "dx", "dw", "db", "ws"))):
         for n in nulls:
             assert fn(**{n: None}) == NULL, n
@@ -96,7 +96,7 @@ def test_linear_refusals():
                     dict(N=1 << 20, K=1 << 20)):
             assert fn(**bad) == DIM, bad
         assert fn(act=6) == UNSUPPORTED and fn(act=-1) == UNSUPPORTED
-        assert fn(wsb=16) == WORKSPACE
+    assert bwd(wsb=16) == WORKSPACE
     assert lin(dt=5) == UNSUPPORTED and bwd(gt=2) == UNSUPPORTED and bwd(wt=2) == UNSUPPORTED
     assert bwd(dx=None, dw=None, db=None) == NULL
 
