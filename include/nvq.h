@@ -509,7 +509,7 @@ int moe_expert_fwd_bf16(const uint16_t* x, int64_t T, int64_t d, const int32_t* 
  * pre-activation in bf16 for the backward; act sees the fp32 one.
  * NVQ_ACT_SWIGLU: w [2*N, K], bias [2*N], z [M, 2*N] (gate half first),
  * act(z) = silu(gate) * up. GELU is the exact one (erf), GELU_TANH the tanh
- * form. Limits as for NVQ_FWD with one expert; M <= 65535 * 64. */
+ * form. Limits as for NVQ_FWD with one expert; M * N < 2^40. */
 enum {
     NVQ_ACT_NONE = 0,
     NVQ_ACT_RELU = 1,

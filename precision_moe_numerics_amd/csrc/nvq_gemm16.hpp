@@ -11,6 +11,8 @@
 // way in and scattered on the way out.
 #pragma once
 
+#include <type_traits>
+
 #include "nvq_device.hpp"
 #include "nvq_host.hpp"
 
@@ -28,7 +30,6 @@ enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };   // operand arrangement
 enum { kEpiOut = 0, kEpiAct = 1, kEpiGlu = 2 };
 
 constexpr int kBK = 64;          // K per LDS stage
-constexpr int kWgradRows = 16;   // (unused rows of a segment cost at most a stage)
 
 // One m-tile of the row-segmented arrangements, written by k_tile_table.
 struct Tile {
@@ -78,7 +79,7 @@ __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t off, uint32_t lds_add
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %1, %2, 0 offen lds"
         :
-        : "s"(lds_addr), "v"(off), "s"(rsrc)
+        : "s"(__builtin_amdgcn_readfirstlane((int)lds_addr)), "v"(off), "s"(rsrc)
         : "memory");
 }
 
@@ -89,7 +90,7 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t off, uint32_t lds_addr
         "s_nop 0\n\t"
         "buffer_load_dword %1, %2, 0 offen lds"
         :
-        : "s"(lds_addr), "v"(off), "s"(rsrc)
+        : "s"(__builtin_amdgcn_readfirstlane((int)lds_addr)), "v"(off), "s"(rsrc)
         : "memory");
 }
 
@@ -350,8 +351,10 @@ __device__ __forceinline__ uint32_t div_by(uint32_t v, uint32_t mul, int shift) 
 
 // ------------------------------------------------------------------ the kernel
 // Tile TM x TN, WM x WN waves; every wave holds (TM / WM) x (TN / WN) outputs
-// as 16 x 16 blocks. Two LDS stages of kBK: the next stage is in flight while
-// this one is multiplied.
+// as 16 x 16 blocks. Two LDS stages of kBK. A step reads its whole stage into
+// registers first; after a barrier the stage two steps on is fetched into its
+// place, under the products of this step and all of the next. Two workgroups
+// of the 128 x 128 tile share a CU and cover each other's waits.
 template <int MODE, int EPI, int TM, int TN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     constexpr int NW = WM * WN;
@@ -370,17 +373,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     const int t = (G % 8 == 0) ? (int)((blockIdx.x % 8) * (G / 8) + blockIdx.x / 8) : (int)blockIdx.x;
     const int nt = t % p.n_tiles, mt = t / p.n_tiles;
     int e = 0, row0, row_end;  // FWD, DGRAD: token rows; WGRAD: output rows
-    int k0 = 0, kend = p.K;    // WGRAD: token rows
+    int k0 = 0, klen = p.K;    // WGRAD: token rows
     if (MODE == kWgrad) {
         e = mt / p.m_tiles;
-        if (e >= p.E) return;
         row0 = (mt % p.m_tiles) * TM;
         row_end = p.M;
+        klen = p.rows;
         if (p.seg) {
             k0 = min(max(sload(p.seg, e), 0), p.rows);
-            kend = min(max(sload(p.seg, e + 1), k0), p.rows);
-        } else {
-            kend = p.rows;
+            klen = max(min(max(sload(p.seg, e + 1), 0), p.rows) - k0, 0);
         }
     } else if (p.tiles) {
         if (mt >= sload(p.tile_count, 0)) return;
@@ -390,113 +391,92 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     } else {
         row0 = mt * TM;
         row_end = p.rows;
-        if (row0 >= row_end) return;
     }
     constexpr int TNO = EPI == kEpiGlu ? TN / 2 : TN;  // output columns of a tile
     const int col0 = nt * TNO;
 
     // ---- operand addressing: lane offsets (bytes) within a descriptor whose
-    // base advances along K
+    // base advances along K. Rows and columns past the tile's edge are loaded as
+    // they come or as zeros: they only reach outputs that are not stored.
     const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
-    uint32_t ao[CA], bo[CB];
+    uint32_t ao[A_R ? 1 : CA], bo;
     const uint16_t *abase, *bbase;
-    int64_t a_lim, b_lim;       // bytes of the descriptor at k0
+    int64_t a_lim, b_lim;       // bytes of the descriptor at k = 0
     const int kc = ((lane & 7) ^ (lane >> 3)) * 8;  // k of this lane's chunk in K-contiguous stages
+    const bool ga = p.a_gather != nullptr, gb = MODE == kWgrad && p.b_gather != nullptr;
+    // K-strided stage of R columns: piece i of a wave is 512 / R k rows of R / 8 chunks
+    auto row_r = [&](int R, int i) { return (i * NW + wave) * (512 / R) + lane / (R / 8); };
+    auto col_r = [&](int R) { return (int)((uint32_t)(lane % (R / 8)) ^ rkey(row_r(R, 0))) * 8; };
     if constexpr (!A_R) {
-        const bool gat = p.a_gather != nullptr;
-        abase = gat ? p.a : p.a + (int64_t)row0 * p.lda;
-        a_lim = gat ? p.a_bytes : (int64_t)(row_end - row0) * lda2;
+        abase = ga ? p.a : p.a + (int64_t)row0 * p.lda;
+        a_lim = ga ? p.a_bytes : (int64_t)(row_end - row0) * lda2;
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
             const int rl = (i * NW + wave) * 8 + (lane >> 3);
-            const bool ok = row0 + rl < row_end;
             uint32_t src = rl;
-            if (gat) src = div_by((uint32_t)p.a_gather[ok ? row0 + rl : row0], p.a_mul, p.a_shift);
-            ao[i] = ok ? src * lda2 + kc * 2 : kNowhere;
+            if (ga) src = div_by((uint32_t)p.a_gather[min(row0 + rl, row_end - 1)], p.a_mul, p.a_shift);
+            ao[i] = src * lda2 + kc * 2;
         }
     } else {
-        abase = p.a_gather ? p.a : p.a + (int64_t)k0 * p.lda;
-        a_lim = p.a_gather ? p.a_bytes : (int64_t)(kend - k0) * lda2;
+        abase = ga ? p.a : p.a + (int64_t)k0 * p.lda;
+        a_lim = ga ? p.a_bytes : (int64_t)klen * lda2;
+        ao[0] = (row0 + col_r(TM)) * 2 + (ga ? 0 : row_r(TM, 0) * lda2);
     }
     if constexpr (!B_R) {
         constexpr int rows_per = EPI == kEpiGlu ? 2 : 1;
-        bbase = p.b + (int64_t)e * rows_per * p.N * p.ldb;
-        b_lim = (int64_t)rows_per * p.N * ldb2;
-#pragma unroll
-        for (int i = 0; i < CB; ++i) {
-            const int r = (i * NW + wave) * 8 + (lane >> 3);
-            int n, src;
-            if (EPI == kEpiGlu) {  // blocks of 16: gate, up, gate, up, ...
-                n = col0 + (r >> 5) * 16 + (r & 15);
-                src = ((r >> 4) & 1) * p.N + n;
-            } else {
-                n = src = col0 + r;
-            }
-            bo[i] = n < p.N ? (uint32_t)src * ldb2 + kc * 2 : kNowhere;
-        }
-    } else if constexpr (MODE == kDgrad) {
-        bbase = p.b + (int64_t)e * p.K * p.ldb;
-        b_lim = (int64_t)p.K * ldb2;
+        bbase = p.b + ((int64_t)e * rows_per * p.N + col0) * p.ldb;
+        b_lim = ((int64_t)rows_per * p.N - col0) * ldb2;
+        const int r = wave * 8 + (lane >> 3);
+        // GLU: blocks of 16: gate, up, gate, up, ...
+        bo = (uint32_t)(EPI == kEpiGlu ? ((r >> 4) & 1) * p.N + (r >> 5) * 16 + (r & 15) : r) * ldb2 + kc * 2;
     } else {
-        bbase = p.b_gather ? p.b : p.b + (int64_t)k0 * p.ldb;
-        b_lim = p.b_gather ? p.b_bytes : (int64_t)(kend - k0) * ldb2;
+        bbase = gb ? p.b : p.b + (MODE == kDgrad ? (int64_t)e * p.K : (int64_t)k0) * p.ldb;
+        b_lim = gb ? p.b_bytes : (int64_t)klen * ldb2;
+        bo = (col0 + col_r(TN)) * 2 + (gb ? 0 : row_r(TN, 0) * ldb2);
     }
-    // K-strided stages: 16-byte chunk id = k row * (R / 8) + slot
-    auto r_off = [&](int i, int R, int c0, int lim, uint32_t ld2, uint32_t* krow) {
-        const int id = (i * NW + wave) * 64 + lane;
-        const uint32_t k = (uint32_t)id / (uint32_t)(R / 8), slot = (uint32_t)id % (uint32_t)(R / 8);
-        const int c = c0 + (int)(slot ^ rkey(k)) * 8;
-        *krow = k;
-        return c < lim ? (uint32_t)c * 2u : kNowhere;
-    };
-    uint32_t ak[CA], bk[CB];
-    if constexpr (A_R) {
-#pragma unroll
-        for (int i = 0; i < CA; ++i) ao[i] = r_off(i, TM, row0, row_end, lda2, &ak[i]);
-    }
-    if constexpr (B_R) {
-#pragma unroll
-        for (int i = 0; i < CB; ++i) bo[i] = r_off(i, TN, col0, p.N, ldb2, &bk[i]);
-    }
-
-    const int klen = kend - k0;
     const int nk = (klen + kBK - 1) / kBK;
-    auto issue = [&](int s, int buf) {
-        const uint32_t la = lds0 + buf * kStage, lb = la + TM * 128;
-        const int k = s * kBK;
-        if constexpr (!A_R) {
-            const i32x4 ra = make_rsrc(abase + k, a_lim - (int64_t)k * 2);
-            const bool ok = k + kc < klen;
+    // K-strided pieces: by row number, or through a gather (its entries by scalar loads)
+    auto issue_r = [&](auto R_tag, const uint16_t* base, int64_t lim, uint32_t o, int ld, bool gat,
+                       const int32_t* gather, uint32_t mul, int shift, int k, uint32_t dst) {
+        constexpr int R = decltype(R_tag)::value, n = R * 8 / (64 * NW), per = 512 / R;
+        const uint32_t ld2 = (uint32_t)ld * 2u;
+        const i32x4 r = gat ? make_rsrc(base, lim) : make_rsrc(base + (int64_t)k * ld, lim - (int64_t)k * ld2);
+        const int q = lane / (R / 8);
 #pragma unroll
-            for (int i = 0; i < CA; ++i) dma16(ra, ok ? ao[i] : kNowhere, la + (i * NW + wave) * 1024);
-        } else {
-            const bool gat = p.a_gather != nullptr;
-            const i32x4 ra = gat ? make_rsrc(abase, a_lim)
-                                 : make_rsrc(abase + (int64_t)k * p.lda, a_lim - (int64_t)k * lda2);
+        for (int i = 0; i < n; ++i) {
+            uint32_t off = o + i * NW * per * ld2;
+            if (gat) {
+                const int kl = k + (i * NW + wave) * per;
+                uint32_t v = (uint32_t)sload(gather, k0 + min(kl, klen - 1));
 #pragma unroll
-            for (int i = 0; i < CA; ++i) {
-                const bool ok = k + (int)ak[i] < klen && ao[i] != kNowhere;
-                uint32_t row = ak[i];
-                if (gat) row = div_by((uint32_t)p.a_gather[ok ? k0 + k + (int)ak[i] : k0], p.a_mul, p.a_shift);
-                dma16(ra, ok ? row * lda2 + ao[i] : kNowhere, la + (i * NW + wave) * 1024);
+                for (int u = 1; u < per; ++u) {
+                    const uint32_t w = (uint32_t)sload(gather, k0 + min(kl + u, klen - 1));
+                    v = q == u ? w : v;
+                }
+                off = kl + q < klen ? div_by(v, mul, shift) * ld2 + o : kNowhere;
             }
+            dma16(r, off, dst + (i * NW + wave) * 1024);
+        }
+    };
+    auto issue = [&](int s) {
+        const uint32_t la = lds0 + (s & 1) * kStage, lb = la + TM * 128;
+        const int k = s * kBK;
+        const bool in_k = k + kc < klen;
+        if constexpr (!A_R) {
+            const i32x4 r = make_rsrc(abase + k, a_lim - (int64_t)k * 2);
+#pragma unroll
+            for (int i = 0; i < CA; ++i) dma16(r, in_k ? ao[i] : kNowhere, la + (i * NW + wave) * 1024);
+        } else {
+            issue_r(std::integral_constant<int, TM>{}, abase, a_lim, ao[0], p.lda, ga, p.a_gather, p.a_mul, p.a_shift, k,
+                    la);
         }
         if constexpr (!B_R) {
-            const i32x4 rb = make_rsrc(bbase + k, b_lim - (int64_t)k * 2);
-            const bool ok = k + kc < klen;
+            const i32x4 r = make_rsrc(bbase + k, b_lim - (int64_t)k * 2);
+            constexpr int step = EPI == kEpiGlu ? NW * 4 : NW * 8;  // rows of w between pieces
 #pragma unroll
-            for (int i = 0; i < CB; ++i) dma16(rb, ok ? bo[i] : kNowhere, lb + (i * NW + wave) * 1024);
+            for (int i = 0; i < CB; ++i) dma16(r, in_k ? bo + i * step * ldb2 : kNowhere, lb + (i * NW + wave) * 1024);
         } else {
-            const bool gat = MODE == kWgrad && p.b_gather != nullptr;
-            const i32x4 rb = gat ? make_rsrc(bbase, b_lim)
-                                 : make_rsrc(bbase + (int64_t)k * p.ldb, b_lim - (int64_t)k * ldb2);
-#pragma unroll
-            for (int i = 0; i < CB; ++i) {
-                const bool ok = k + (int)bk[i] < klen && bo[i] != kNowhere;
-                uint32_t row = bk[i];
-                if (gat) row = div_by((uint32_t)p.b_gather[ok ? k0 + k + (int)bk[i] : k0], p.b_mul, p.b_shift);
-                dma16(rb, ok ? row * ldb2 + bo[i] : kNowhere, lb + (i * NW + wave) * 1024);
-            }
+            issue_r(std::integral_constant<int, TN>{}, bbase, b_lim, bo, p.ldb, gb, p.b_gather, p.b_mul, p.b_shift, k, lb);
         }
     };
 
@@ -506,34 +486,41 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
 #pragma unroll
         for (int j = 0; j < NF; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (nk > 0) issue(0, 0);
+    if (nk > 0) issue(0);
+    if (nk > 1) issue(1);
     for (int s = 0; s < nk; ++s) {
-        wait_vm<0>();
+        if (s + 1 < nk) wait_vm<CA + CB>();
+        else wait_vm<0>();
         stage_barrier();
-        if (s + 1 < nk) issue(s + 1, (s + 1) & 1);
         const uint8_t* sa = lds[s & 1];
         const uint8_t* sb = sa + TM * 128;
+        bf16x8 av[2][MF], bv[2][NF];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 av[MF], bv[NF];
-#pragma unroll
-            for (int i = 0; i < MF; ++i) {
-                const int r0 = wm * (TM / WM) + 16 * i;
-                if constexpr (A_R) av[i] = frag_r<TM>(sa, r0, ks, lane);
-                else av[i] = frag_k(sa, r0, ks, lane);
-            }
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
                 const int r0 = wn * (TN / WN) + 16 * j;
-                if constexpr (B_R) bv[j] = frag_r<TN>(sb, r0, ks, lane);
-                else bv[j] = frag_k(sb, r0, ks, lane);
+                if constexpr (B_R) bv[ks][j] = frag_r<TN>(sb, r0, ks, lane);
+                else bv[ks][j] = frag_k(sb, r0, ks, lane);
             }
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                const int r0 = wm * (TM / WM) + 16 * i;
+                if constexpr (A_R) av[ks][i] = frag_r<TM>(sa, r0, ks, lane);
+                else av[ks][i] = frag_k(sa, r0, ks, lane);
+            }
+        }
+        if (s + 2 < nk) {
+            stage_barrier();
+            issue(s + 2);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
                 for (int j = 0; j < NF; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], av[i], acc[i][j], 0, 0, 0);
-        }
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[ks][j], av[ks][i], acc[i][j], 0, 0, 0);
     }
     Pos o;
     o.out_base = MODE == kWgrad ? (int64_t)e * p.M * p.N : 0;

@@ -28,7 +28,9 @@ __device__ __forceinline__ float act_bwd(float dout, float z) {
 }
 
 constexpr int kBwdCols = 512;  // columns of a workgroup: 64 lanes x 8
-constexpr int kBwdRows = 64;   // rows of a workgroup: 4 waves x 16
+// Rows of a workgroup, a multiple of its 4 waves: 64, or 16 where that would leave compute units without work (4091 x
+// 1024 SwiGLU: 23 us with 64, 128 workgroups; 11 with 16). Each costs one row of partial sums.
+inline int bwd_rows(int64_t M, int64_t N) { return (M / 64) * ((N + kBwdCols - 1) / kBwdCols) >= 1024 ? 64 : 16; }
 constexpr int kFoldWaves = 16; // row blocks folded side by side
 
 __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
@@ -47,20 +49,22 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
 
 // dz [M, R] = dout * act'(z) in bf16 (R = N, SwiGLU 2 N; not written when dz
 // is NULL) and, when part is not NULL, the column sums of the unrounded fp32
-// dz over this workgroup's rows: part[blockIdx.y][R]. A lane owns 8 columns
+// dz over this workgroup's rows: part[row block][R]. A lane owns 8 columns
 // and walks rows wave, wave + 4, ...; the four waves' sums are added in order
 // through LDS, so the result does not depend on timing.
 template <int ACT, bool F32>
 __global__ __launch_bounds__(256) void k_act_bwd(const void* __restrict__ dout, const uint16_t* __restrict__ z,
-                                                 int64_t M, int N, uint16_t* __restrict__ dz,
+                                                 int64_t M, int N, int rows, uint16_t* __restrict__ dz,
                                                  float* __restrict__ part) {
     constexpr bool GLU = ACT == NVQ_ACT_SWIGLU;
     constexpr int H = GLU ? 2 : 1;
     __shared__ float red[4][64 * 8 * H];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * kBwdCols + lane * 8;
+    const unsigned col_blocks = ((unsigned)N + kBwdCols - 1) / kBwdCols;
+    const int64_t rb = blockIdx.x / col_blocks;
+    const int c0 = (int)(blockIdx.x % col_blocks) * kBwdCols, c = c0 + lane * 8;
     const int64_t R = (int64_t)N * H;
-    const int64_t r0 = (int64_t)blockIdx.y * kBwdRows, r1 = min(r0 + kBwdRows, M);
+    const int64_t r0 = rb * rows, r1 = min(r0 + rows, M);
     float sum[H][8] = {};
     if (c < N) {
         for (int64_t r = r0 + wave; r < r1; r += 4) {
@@ -99,9 +103,9 @@ __global__ __launch_bounds__(256) void k_act_bwd(const void* __restrict__ dout, 
         for (int i = 0; i < 8; ++i) red[wave][h * 512 + lane * 8 + i] = sum[h][i];
     __syncthreads();
     for (int i = threadIdx.x; i < 512 * H; i += 256) {
-        const int col = blockIdx.x * kBwdCols + (i & 511);
+        const int col = c0 + (i & 511);
         if (col < N)
-            part[(int64_t)blockIdx.y * R + (int64_t)(i >> 9) * N + col] =
+            part[rb * R + (int64_t)(i >> 9) * N + col] =
                 (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
     }
 }
@@ -128,20 +132,22 @@ __global__ __launch_bounds__(64 * kFoldWaves) void k_fold_bias(const float* __re
 template <int ACT>
 void launch_act_bwd(const void* dout, bool f32, const uint16_t* z, int64_t M, int64_t N, uint16_t* dz, float* part,
                     hipStream_t s) {
-    const dim3 grid((unsigned)((N + kBwdCols - 1) / kBwdCols), (unsigned)((M + kBwdRows - 1) / kBwdRows));
-    if (f32) hipLaunchKernelGGL((k_act_bwd<ACT, true>), grid, dim3(256), 0, s, dout, z, M, (int)N, dz, part);
-    else hipLaunchKernelGGL((k_act_bwd<ACT, false>), grid, dim3(256), 0, s, dout, z, M, (int)N, dz, part);
+    const int rows = bwd_rows(M, N);
+    const dim3 grid((unsigned)((N + kBwdCols - 1) / kBwdCols * ((M + rows - 1) / rows)));
+    if (f32) hipLaunchKernelGGL((k_act_bwd<ACT, true>), grid, dim3(256), 0, s, dout, z, M, (int)N, rows, dz, part);
+    else hipLaunchKernelGGL((k_act_bwd<ACT, false>), grid, dim3(256), 0, s, dout, z, M, (int)N, rows, dz, part);
 }
 
 bool act_ok(int act) { return act >= NVQ_ACT_NONE && act <= NVQ_ACT_SWIGLU; }
 bool linear_dims_ok(int64_t M, int64_t N, int64_t K, int act) {
     const bool glu = act == NVQ_ACT_SWIGLU;
-    return gemm16_dims_ok(kFwd, glu, M, 1, 0, N, K) && M <= (int64_t)65535 * kBwdRows;
+    return gemm16_dims_ok(kFwd, glu, M, 1, 0, N, K) && M * N < ((int64_t)1 << 40);
 }
 
-size_t bwd_carve(Carver& c, int64_t M, int64_t R, uint16_t** dz, float** part) {
+size_t bwd_carve(Carver& c, int64_t M, int64_t N, int64_t R, uint16_t** dz, float** part) {
+    const int rows = bwd_rows(M, N);
     *dz = c.take<uint16_t>((size_t)(M * R));
-    *part = c.take<float>((size_t)((M + kBwdRows - 1) / kBwdRows * R));
+    *part = c.take<float>((size_t)((M + rows - 1) / rows * R));
     return c.need;
 }
 
@@ -177,8 +183,9 @@ size_t linear_act_bwd_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int a
     Carver c(nullptr);
     uint16_t* dz;
     float* part;
-    return bwd_carve(c, std::max<int64_t>(M, 0), std::max<int64_t>(N, 0) * (act == NVQ_ACT_SWIGLU ? 2 : 1), &dz,
-                     &part);
+    M = std::max<int64_t>(M, 0);
+    N = std::max<int64_t>(N, 0);
+    return bwd_carve(c, M, N, N * (act == NVQ_ACT_SWIGLU ? 2 : 1), &dz, &part);
 }
 
 int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, const uint16_t* w, const uint16_t* z,
@@ -202,7 +209,7 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
     Carver cv(ws);
     uint16_t* dz;
     float* part;
-    bwd_carve(cv, M, R, &dz, &part);
+    bwd_carve(cv, M, N, R, &dz, &part);
     // without an activation a bf16 dout is dz itself
     const bool same = act == NVQ_ACT_NONE && dout_dtype == NVQ_OUT_BF16;
     const bool need_dz = !same && (dx || dw);
@@ -222,7 +229,7 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
     }
     if (dbias)
         hipLaunchKernelGGL(k_fold_bias, dim3((unsigned)((R + 63) / 64)), dim3(64 * kFoldWaves), 0, s, part,
-                           (M + kBwdRows - 1) / kBwdRows, R, accumulate, dbias);
+                           (M + bwd_rows(M, N) - 1) / bwd_rows(M, N), R, accumulate, dbias);
     const uint16_t* dzp = same ? static_cast<const uint16_t*>(dout) : dz;
     Args p{};
     p.a = dzp;

@@ -92,7 +92,7 @@ def test_linear_refusals():
             assert fn(**{n: None}) == NULL, n
         for n in mis:
             assert fn(**{n: MIS}) == ALIGN, n
-        for bad in (dict(M=-1), dict(M=65535 * 64 + 1), dict(N=12), dict(N=0), dict(K=4), dict(K=1 << 23),
+        for bad in (dict(M=-1), dict(M=1 << 31), dict(M=1 << 30, N=1 << 11), dict(N=12), dict(N=0), dict(K=4), dict(K=1 << 23),
                     dict(N=1 << 20, K=1 << 20)):
             assert fn(**bad) == DIM, bad
         assert fn(act=6) == UNSUPPORTED and fn(act=-1) == UNSUPPORTED
