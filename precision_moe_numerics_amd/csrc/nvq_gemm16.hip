@@ -62,8 +62,9 @@ template <int MODE, int EPI, int TM, int TN, int WM, int WN>
 void run(Args p, int64_t m_tiles_cap, hipStream_t s) {
     constexpr int TNO = EPI == kEpiGlu ? TN / 2 : TN;
     p.n_tiles = (p.N + TNO - 1) / TNO;
-    const int64_t grid = m_tiles_cap * p.n_tiles;
-    hipLaunchKernelGGL((k_gemm16<MODE, EPI, TM, TN, WM, WN>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, p);
+    p.total = (int)(m_tiles_cap * p.n_tiles);
+    const unsigned grid = ((unsigned)p.total + 7u) & ~7u;  // xcd_id: whole rounds of the 8 XCDs
+    hipLaunchKernelGGL((k_gemm16<MODE, EPI, TM, TN, WM, WN>), dim3(grid), dim3(64 * WM * WN), 0, s, p);
 }
 
 // Multiplier and shift of div_by.
@@ -83,24 +84,38 @@ template <int MODE, int EPI>
 void run_big(Args p, int64_t m_tiles_cap, hipStream_t s) {
     constexpr int TNO = EPI == kEpiGlu ? kBigT / 2 : kBigT;
     p.n_tiles = (p.N + TNO - 1) / TNO;
-    const int64_t total = m_tiles_cap * p.n_tiles;
-    const int64_t grid = std::min<int64_t>(total, device_cus());
+    p.total = (int)(m_tiles_cap * p.n_tiles);
+    const unsigned grid = std::min(((unsigned)p.total + 7u) & ~7u, std::max((unsigned)device_cus() & ~7u, 8u));
     set_div((uint32_t)(kGroupM * p.n_tiles), &p.group_mul, &p.group_shift);
-    hipLaunchKernelGGL((k_gemm16_big<MODE, EPI>), dim3((unsigned)grid), dim3(64 * kBigWaves), 0, s, p, (int)total);
+    hipLaunchKernelGGL((k_gemm16_big<MODE, EPI>), dim3(grid), dim3(64 * kBigWaves), 0, s, p);
 }
 
-template <int EPI, int MB>
+template <int EPI, int MB, int KS>
 void run_skinny(Args p, hipStream_t s) {
-    p.n_tiles = EPI == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
+    constexpr int TN = (EPI == kEpiGlu ? 8 : 16) * (kSkWaves / KS);
+    p.n_tiles = (p.N + TN - 1) / TN;
     int64_t mt = (p.rows + 16 * MB - 1) / (16 * MB);
     if (p.seg) mt = std::min<int64_t>(p.rows, mt + p.E);
-    hipLaunchKernelGGL((k_gemm16_skinny<EPI, MB>), dim3((unsigned)(mt * p.n_tiles)), dim3(64 * kSkWaves), 0, s, p);
+    hipLaunchKernelGGL((k_gemm16_skinny<EPI, MB, KS>), dim3((unsigned)(mt * p.n_tiles)), dim3(64 * kSkWaves), 0, s, p);
 }
+// K in as few parts as give the chip waves enough, some 2048: a part costs its share of the sum through LDS (fc2 of 64
+// tokens, 384 experts: 522 us in 2 parts, 653 in 4, 986 in 8; 16 rows x 4096 x 4096, 256 blocks: 35, 20 and 12).
+template <int EPI, int MB>
+void run_skinny_k(const Args& p, hipStream_t s) {
+    const int64_t mt = (p.rows + 16 * MB - 1) / (16 * MB);
+    const int64_t blocks = (p.seg ? std::min<int64_t>(p.rows, mt + p.E) : mt) * ((p.N + 15) / 16);
+    if (blocks >= 1024) run_skinny<EPI, MB, 2>(p, s);
+    else if (blocks >= 512) run_skinny<EPI, MB, 4>(p, s);
+    else run_skinny<EPI, MB, 8>(p, s);
+}
+// Rows of x a workgroup takes: those of a typical expert, up to 64 where that still gives the chip workgroups (64 rows
+// x 4096 x 4096: 23 us with 64, 27 with 32; 128 x 1024 x 4096: 23 and 15).
 template <int EPI>
-void run_skinny_rows(int rows, const Args& p, hipStream_t s) {
-    if (rows <= 16) run_skinny<EPI, 1>(p, s);
-    else if (rows <= 32) run_skinny<EPI, 2>(p, s);
-    else run_skinny<EPI, 4>(p, s);
+void run_skinny_rows(const Args& p, int64_t active, hipStream_t s) {
+    const int64_t per = (p.rows + active - 1) / active, blocks = EPI == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
+    if (per <= 16) run_skinny_k<EPI, 1>(p, s);
+    else if (per > 32 && (p.rows + 63) / 64 * blocks >= 256) run_skinny_k<EPI, 4>(p, s);
+    else run_skinny_k<EPI, 2>(p, s);
 }
 
 }  // namespace g16
@@ -148,13 +163,22 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
         return;
     }
     if (p.rows == 0) return;
-    // rows that most of the experts stay within
-    const int few = p.seg ? 4 * ((p.rows + p.E - 1) / p.E) : p.rows;
-    if (mode == kFwd && few <= 64) {
-        if (epi == kEpiGlu) run_skinny_rows<kEpiGlu>(few, p, s);
-        else if (epi == kEpiAct) run_skinny_rows<kEpiAct>(few, p, s);
-        else run_skinny_rows<kEpiOut>(few, p, s);
-        return;
+    // Few tiles leave the 128 x 128 kernel with the latency of its K steps, 0.62 us each however few its workgroups; the
+    // skinny kernel's time is that of its traffic: x once per 16 rows of weights, at about 8 TB/s from the caches, and the
+    // weights once per block of rows, at about 5. (One token, 384 experts, fc1: 30 us against 47; two tokens: 60 against
+    // 50; 32 rows x 4096 x 4096: 15 against 41; 512 x 1024 x 4096: 43 against 42.)
+    if (mode == kFwd) {
+        const int64_t active = p.seg ? std::min<int64_t>(p.E, p.rows) : 1;
+        const int64_t blocks = epi == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
+        const double skinny = ((double)p.rows * blocks / 8 + (double)(active + p.rows / 64) * blocks * 16 / 5) * p.K * 2e-6;
+        const int tn = epi == kEpiGlu ? 64 : 128;
+        const double tiles = (double)(active + p.rows / 128) * ((p.N + tn - 1) / tn);
+        if (skinny < 0.62 * ((p.K + 63) / 64) * std::max(1.0, tiles / 512)) {
+            if (epi == kEpiGlu) run_skinny_rows<kEpiGlu>(p, active, s);
+            else if (epi == kEpiAct) run_skinny_rows<kEpiAct>(p, active, s);
+            else run_skinny_rows<kEpiOut>(p, active, s);
+            return;
+        }
     }
     const bool big = p.rows / p.E >= 128 && (p.rows + 255) / 256 * n_big >= cus;
     const int tm = big ? 256 : 128;

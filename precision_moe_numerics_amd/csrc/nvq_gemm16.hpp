@@ -58,7 +58,7 @@ struct Args {
     int32_t lda, ldb;         // row strides in elements
     int32_t E, rows;          // experts; logical token rows
     int32_t M, N, K;          // WGRAD: M x N outputs; FWD, DGRAD: N columns (GLU: N outputs), K
-    int32_t m_tiles, n_tiles;
+    int32_t m_tiles, n_tiles, total;  // tiles: of an expert's rows (WGRAD), of columns, in all (segments: at most)
     int32_t out_f32, accumulate, act;
 };
 
@@ -349,6 +349,15 @@ __device__ __forceinline__ uint32_t div_by(uint32_t v, uint32_t mul, int shift) 
     return shift < 0 ? v : __umulhi(v, mul) >> shift;
 }
 
+// Virtual id of a workgroup: consecutive ids on one XCD (workgroups are dealt to
+// the 8 XCDs round robin), ids 0 .. n - 1 spread over all of them. -1 where the
+// grid has more workgroups than ids.
+__device__ __forceinline__ int xcd_id(int n) {
+    const int per = (n + 7) / 8, i = (int)(blockIdx.x / 8);
+    const int v = (int)(blockIdx.x % 8) * per + i;
+    return i < per && v < n ? v : -1;
+}
+
 // ------------------------------------------------------------------ the kernel
 // Tile TM x TN, WM x WN waves; every wave holds (TM / WM) x (TN / WN) outputs
 // as 16 x 16 blocks. Two LDS stages of kBK. A step reads its whole stage into
@@ -368,9 +377,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     const int wm = wave / WN, wn = wave % WN;
     const uint32_t lds0 = lds_off(&lds[0][0]);
 
-    // consecutive virtual ids on one XCD (workgroups are dealt to the 8 XCDs round robin)
-    const int G = gridDim.x;
-    const int t = (G % 8 == 0) ? (int)((blockIdx.x % 8) * (G / 8) + blockIdx.x / 8) : (int)blockIdx.x;
+    const int t = xcd_id(MODE != kWgrad && p.tiles ? sload(p.tile_count, 0) * p.n_tiles : p.total);
+    if (t < 0) return;
     const int nt = t % p.n_tiles, mt = t / p.n_tiles;
     int e = 0, row0, row_end;  // FWD, DGRAD: token rows; WGRAD: output rows
     int k0 = 0, klen = p.K;    // WGRAD: token rows
@@ -384,7 +392,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
             klen = max(min(max(sload(p.seg, e + 1), 0), p.rows) - k0, 0);
         }
     } else if (p.tiles) {
-        if (mt >= sload(p.tile_count, 0)) return;
         e = sload(&p.tiles[mt].e, 0);
         row0 = sload(&p.tiles[mt].row0, 0);
         row_end = sload(&p.tiles[mt].row_end, 0);

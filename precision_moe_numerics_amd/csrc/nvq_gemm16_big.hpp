@@ -323,7 +323,7 @@ __device__ __forceinline__ void big_mul(f32x4 (*acc)[4], int i0, int j0, const F
 // landed; a half has six quarters, 3072 matrix cycles of the SIMD, to arrive.
 // (Ten slots, the whole LDS and eight quarters, measured no faster.)
 template <int MODE, int EPI>
-__global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p, int total_cap) {
+__global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kHalf];
     __shared__ int32_t rows_lds[kBigWaves][64];
     __shared__ __attribute__((aligned(16))) int32_t ring[kBigWaves][4][4];
@@ -334,10 +334,10 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p, int to
     const int wm = wave >> 2, wn = wave & 3;
     const uint32_t lds0 = lds_off(&lds[0]);
     const int G = gridDim.x;
-    const int v = (G % 8 == 0) ? (int)((blockIdx.x % 8) * (G / 8) + blockIdx.x / 8) : (int)blockIdx.x;
     const int m_count = MODE == kWgrad ? p.m_tiles : p.tiles ? sload(p.tile_count, 0) : (p.rows + kBigT - 1) / kBigT;
-    const int total = MODE == kWgrad ? total_cap : min(m_count * p.n_tiles, total_cap);
-    if (v >= total) return;
+    const int total = MODE == kWgrad ? p.total : m_count * p.n_tiles;
+    const int v = xcd_id(min(total, G));
+    if (v < 0) return;
 
     Load ld;
     BigWalk<MODE, EPI> lw;  // the tile after the one fetched

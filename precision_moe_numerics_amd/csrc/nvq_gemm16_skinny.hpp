@@ -7,7 +7,7 @@
 namespace nvq {
 namespace g16 {
 
-constexpr int kSkWaves = 8;   // waves of a workgroup, splitting K
+constexpr int kSkWaves = 8;   // waves of a workgroup: KS parts of K x 8 / KS blocks of weight rows
 constexpr int kSkBatch = 8;   // 32-deep steps whose loads are in flight together
 
 // Expert and first row of m-tile `t` of the segments (tm rows each), by one
@@ -49,12 +49,13 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int rows, i
     }
 }
 
-// One workgroup: 16 rows of the weights (GLU: 8 gate rows and their 8 up rows)
-// times up to 16 MB rows of one expert. Each wave takes a contiguous part of K
-// and loads both operands as MFMA fragments straight into registers, a batch of
-// steps at once, the weights past the caches (they are read once); rows of x that do not exist
-// cost no traffic. The waves' sums meet in LDS and are added in order.
-template <int EPI, int MB>
+// One workgroup: 8 / KS blocks of 16 rows of the weights (GLU: of 8 gate rows
+// and their 8 up rows) times up to 16 MB rows of one expert. Each wave takes one
+// block and a contiguous part of K and loads both operands as MFMA fragments
+// straight into registers, a batch of steps at once, the weights past the
+// caches (they are read once); rows of x that do not exist cost no traffic. The
+// sums of the KS parts meet in LDS and are added in order.
+template <int EPI, int MB, int KS>
 __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
     __shared__ float red[kSkWaves][MB][16][17];
     const int lane = threadIdx.x & 63;
@@ -62,8 +63,10 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
     const int nt = blockIdx.x % p.n_tiles, mt = blockIdx.x / p.n_tiles;
     int e = 0, row0 = mt * 16 * MB, row_end = p.rows;
     if (p.seg && !find_tile(p.seg, p.E, p.rows, 16 * MB, mt, lane, &e, &row0, &row_end)) return;
-    constexpr int TNO = EPI == kEpiGlu ? 8 : 16;
-    const int n0 = nt * TNO;
+    constexpr int TNO = EPI == kEpiGlu ? 8 : 16, NB = kSkWaves / KS;
+    const int part_k = wave % KS;
+    const int n_first = nt * TNO * NB;
+    const int n0 = n_first + wave / KS * TNO;
     const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
     const int r = lane & 15, kc = (lane >> 4) * 8;
     constexpr int rows_per = EPI == kEpiGlu ? 2 : 1;
@@ -71,7 +74,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
         const_cast<uint16_t*>(p.b + (int64_t)e * rows_per * p.N * p.ldb), 0, (int)((uint32_t)(rows_per * p.N) * ldb2),
         0x00020000);
     const int brow = EPI == kEpiGlu ? (r < 8 ? n0 + r : p.N + n0 + r - 8) : n0 + r;
-    const bool b_ok = EPI == kEpiGlu || brow < p.N;
+    const bool b_ok = n0 + (EPI == kEpiGlu ? 0 : r) < p.N;
     const uint32_t bo = (uint32_t)brow * ldb2 + kc * 2;
     const bool gat = p.a_gather != nullptr;
     const uint16_t* abase = gat ? p.a : p.a + (int64_t)row0 * p.lda;
@@ -89,13 +92,13 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
         ao[i] = src * lda2 + kc * 2;
     }
     const int steps = (p.K + 31) / 32;
-    const int part = ((steps + kSkWaves - 1) / kSkWaves + 1) & ~1;  // even: whole 128-byte lines
-    const int s_end = min((wave + 1) * part, steps);
+    const int part = ((steps + KS - 1) / KS + 1) & ~1;  // even: whole 128-byte lines
+    const int s_end = min((part_k + 1) * part, steps);
     f32x4 acc[MB];
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    for (int s0 = wave * part; s0 < s_end; s0 += kSkBatch) {
+    for (int s0 = part_k * part; s0 < s_end; s0 += kSkBatch) {
         u32x4 bv[kSkBatch], av[kSkBatch][MB];
 #pragma unroll
         for (int j = 0; j < kSkBatch; ++j) {
@@ -119,22 +122,23 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) red[wave][i][4 * (lane >> 4) + t][r] = acc[i][t];
     __syncthreads();
-    auto total = [&](int i, int n, int m) {
-        float s = red[0][i][n][m];
+    auto total = [&](int b, int i, int n, int m) {
+        float s = red[b * KS][i][n][m];
 #pragma unroll
-        for (int w = 1; w < kSkWaves; ++w) s += red[w][i][n][m];
+        for (int w = 1; w < KS; ++w) s += red[b * KS + w][i][n][m];
         return s;
     };
     auto put = [&](void* out, int64_t idx, float v, bool f32) {
         if (f32) static_cast<float*>(out)[idx] = v;
         else static_cast<uint16_t*>(out)[idx] = (uint16_t)bf16x2_rne(v, v);
     };
-    for (int u = threadIdx.x; u < MB * 16 * TNO; u += 64 * kSkWaves) {
-        const int n = u % TNO, m16 = u / TNO, i = m16 >> 4, mr = m16 & 15;
-        const int m = row0 + m16, col = n0 + n;
+    for (int u = threadIdx.x; u < MB * 16 * TNO * NB; u += 64 * kSkWaves) {
+        const int nn = u % (TNO * NB), b = nn / TNO, n = nn % TNO;
+        const int m16 = u / (TNO * NB), i = m16 >> 4, mr = m16 & 15;
+        const int m = row0 + m16, col = n_first + nn;
         if (m >= row_end || col >= p.N) continue;
         const int64_t base = (EPI == kEpiOut && p.scatter ? (int64_t)p.scatter[m] : m) * p.N;
-        float v = total(i, n, mr);
+        float v = total(b, i, n, mr);
         if (EPI == kEpiAct) {
             if (p.bias) v += p.bias[col];
             if (p.z) put(p.z, base + col, v, false);
@@ -146,7 +150,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
                 default: break;
             }
         } else if (EPI == kEpiGlu) {
-            float g = v, up = total(i, n + 8, mr);
+            float g = v, up = total(b, i, n + 8, mr);
             if (p.bias) {
                 g += p.bias[col];
                 up += p.bias[p.N + col];
