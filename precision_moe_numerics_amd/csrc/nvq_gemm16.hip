@@ -3,6 +3,7 @@
 #include "nvq_gemm16_skinny.hpp"
 
 #include <algorithm>
+#include <cmath>
 
 namespace nvq {
 namespace g16 {
@@ -146,19 +147,30 @@ bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int6
     return tile_cap(rows, E, kMinTileM) * ((N + 63) / 64) < i31;
 }
 
+// Whether 256 x 256 tiles (one persistent workgroup per CU) beat 128 x 128 ones (two workgroups per CU), by the rounds
+// that the chip makes over them. A K step of a big tile takes a CU 13 units, one of two small tiles at once 11; a CU that
+// has one small tile only, 7. Measured, small against big: 2048 x 4096 x 4096 73 us, 88; 4096^3 152, 112; 3000 x 7000 x
+// 1000 76, 62; 6000 x 6000 x 600 79, 67; fc1 of 384 experts at 4096 tokens 1326, 1413, at 8192 1909, 1490; weight
+// gradients of 270 matrices of 192 x 152 22, 42, of 384 of 4096 x 7168 1493, 1131.
+static bool big_tiles(double big, double small, int cus) {
+    const double t_small = small <= cus ? 7.0 : 11.0 * std::max(1.0, small / (2.0 * cus));
+    return 13.0 * std::max(1.0, std::ceil(big / cus)) < t_small;
+}
+
 void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
     set_div(p.a_div, &p.a_mul, &p.a_shift);
     set_div(p.b_div, &p.b_mul, &p.b_shift);
     const int64_t n_big = (p.N + (epi == kEpiGlu ? 127 : 255)) / (epi == kEpiGlu ? 128 : 256);
+    const int64_t n_small = (p.N + (epi == kEpiGlu ? 63 : 127)) / (epi == kEpiGlu ? 64 : 128);
     const int cus = device_cus();
     if (mode == kWgrad) {
-        const int64_t mb = (p.M + 255) / 256 * (int64_t)p.E;
-        if (mb * n_big >= cus) {
+        const int64_t mb = (p.M + 255) / 256 * (int64_t)p.E, ms = (p.M + 127) / 128 * (int64_t)p.E;
+        if (big_tiles((double)mb * n_big, (double)ms * n_small, cus)) {
             p.m_tiles = (p.M + 255) / 256;
             run_big<kWgrad, kEpiOut>(p, mb, s);
         } else {
             p.m_tiles = (p.M + 127) / 128;
-            run<kWgrad, kEpiOut, 128, 128, 2, 2>(p, (int64_t)p.m_tiles * p.E, s);
+            run<kWgrad, kEpiOut, 128, 128, 2, 2>(p, ms, s);
         }
         return;
     }
@@ -167,12 +179,11 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
     // skinny kernel's time is that of its traffic: x once per 16 rows of weights, at about 8 TB/s from the caches, and the
     // weights once per block of rows, at about 5. (One token, 384 experts, fc1: 30 us against 47; two tokens: 60 against
     // 50; 32 rows x 4096 x 4096: 15 against 41; 512 x 1024 x 4096: 43 against 42.)
+    const int64_t active = p.seg ? std::min<int64_t>(p.E, p.rows) : 1;
     if (mode == kFwd) {
-        const int64_t active = p.seg ? std::min<int64_t>(p.E, p.rows) : 1;
         const int64_t blocks = epi == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
         const double skinny = ((double)p.rows * blocks / 8 + (double)(active + p.rows / 64) * blocks * 16 / 5) * p.K * 2e-6;
-        const int tn = epi == kEpiGlu ? 64 : 128;
-        const double tiles = (double)(active + p.rows / 128) * ((p.N + tn - 1) / tn);
+        const double tiles = (double)(active + p.rows / 128) * n_small;
         if (skinny < 0.62 * ((p.K + 63) / 64) * std::max(1.0, tiles / 512)) {
             if (epi == kEpiGlu) run_skinny_rows<kEpiGlu>(p, active, s);
             else if (epi == kEpiAct) run_skinny_rows<kEpiAct>(p, active, s);
@@ -180,7 +191,12 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
             return;
         }
     }
-    const bool big = p.rows / p.E >= 128 && (p.rows + 255) / 256 * n_big >= cus;
+    // m-tiles: exact for one segment, half a tile more than its rows fill for a typical expert
+    auto m_tiles = [&](int tm) {
+        if (!p.seg) return (double)((p.rows + tm - 1) / tm);
+        return std::max((double)active, (double)p.rows / tm + 0.5 * active);
+    };
+    const bool big = big_tiles(m_tiles(256) * n_big, m_tiles(128) * n_small, cus);
     const int tm = big ? 256 : 128;
     int64_t mt;
     if (p.seg) {

@@ -320,7 +320,7 @@ __device__ __forceinline__ void big_mul(f32x4 (*acc)[4], int i0, int j0, const F
 // the barrier that opens quarter n its slot is free and half n + 8 is fetched
 // into it. At the barriers before quarters 3, 0 and 1, whose reads need a new
 // half, everything but the newest five halves (10 loads of the wave) has
-// landed; a half has six quarters, 3072 matrix cycles of the SIMD, to arrive.
+// landed; a half has six quarters of some 512 matrix cycles to arrive.
 // (Ten slots, the whole LDS and eight quarters, measured no faster.)
 template <int MODE, int EPI>
 __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
