@@ -269,7 +269,7 @@ def test_streams_and_graph_replays():
         assert torch.equal(y, expect[r]), f"replay {r}"
 
 
-# ------------------------------------------------------------------ sizes that take the 256 x 256 tiles
+# ------------------------------------------------------------------ many tiles
 @pytest.mark.parametrize("mode", [nvq.FWD, nvq.DGRAD])
 @pytest.mark.parametrize("lens,N,K", [([257, 0, 64, 511, 1], 16392, 72), ([700], 22008, 40), ([300, 200], 22000, 8),
                                       ([513, 129], 22016, 256), ([65, 320], 33000, 328)])
