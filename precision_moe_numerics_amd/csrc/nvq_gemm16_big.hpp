@@ -327,6 +327,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kHalf];
     __shared__ int32_t rows_lds[kBigWaves][64];
     __shared__ __attribute__((aligned(16))) int32_t ring[kBigWaves][4][4];
+    __shared__ __attribute__((aligned(16))) uint8_t row_buf[MODE == kWgrad ? kBigWaves : 1][kRowBuf];
     using Load = BigLoad<MODE, EPI>;
     constexpr int kNew = 2 * (kSlots - 3);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -421,12 +422,17 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
     big_read_a<Load::A_R>(a, lds + kHalf, 0, wave, lane);
     big_read_b<Load::B_R>(bx, lds, wave, lane);
 
+    int behind = 0;  // stores of the last tile that its loads in flight are older than (see tile)
+
     // One tile of a wave with NA active A halves (0, 1 or 2): separate loops
     // rather than a branch inside one, so that the accumulators never cross a
     // join of paths that write different parts of them. On entry a and bx hold
     // the first stage's A0 (first K half) and B0, and every load issued so far
     // has landed in this wave's view: until loads of the tile itself are needed
     // no wait is made, so that none waits for the stores of the tile before.
+    // A weight gradient's whole tile is 16 (fp32: 32) stores of each wave: the
+    // tile after it counts them in (`behind`) instead, and the loads of its
+    // first stages, whose latency would be a tenth of a tile, stay in flight.
     auto tile = [&](const BigTile& T, auto na_tag) {
         constexpr int NA = decltype(na_tag)::value;
         constexpr int RA = Load::A_R ? 8 : 4, RB = Load::B_R ? 8 : 4;  // LDS reads of half the A, all the B fragments
@@ -436,6 +442,12 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
         for (int i = 0; i < 4 * NA; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        // loads older than the newest five halves, where stores of the tile before may lie between
+        auto settled = [&](bool steady) {
+            if (steady) wait_vm<kNew>();
+            else if (MODE == kWgrad && behind == 16) wait_vm<kNew + 16>();
+            else if (MODE == kWgrad && behind == 32) wait_vm<kNew + 32>();
+        };
         auto step = [&](int s, FragB& b0, FragB& b1) {
             const uint8_t* A0 = lds + slot_of(1) * kHalf;
             const uint8_t* B1 = lds + slot_of(2) * kHalf;
@@ -443,7 +455,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
             const uint8_t* nB0 = lds + slot_of(4) * kHalf;
             const uint8_t* nA0 = lds + slot_of(5) * kHalf;
             // quarter 0
-            if (s > 1) wait_vm<kNew>();
+            settled(s > 1);
             stage_barrier();
             fetch(kB0, base, 0);
             if (NA > 0) big_read_a<Load::A_R>(a, A0, 1, wave, lane);
@@ -452,7 +464,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
             if (NA > 0) big_read_b<Load::B_R>(b1, B1, wave, lane);
             big_mul<(NA > 0), RB>(acc, 0, 0, a, b0, 1);
             // quarter 1
-            if (s > 1) wait_vm<kNew>();
+            settled(s > 1);
             stage_barrier();
             fetch(kA0, slot_of(1), 0);
             big_mul<(NA > 0), 0>(acc, 0, 2, a, b1, 0);
@@ -468,7 +480,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
             fetch(kB1, slot_of(2), 1);
             big_mul<(NA > 1), 0>(acc, 4, 2, a, b1, 1);
             // quarter 3
-            if (s > 0) wait_vm<kNew>();
+            settled(s > 0);
             stage_barrier();
             if (gat_b) eb = ld.entries(p.b_gather, ld.k + kBigK, wave);
             fetch(kA1, slot_of(3), 0);
@@ -492,7 +504,10 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
             if (s + 1 < nk) step(s + 1, by, bx);
             else bx = by;
         }
-        if (nk > 0) wait_vm<0>();
+        const bool full = T.row_end - T.row0 >= kBigT && p.N - T.col0 >= kBigT;
+        const int stays = MODE == kWgrad && full && !p.accumulate ? p.out_f32 ? 32 : 16 : 0;
+        if (!stays && (nk > 0 || behind)) wait_vm<0>();
+        behind = stays;
         if constexpr (NA > 0) {
             Pos o;
             o.out_base = MODE == kWgrad ? (int64_t)T.e * p.M * p.N : 0;
@@ -500,7 +515,12 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
             o.row_end = T.row_end;
             o.col0 = T.col0 + wn * 32;
             o.pair_step = 128;
-            epilogue<EPI>(p, acc, o, lane);
+            if constexpr (MODE == kWgrad) {
+                if (p.out_f32) epilogue_wgrad<true>(p, acc, o, row_buf[wave], full, lane);
+                else epilogue_wgrad<false>(p, acc, o, row_buf[wave], full, lane);
+            } else {
+                epilogue<EPI>(p, acc, o, lane);
+            }
         }
     };
     for (int t = v; t < total; t += G) {
