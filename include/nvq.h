@@ -446,8 +446,8 @@ int moe_grouped_gemm_nvfp4_bwd(int mode, const uint8_t* a_codes, const uint8_t* 
 /* expert forward is 4-bit). Operands are bf16, products accumulate in fp32  */
 /* and are rounded once. In all calls of this section: outputs must not      */
 /* overlap inputs or the workspace (residual == out is allowed: each element  */
-/* is read by the thread that writes it), and infinities and NaN propagate   */
-/* as in the formulas.                                                       */
+/* is read before it is written), and infinities and NaN propagate as in the  */
+/* formulas. The same call on the same values gives the same bits.            */
 /* ------------------------------------------------------------------------ */
 
 /* Products grouped by expert. Logical token rows r = 0 .. R-1 lie in expert
@@ -472,9 +472,7 @@ int moe_grouped_gemm_nvfp4_bwd(int mode, const uint8_t* a_codes, const uint8_t* 
  * checked on the host: offsets (clamped to [0, R] on the device) and gather
  * and scatter entries of rows before seg_offsets[E] (non-negative; a gathered
  * row outside its operand reads unspecified values, never memory outside the
- * operand; out_scatter entries must be rows of out, each at most once).
- * The same sums in the same order whatever the launch: results are
- * reproducible bit for bit. */
+ * operand; out_scatter entries must be rows of out, each at most once). */
 size_t moe_grouped_gemm_bf16_workspace_size(int mode, int64_t E, int64_t R);
 int moe_grouped_gemm_bf16(int mode, const uint16_t* a, int64_t a_rows, const int32_t* a_gather, int32_t a_div,
                           const uint16_t* b, int64_t b_rows, const int32_t* b_gather, int32_t b_div,

@@ -48,7 +48,8 @@ ROWS = [([3, 1, 0], 200, 136), ([5], 8200, 200), ([1] * 9 + [16], 2056, 264), ([
         ([50], 4104, 456), ([33], 8200, 8), ([175], 2280, 808), ([350], 1160, 576),
         ([63, 60], 2056, 520), ([40, 35, 50, 63], 1160, 72), ([64] * 8, 136, 64),
         ([400, 300], 1032, 456), ([1000, 0, 500], 2056, 64), (MIXED, 5512, 8), (MIXED, 5512, 64),
-        (MIXED, 5512, 136), ([2000], 8072, 40), (MIXED, 11016, 328), ([256] * 8, 4096, 256), ([257] * 8, 4104, 128)]
+        (MIXED, 5512, 136), ([2000], 8072, 40), (MIXED, 11016, 328), ([256] * 8, 4096, 256), ([257] * 8, 4104, 128),
+        ([1, 0, 2, 0] * 1024, 24, 16)]
 
 
 @pytest.mark.parametrize("mode", [nvq.FWD, nvq.DGRAD])
@@ -143,3 +144,40 @@ def test_wgrad(gather, lens, M, N):
         ref = ref + d64(start[e])
         check(acc16[e], ref, out_bound(ref, err + ref.abs() * U23, False), f"added to bf16, expert {e}")
         check(acc32[e], ref, out_bound(ref, err + ref.abs() * U23, True), f"added to fp32, expert {e}")
+
+
+# ------------------------------------------------------------------ past 32 bits
+def test_outputs_past_32_bits():
+    """40000 x 65536 outputs: rows at both ends and on both sides of element 2^31, with a residual and z."""
+    M, N, K = 40000, 65536, 8
+    x, w = rnd(41, M, K), rnd(42, N, K)
+    res = torch.zeros((M, N), dtype=BF16, device="cuda")
+    at = [0, 1, 2 ** 31 // N - 1, 2 ** 31 // N, M - 2, M - 1]
+    res[at] = rnd(43, len(at), N)
+    out, z = nvq.linear_act_bf16(x, w, residual=res, save_z=True)
+    ref, err = matmul_bound(d64(x[at]), d64(w).T)
+    check(z[at], ref, out_bound(ref, err, False), "z")
+    ref = ref + d64(res[at])
+    check(out[at], ref, out_bound(ref, err + ref.abs() * U23, False), "out")
+    del out, z, res
+    got = nvq.moe_grouped_gemm_bf16(nvq.DGRAD, x, w.T.contiguous()[None], seg_of([M]))
+    ref, err = matmul_bound(d64(x[at]), d64(w).T)
+    check(got[at], ref, out_bound(ref, err, False), "grouped")
+
+
+@pytest.mark.parametrize("N", [8, 264])
+def test_rows_past_4_gib(N):
+    """70000 x 32768 rows: the products along K and, with the last rows alone not zero, along the rows."""
+    M, K = 70000, 32768
+    x = torch.zeros((M, K), dtype=BF16, device="cuda")
+    at = [0, 65535, 65536, M - 130, M - 1]
+    x[at] = rnd(51, len(at), K)
+    w = rnd(52, N, K)
+    out = nvq.linear_act_bf16(x, w, out_dtype=F32)
+    ref, err = matmul_bound(d64(x[at]), d64(w).T)
+    check(out[at], ref, out_bound(ref, err, True), "rows")
+    dz = rnd(53, M, N)
+    dw = nvq.moe_grouped_gemm_bf16(nvq.WGRAD, dz, x, seg_of([65536, M - 65536]), out_dtype=F32)
+    for e, rows in enumerate((at[:2], at[2:])):
+        ref, err = matmul_bound(d64(dz[rows]).T, d64(x[rows]))
+        check(dw[e], ref, out_bound(ref, err, True), f"weights {e}")
