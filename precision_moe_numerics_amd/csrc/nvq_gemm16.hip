@@ -59,13 +59,21 @@ __global__ __launch_bounds__(kTabThreads) void k_tile_table(const int32_t* __res
     }
 }
 
-template <int MODE, int EPI, int TM, int TN, int WM, int WN>
+template <int MODE, int EPI, bool AHEAD>
 void run(Args p, int64_t m_tiles_cap, hipStream_t s) {
-    constexpr int TNO = EPI == kEpiGlu ? TN / 2 : TN;
+    constexpr int TNO = EPI == kEpiGlu ? 64 : 128;
     p.n_tiles = (p.N + TNO - 1) / TNO;
     p.total = (int)(m_tiles_cap * p.n_tiles);
     const unsigned grid = ((unsigned)p.total + 7u) & ~7u;  // xcd_id: whole rounds of the 8 XCDs
-    hipLaunchKernelGGL((k_gemm16<MODE, EPI, TM, TN, WM, WN>), dim3(grid), dim3(64 * WM * WN), 0, s, p);
+    hipLaunchKernelGGL((k_gemm16<MODE, EPI, 128, 128, 2, 2, AHEAD>), dim3(grid), dim3(256), 0, s, p);
+}
+// Reading a stage ahead pays where a CU has one workgroup, whose reads nothing else covers (512 x 1024 x 4096 47 us
+// without, 37 with; 2048^3 27.6, 25.3), and for the transposed reads of the gradients (dgrad of 8192 rows, 8 experts of
+// 2048 x 4096 163, 153; weight gradients within 2 %); with two forward workgroups it costs (16384 x 384 x 4096 65, 69).
+template <int EPI>
+void run_fwd(const Args& p, int64_t m_tiles_cap, bool one, hipStream_t s) {
+    if (one) run<kFwd, EPI, true>(p, m_tiles_cap, s);
+    else run<kFwd, EPI, false>(p, m_tiles_cap, s);
 }
 
 // Multiplier and shift of div_by.
@@ -170,21 +178,21 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
             run_big<kWgrad, kEpiOut>(p, mb, s);
         } else {
             p.m_tiles = (p.M + 127) / 128;
-            run<kWgrad, kEpiOut, 128, 128, 2, 2>(p, ms, s);
+            run<kWgrad, kEpiOut, true>(p, ms, s);
         }
         return;
     }
     if (p.rows == 0) return;
-    // Few tiles leave the 128 x 128 kernel with the latency of its K steps, 0.62 us each however few its workgroups; the
+    // Few tiles leave the 128 x 128 kernel with the latency of its K steps, 0.55 us each however few its workgroups; the
     // skinny kernel's time is that of its traffic: x once per 16 rows of weights, at about 8 TB/s from the caches, and the
     // weights once per block of rows, at about 5. (One token, 384 experts, fc1: 30 us against 47; two tokens: 60 against
-    // 50; 32 rows x 4096 x 4096: 15 against 41; 512 x 1024 x 4096: 43 against 42.)
+    // 50; 32 rows x 4096 x 4096: 15 against 37; 512 x 1024 x 4096: 43 against 37.)
     const int64_t active = p.seg ? std::min<int64_t>(p.E, p.rows) : 1;
     if (mode == kFwd) {
         const int64_t blocks = epi == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
         const double skinny = ((double)p.rows * blocks / 8 + (double)(active + p.rows / 64) * blocks * 16 / 5) * p.K * 2e-6;
         const double tiles = (double)(active + p.rows / 128) * n_small;
-        if (skinny < 0.62 * ((p.K + 63) / 64) * std::max(1.0, tiles / 512)) {
+        if (skinny < 0.55 * ((p.K + 63) / 64) * std::max(1.0, tiles / 512)) {
             if (epi == kEpiGlu) run_skinny_rows<kEpiGlu>(p, active, s);
             else if (epi == kEpiAct) run_skinny_rows<kEpiAct>(p, active, s);
             else run_skinny_rows<kEpiOut>(p, active, s);
@@ -218,10 +226,11 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
         else run_big<kFwd, kEpiOut>(p, mt, s);
         return;
     }
-    if (mode == kDgrad) run<kDgrad, kEpiOut, 128, 128, 2, 2>(p, mt, s);
-    else if (epi == kEpiGlu) run<kFwd, kEpiGlu, 128, 128, 2, 2>(p, mt, s);
-    else if (epi == kEpiAct) run<kFwd, kEpiAct, 128, 128, 2, 2>(p, mt, s);
-    else run<kFwd, kEpiOut, 128, 128, 2, 2>(p, mt, s);
+    const bool one = m_tiles(128) * n_small <= cus;  // tile per CU
+    if (mode == kDgrad) run<kDgrad, kEpiOut, true>(p, mt, s);
+    else if (epi == kEpiGlu) run_fwd<kEpiGlu>(p, mt, one, s);
+    else if (epi == kEpiAct) run_fwd<kEpiAct>(p, mt, one, s);
+    else run_fwd<kEpiOut>(p, mt, one, s);
 }
 
 }  // namespace nvq

@@ -421,8 +421,10 @@ __device__ __forceinline__ int xcd_id(int n) {
 // as 16 x 16 blocks. Two LDS stages of kBK. A step reads its whole stage into
 // registers first; after a barrier the stage two steps on is fetched into its
 // place, under the products of this step and all of the next. Two workgroups
-// of the 128 x 128 tile share a CU and cover each other's waits.
-template <int MODE, int EPI, int TM, int TN, int WM, int WN>
+// of the 128 x 128 tile share a CU and cover each other's waits. AHEAD: a step
+// reads the stage after its own into a second set of registers under the first
+// half of its products, and fetches the one three steps on.
+template <int MODE, int EPI, int TM, int TN, int WM, int WN, bool AHEAD>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     constexpr int NW = WM * WN;
     constexpr int MF = TM / WM / 16, NF = TN / WN / 16;
@@ -554,39 +556,86 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
 
     if (nk > 0) issue(0);
     if (nk > 1) issue(1);
-    for (int s = 0; s < nk; ++s) {
-        if (s + 1 < nk) wait_vm<CA + CB>();
-        else wait_vm<0>();
-        stage_barrier();
+    struct Frags {
+        bf16x8 a[2][MF], b[2][NF];
+    };
+    auto read = [&](Frags& f, int s) {
         const uint8_t* sa = lds[s & 1];
         const uint8_t* sb = sa + TM * 128;
-        bf16x8 av[2][MF], bv[2][NF];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
                 const int r0 = wn * (TN / WN) + 16 * j;
-                if constexpr (B_R) bv[ks][j] = frag_r<TN>(sb, r0, ks, lane);
-                else bv[ks][j] = frag_k(sb, r0, ks, lane);
+                if constexpr (B_R) f.b[ks][j] = frag_r<TN>(sb, r0, ks, lane);
+                else f.b[ks][j] = frag_k(sb, r0, ks, lane);
             }
 #pragma unroll
             for (int i = 0; i < MF; ++i) {
                 const int r0 = wm * (TM / WM) + 16 * i;
-                if constexpr (A_R) av[ks][i] = frag_r<TM>(sa, r0, ks, lane);
-                else av[ks][i] = frag_k(sa, r0, ks, lane);
+                if constexpr (A_R) f.a[ks][i] = frag_r<TM>(sa, r0, ks, lane);
+                else f.a[ks][i] = frag_k(sa, r0, ks, lane);
             }
         }
-        if (s + 2 < nk) {
-            stage_barrier();
-            issue(s + 2);
+    };
+    auto mul = [&](const Frags& f, int ks) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[ks][j], f.a[ks][i], acc[i][j], 0, 0, 0);
+    };
+    // this wave's loads of stage s have landed, those of stage s + 1 may be under way
+    auto landed = [&](int s) {
+        if (s + 1 < nk) wait_vm<CA + CB>();
+        else wait_vm<0>();
+        stage_barrier();
+    };
+    constexpr int kReads = (A_R ? 4 : 2) * MF + (B_R ? 4 : 2) * NF, kMuls = MF * NF;
+    auto step = [&](int s, const Frags& f, Frags& next) {
+        landed(s + 1);
+        read(next, s + 1);
+        mul(f, 0);
+#pragma unroll
+        for (int r = 0; r < kMuls; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x100, kReads / kMuls, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int i = 0; i < MF; ++i)
-#pragma unroll
-                for (int j = 0; j < NF; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[ks][j], av[ks][i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 3 < nk) {
+            stage_barrier();
+            issue(s + 3);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        mul(f, 1);
+    };
+    if constexpr (!AHEAD) {
+        for (int s = 0; s < nk; ++s) {
+            Frags f;
+            landed(s);
+            read(f, s);
+            if (s + 2 < nk) {
+                stage_barrier();
+                issue(s + 2);
+            }
+            mul(f, 0);
+            mul(f, 1);
+        }
+    } else if (nk > 0) {
+        Frags x, y;
+        landed(0);
+        read(x, 0);
+        if (nk > 2) {
+            stage_barrier();
+            issue(2);
+        }
+        for (int s = 0; s + 1 < nk; s += 2) {
+            step(s, x, y);
+            if (s + 2 < nk) step(s + 1, y, x);
+            else x = y;
+        }
+        mul(x, 0);
+        mul(x, 1);
     }
     Pos o;
     o.out_base = MODE == kWgrad ? (int64_t)e * p.M * p.N : 0;
