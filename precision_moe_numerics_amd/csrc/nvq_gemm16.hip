@@ -68,12 +68,12 @@ void run(Args p, int64_t m_tiles_cap, hipStream_t s) {
     hipLaunchKernelGGL((k_gemm16<MODE, EPI, 128, 128, 2, 2, AHEAD>), dim3(grid), dim3(256), 0, s, p);
 }
 // Reading a stage ahead pays where a CU has one workgroup, whose reads nothing else covers (512 x 1024 x 4096 47 us
-// without, 37 with; 2048^3 27.6, 25.3), and for the transposed reads of the gradients (dgrad of 8192 rows, 8 experts of
-// 2048 x 4096 163, 153; weight gradients within 2 %); with two forward workgroups it costs (16384 x 384 x 4096 65, 69).
-template <int EPI>
-void run_fwd(const Args& p, int64_t m_tiles_cap, bool one, hipStream_t s) {
-    if (one) run<kFwd, EPI, true>(p, m_tiles_cap, s);
-    else run<kFwd, EPI, false>(p, m_tiles_cap, s);
+// without, 37 with; 2048^3 27.6, 25.3); with two it costs (16384 x 384 x 4096 65, 69; the weight gradient of 4091 x 2048
+// x 4096 74, 78), but for the transposed reads of dgrad (8192 rows, 8 experts of 2048 x 4096 163, 153).
+template <int MODE, int EPI>
+void run_ahead(const Args& p, int64_t m_tiles_cap, bool one, hipStream_t s) {
+    if (one) run<MODE, EPI, true>(p, m_tiles_cap, s);
+    else run<MODE, EPI, false>(p, m_tiles_cap, s);
 }
 
 // Multiplier and shift of div_by.
@@ -178,7 +178,7 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
             run_big<kWgrad, kEpiOut>(p, mb, s);
         } else {
             p.m_tiles = (p.M + 127) / 128;
-            run<kWgrad, kEpiOut, true>(p, ms, s);
+            run_ahead<kWgrad, kEpiOut>(p, ms, ms * n_small <= cus, s);
         }
         return;
     }
@@ -228,9 +228,9 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
     }
     const bool one = m_tiles(128) * n_small <= cus;  // tile per CU
     if (mode == kDgrad) run<kDgrad, kEpiOut, true>(p, mt, s);
-    else if (epi == kEpiGlu) run_fwd<kEpiGlu>(p, mt, one, s);
-    else if (epi == kEpiAct) run_fwd<kEpiAct>(p, mt, one, s);
-    else run_fwd<kEpiOut>(p, mt, one, s);
+    else if (epi == kEpiGlu) run_ahead<kFwd, kEpiGlu>(p, mt, one, s);
+    else if (epi == kEpiAct) run_ahead<kFwd, kEpiAct>(p, mt, one, s);
+    else run_ahead<kFwd, kEpiOut>(p, mt, one, s);
 }
 
 }  // namespace nvq

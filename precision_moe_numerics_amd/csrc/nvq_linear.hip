@@ -29,7 +29,7 @@ __device__ __forceinline__ float act_bwd(float dout, float z) {
 
 constexpr int kBwdCols = 512;  // columns of a workgroup: 64 lanes x 8
 // Rows of a workgroup, a multiple of its 4 waves: 64, or 16 where that would leave compute units without work (4091 x
-// 1024 SwiGLU: 23 us with 64, 128 workgroups; 11 with 16). Each costs one row of partial sums.
+// 1024 SwiGLU: 23 us with 64, 128 workgroups; 10 with 16). Each costs one row of partial sums.
 inline int bwd_rows(int64_t M, int64_t N) { return (M / 64) * ((N + kBwdCols - 1) / kBwdCols) >= 1024 ? 64 : 16; }
 constexpr int kFoldWaves = 16; // row blocks folded side by side
 
@@ -119,8 +119,10 @@ __global__ __launch_bounds__(64 * kFoldWaves) void k_fold_bias(const float* __re
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float s = 0.0f;
-    if (c < R)
+    if (c < R) {
+#pragma unroll 8
         for (int64_t b = wave; b < nb; b += kFoldWaves) s += part[b * R + c];
+    }
     red[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || c >= R) return;
