@@ -181,3 +181,33 @@ def test_rows_past_4_gib(N):
     for e, rows in enumerate((at[:2], at[2:])):
         ref, err = matmul_bound(d64(dz[rows]).T, d64(x[rows]))
         check(dw[e], ref, out_bound(ref, err, True), f"weights {e}")
+
+
+def test_many_tiles_replayed_as_a_graph():
+    """Products of many tiles, their tile tables in one workspace, captured once; replays on other rows and segments,
+    with eager calls between them, equal the eager results."""
+    N, d, E = 5512, 72, len(MIXED)
+    R = sum(MIXED)
+    w, lw = rnd(61, E, N, d), rnd(62, 2000, d)
+    xs, gs = [rnd(63 + i, R, d) for i in range(2)], [rnd(65 + i, R, N) for i in range(2)]
+    segs = [seg_of(MIXED), seg_of(MIXED[::-1])]
+
+    def layer(x, g, seg, ws=None):
+        return (nvq.moe_grouped_gemm_bf16(nvq.FWD, x, w, seg, ws=ws), nvq.moe_grouped_gemm_bf16(nvq.DGRAD, g, w, seg, ws=ws),
+                nvq.moe_grouped_gemm_bf16(nvq.WGRAD, g, x, seg, ws=ws), nvq.linear_act_bf16(x, lw, act=GELU))
+
+    expect = [layer(*a) for a in zip(xs, gs, segs)]
+    x, g, seg = xs[0].clone(), gs[0].clone(), segs[0].clone()
+    size = int(nvq.lib().moe_grouped_gemm_bf16_workspace_size(nvq.FWD, E, R))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(x, g, seg, ws)
+    for r in (0, 1, 1, 0):
+        x.copy_(xs[r]); g.copy_(gs[r]); seg.copy_(segs[r]); ws.fill_(255)
+        again = layer(xs[1 - r], gs[1 - r], segs[1 - r])
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref, other, eager in zip(out, expect[r], again, expect[1 - r]):
+            assert torch.equal(got, ref) and torch.equal(other, eager), f"replay {r}"
