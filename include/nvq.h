@@ -447,7 +447,10 @@ int moe_grouped_gemm_nvfp4_bwd(int mode, const uint8_t* a_codes, const uint8_t* 
 /* and are rounded once. In all calls of this section: outputs must not      */
 /* overlap inputs or the workspace (residual == out is allowed: each element  */
 /* is read before it is written), and infinities and NaN propagate as in the  */
-/* formulas. The same call on the same values gives the same bits.            */
+/* formulas. The same call on the same values gives the same bits. Sizes whose */
+/* launch would hold 2^32 work-items are refused (NVQ_ERR_DIM): T * C / 8 for */
+/* the combine; 64 T, past C = 1024 256 T, for its backward; 64 T for the     */
+/* routers' backward; 4 M ceil(N / 512) for the linear backward.             */
 /* ------------------------------------------------------------------------ */
 
 /* Products grouped by expert. Logical token rows r = 0 .. R-1 lie in expert
@@ -468,7 +471,8 @@ int moe_grouped_gemm_nvfp4_bwd(int mode, const uint8_t* a_codes, const uint8_t* 
  * NVQ_OUT_F32. accumulate and b_gather need WGRAD, out_scatter FWD or DGRAD
  * (else NVQ_ERR_UNSUPPORTED). Limits (else NVQ_ERR_DIM): M, N, K multiples of
  * 8 up to 2^22, E <= 4096, R < 2^31 - 256, one expert's weights and the whole
- * of a gathered operand below 4 GiB - 512, output tiles below 2^31. Not
+ * of a gathered operand below 4 GiB - 512, output tiles (128 x 128, SwiGLU
+ * 128 x 64) below 2^24. Not
  * checked on the host: offsets (clamped to [0, R] on the device) and gather
  * and scatter entries of rows before seg_offsets[E] (non-negative; a gathered
  * row outside its operand reads unspecified values, never memory outside the

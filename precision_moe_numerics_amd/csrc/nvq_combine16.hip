@@ -218,17 +218,18 @@ void launch_router_bwd(const float* w, const float* logits, const int32_t* ids, 
 }
 
 // The rows of y that one workgroup addresses from its descriptor's base (the
-// tokens its 256 threads touch) below 4 GiB, and a 31-bit grid.
+// tokens its 256 threads touch) below 4 GiB.
 bool combine_dims_ok(int64_t T, int k, int64_t C, int64_t E, bool ids) {
     const int64_t i31 = (int64_t)1 << 31;
     if (T < 0 || T >= i31 || k < 1 || k > 1024 || C < 8 || C % 8 != 0 || C > (1 << 20) || (ids && (E < 1 || E >= i31)))
         return false;
     if (T * k >= i31 || (int64_t)k * (256 + 2 * (C / 8)) * 16 > (int64_t)kNowhere) return false;
-    return (T * (C / 8) + 255) / 256 < i31;
+    return true;
 }
 
 bool router_dims_ok(int64_t T, int64_t E, int k) {
-    return T >= 0 && k >= 1 && E >= 1 && k <= E && k <= 64 && E <= 1024 && T * E < ((int64_t)1 << 31);
+    return T >= 0 && k >= 1 && E >= 1 && k <= E && k <= 64 && E <= 1024 && T * E < ((int64_t)1 << 31) &&
+           grid_ok((T + 3) / 4, 256);
 }
 
 }  // namespace
@@ -246,6 +247,7 @@ int moe_combine_bf16(const uint16_t* y, const float* w, const int32_t* topk_ids,
     if (T == 0) return NVQ_OK;
     const int C8 = (int)(C / 8);
     const int64_t grid = (T * C8 + 255) / 256;
+    if (!grid_ok(grid, 256)) return NVQ_ERR_DIM;
     hipLaunchKernelGGL(k_combine16, dim3((unsigned)grid), dim3(256), 0, as_stream(stream), y, w, topk_ids, (int)E,
                        residual, T, k, C8, out);
     return launch_status();
@@ -258,6 +260,7 @@ int moe_combine_bwd_bf16(const uint16_t* dout, const uint16_t* y, const float* w
     if (!aligned16(dout) || !aligned16(y) || !aligned16(dy)) return NVQ_ERR_ALIGN;
     if (T == 0) return NVQ_OK;
     const int C8 = (int)(C / 8);
+    if (!grid_ok(C8 <= 128 ? (T + 3) / 4 : T, 256)) return NVQ_ERR_DIM;
     hipStream_t s = as_stream(stream);
     if (C8 <= 128)
         hipLaunchKernelGGL(k_combine16_bwd<1>, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, s, dout, y, w, topk_ids,

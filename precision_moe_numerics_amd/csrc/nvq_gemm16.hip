@@ -147,12 +147,13 @@ bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int6
     if (rows < 0 || rows >= i31 - 256 || E < 1 || E > kMaxE || N < 8 || N % 8 != 0 || N > (1 << 22)) return false;
     if (mode == kWgrad) {
         if (M < 8 || M % 8 != 0 || M > (1 << 22)) return false;
-        return E * ((M + 127) / 128) * ((N + 127) / 128) < i31;
+        return grid_ok(E * ((M + 127) / 128) * ((N + 127) / 128) + 8, 256);
     }
     if (K < 8 || K % 8 != 0 || K > (1 << 22)) return false;
     // one expert's weights are one buffer descriptor
     if ((glu ? 2 : 1) * N * K * 2 > kMaxBytes) return false;
-    return tile_cap(rows, E, kMinTileM) * ((N + 63) / 64) < i31;
+    const int tn = glu ? 64 : 128;
+    return grid_ok(tile_cap(rows, E, kMinTileM) * ((N + tn - 1) / tn) + 8, 256);
 }
 
 // Whether 256 x 256 tiles (one persistent workgroup per CU) beat 128 x 128 ones (two workgroups per CU), by the rounds
@@ -192,7 +193,8 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
         const int64_t blocks = epi == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
         const double skinny = ((double)p.rows * blocks / 8 + (double)(active + p.rows / 64) * blocks * 16 / 5) * p.K * 2e-6;
         const double tiles = (double)(active + p.rows / 128) * n_small;
-        if (skinny < 0.55 * ((p.K + 63) / 64) * std::max(1.0, tiles / 512)) {
+        // (its workgroups are at most five per tile: the bound keeps a launch below 2^32 work-items)
+        if (tiles < (1 << 18) && skinny < 0.55 * ((p.K + 63) / 64) * std::max(1.0, tiles / 512)) {
             if (epi == kEpiGlu) run_skinny_rows<kEpiGlu>(p, active, s);
             else if (epi == kEpiAct) run_skinny_rows<kEpiAct>(p, active, s);
             else run_skinny_rows<kEpiOut>(p, active, s);

@@ -26,6 +26,9 @@ inline int device_cus() {
     return cus;
 }
 
+// A launch must hold fewer than 2^32 work-items.
+inline bool grid_ok(int64_t blocks, int64_t threads) { return blocks < ((int64_t)1 << 32) / threads; }
+
 // Workgroups of 256 threads of `kernel` that one CU holds at once (from its
 // register and LDS use), at least 1.
 inline int resident_blocks(const void* kernel) {

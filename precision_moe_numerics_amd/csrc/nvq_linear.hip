@@ -199,7 +199,8 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
     const bool glu = act == NVQ_ACT_SWIGLU;
     const int64_t R = glu ? 2 * N : N;
     if (!linear_dims_ok(M, N, K, act) || !gemm16_dims_ok(kDgrad, false, M, 1, 0, K, R) ||
-        !gemm16_dims_ok(kWgrad, false, M, 1, R, K, 0))
+        !gemm16_dims_ok(kWgrad, false, M, 1, R, K, 0) ||
+        !grid_ok((N + kBwdCols - 1) / kBwdCols * ((M + bwd_rows(M, N) - 1) / bwd_rows(M, N)), 256))
         return NVQ_ERR_DIM;
     if (!ws || (!dx && !dw && !dbias) || (dx && !w)) return NVQ_ERR_NULL;
     if (M > 0 && (!dout || (dw && !x) || (act != NVQ_ACT_NONE && !z))) return NVQ_ERR_NULL;

@@ -127,6 +127,23 @@ def test_combine_and_router_refusals():
         assert fn(0, 8, 2) == OK
 
 
+def test_launches_of_2_to_the_32_work_items_are_refused():
+    """Sizes within every other limit; the sizes below them are not run here, only refused for a missing operand."""
+    L = nvq.lib()
+    assert L.linear_act_bf16(_p(0), _p(1), None, None, (1 << 31) - 512, 8, 8, 0, _p(2), 0, None, None) == DIM
+    assert L.linear_act_bf16(None, _p(1), None, None, 1 << 30, 8, 8, 0, _p(2), 0, None, None) == NULL
+    assert gemm(mode=nvq.WGRAD, a=None, R=64, M=1 << 22, N=1 << 22, E=1) == DIM
+    assert gemm(mode=nvq.FWD, a=None, R=1 << 30, N=1 << 10, E=1, a_rows=1 << 30) == DIM
+    for T, C in ((1 << 24, 1 << 11), (1 << 16, 1 << 19)):
+        assert L.moe_combine_bf16(_p(0), _p(1), None, 0, None, T, 1, C, _p(2), None) == DIM
+        assert L.moe_combine_bf16(None, _p(1), None, 0, None, T // 2, 1, C, _p(2), None) == NULL
+    for T, C in ((1 << 26, 64), (1 << 24, 2048)):
+        assert L.moe_combine_bwd_bf16(_p(0), _p(1), _p(2), None, 0, T, 1, C, _p(3), _p(4), None) == DIM
+    assert L.moe_router_softmax_topk_bwd(_p(0), _p(1), _p(2), 1 << 26, 8, 2, _p(3), None) == DIM
+    assert L.linear_act_bwd_bf16(_p(0), 0, _p(1), _p(2), _p(3), 1 << 30, 8, 8, 4, _p(4), None, 1, 0, None, _p(7), BIG,
+                                 None) == DIM
+
+
 def test_the_binding_refuses_host_tensors_and_wrong_arguments():
     x, w = torch.zeros((8, 64), dtype=torch.bfloat16), torch.zeros((64, 64), dtype=torch.bfloat16)
     seg = torch.zeros(2, dtype=torch.int32)
