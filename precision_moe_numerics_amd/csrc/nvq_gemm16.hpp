@@ -157,7 +157,7 @@ __device__ __forceinline__ bf16x8 frag_r(const uint8_t* st, int r0, int ks, int 
 __device__ __forceinline__ float sigmoidf(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 // erfc(x) for x >= 0 by Abramowitz and Stegun 7.1.28, 1 / (1 + a1 x + .. + a6 x^6)^16, within 3e-7; here of
 // x = |v| / sqrt(2), the powers of which are in the coefficients: far below half a step of a bf16 output, and
-// short beside an erff to the last ulp. gelu(v) = max(v, 0) - |v| erfc / 2.
+// short beside an erff to the last ulp.
 __device__ __forceinline__ float erfc_sqrt2(float v) {
     const float x = fabsf(v);
     float q = __builtin_fmaf(0.0000430638f / 8.0f, x, 0.0002765672f * 0.17677669529663688f);
@@ -171,8 +171,10 @@ __device__ __forceinline__ float erfc_sqrt2(float v) {
     r *= r;
     return r * r;
 }
+// v Phi(v). For v > 0 the tail is taken from 1 before the product: v - v (1 - Phi(v)) would be inf - inf * 0 at inf.
 __device__ __forceinline__ float gelu_erf(float v) {
-    return __builtin_fmaf(-0.5f * fabsf(v), erfc_sqrt2(v), v > 0.0f ? v : v != v ? v : 0.0f);
+    const float tail = 0.5f * erfc_sqrt2(v);
+    return v * (v > 0.0f ? 1.0f - tail : tail);
 }
 // 0.5 (1 + tanh(t)) = sigmoid(2 t)
 __device__ __forceinline__ float gelu_tanh(float v) {
