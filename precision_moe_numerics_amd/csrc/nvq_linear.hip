@@ -13,9 +13,10 @@ using namespace g16;
 template <int ACT>
 __device__ __forceinline__ float act_bwd(float dout, float z) {
     if (ACT == NVQ_ACT_RELU) return z > 0.0f ? dout : 0.0f;
-    if (ACT == NVQ_ACT_GELU)
-        return dout * ((z > 0.0f ? __builtin_fmaf(-0.5f, erfc_sqrt2(z), 1.0f) : 0.5f * erfc_sqrt2(z)) +
-                       z * (0.39894228040143268f * __expf(-0.5f * z * z)));
+    if (ACT == NVQ_ACT_GELU) {
+        const NormTail n(z);
+        return dout * (n.phi(z) + z * (0.39894228040143268f * n.e));
+    }
     if (ACT == NVQ_ACT_GELU_TANH) {
         const float q = sigmoidf(1.5957691216057308f * (z + 0.044715f * z * z * z));
         return dout * (q + z * q * (1.0f - q) * 1.5957691216057308f * (1.0f + 0.134145f * z * z));

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import precision_moe_numerics_amd as nvq
-from bf16_ref import GELU, GELU_TANH, NONE, RELU, SILU, SWIGLU, act_ref, d64
+from bf16_ref import GELU, GELU_TANH, NONE, RELU, SILU, SWIGLU, act_ref, check
 from gpu_util import require_gpu
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +49,82 @@ def test_infinite_and_nan_pre_activations(M, N, K, act, dtype):
     assert torch.equal(got.isnan(), ref.isnan())
     assert torch.equal(got.isinf(), ref.isinf())
     assert torch.equal(got[got.isinf()].double(), ref[ref.isinf()])
+
+
+# Relative errors of the fp32 forms, in u = 2^-23. An exponential's argument a is rounded a few times (tanh GELU: eight,
+# of 2^-24 each; else at most two), which moves the result by that part of |a|; the reciprocal, the exponential, the
+# products and the polynomial of Phi (fitted to 1e-7, nine steps) stay within 16 u, a derivative's further products within
+# 24 u of its terms taken absolutely. Results and factors below 2^-126 may be flushed.
+U = 2.0 ** -23
+
+
+def tail_ref(z, act, n):
+    """act_ref with the two GELU forms written without a difference: Phi(z) = erfc(-z / sqrt(2)) / 2 and, by the sigmoid,
+    0.5 (1 + tanh v) = sigmoid(2 v). In 64 bits ndtr and 1 + tanh(v) are off by 2^-53 absolutely, which leaves them no
+    digits where they are 1e-17."""
+    if act == GELU:
+        phi = torch.special.erfc(-z * 0.5 ** 0.5) / 2
+        return z * phi, (phi + z * torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5,)
+    if act == GELU_TANH:
+        a = 2 * (2 / torch.pi) ** 0.5
+        v = a * (z + 0.044715 * z ** 3)
+        q, p = torch.sigmoid(v), torch.sigmoid(-v)
+        return z * q, (q + z * q * p * a * (1 + 3 * 0.044715 * z * z),)
+    return act_ref(z, act, n)
+
+
+def argument(z, act):
+    if act == GELU:
+        return z * z / 2
+    return 4 * (1.6 * z.abs() + 0.0715 * z.abs() ** 3) if act == GELU_TANH else z.abs()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", KERNELS)
+def test_values_relative_to_themselves(M, N, K, act, dtype):
+    """Pre-activations over [-10, 10], every 1/400: tails as exact as the rest."""
+    vals = torch.linspace(-10, 10, 8001, dtype=F32)[torch.randperm(8001, generator=torch.Generator().manual_seed(1))]
+    vals = vals[vals != 0]
+    for part in vals.split(N):
+        got, z = act_of(part, torch.full_like(part, 3.0), act, M, N, K, dtype)
+        ref = tail_ref(z, act, N)[0][0]
+        err = (argument(z[0, :N], act) + 16) * U * ref.abs() + 2.0 ** -120
+        if act in (NONE, RELU):
+            err = torch.zeros_like(ref)  # a bias and zeros
+        check(got, ref, err + (2.0 ** -8 * (ref.abs() + err) if dtype is BF16 else 0.0), "value")
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gradients_relative_to_their_terms(act):
+    """The pre-activation's gradient at every bf16 z with 2^-8 <= |z| <= 10: in fp32 as the bias gradient of one row, in
+    bf16 as dx through the identity."""
+    z = torch.arange(0x3B80, 0x4121, dtype=torch.int32).to(torch.int16).view(BF16)
+    z = torch.cat([z, -z])[:2 * (z.numel() // 8 * 8)]
+    N = z.numel() // 8 * 8
+    z = z[:N]
+    full = torch.cat([z, torch.full_like(z, 3.0)]) if act == SWIGLU else z
+    dout = torch.full((1, N), 0.75, dtype=BF16, device="cuda")
+    eye = torch.eye(full.numel(), dtype=BF16, device="cuda")
+    dx, _, db = nvq.linear_act_bwd_bf16(dout, torch.zeros((1, full.numel()), dtype=BF16, device="cuda"), eye,
+                                        z=full[None].cuda() if act != NONE else None, act=act, need_dw=False, need_dbias=True)
+    z64 = full.double()[None]
+    parts = tail_ref(z64, act, N)[1]
+    ref = 0.75 * torch.cat([p.expand(1, N) for p in parts], 1)
+    g = z64[:, :N]
+    s = torch.sigmoid(g)
+    if act in (NONE, RELU):
+        terms = torch.zeros_like(g)
+    elif act == GELU:
+        terms = torch.special.erfc(-g * 0.5 ** 0.5) / 2 + g.abs() * torch.exp(-g * g / 2) / (2 * torch.pi) ** 0.5
+    elif act == GELU_TANH:
+        q = torch.sigmoid(2 * (2 / torch.pi) ** 0.5 * (g + 0.044715 * g ** 3))
+        terms = q * (1 + 1.6 * g.abs() * (1 + 0.135 * g * g))
+    elif act == SILU:
+        terms = s * (1 + g.abs())
+    else:
+        terms = torch.cat([3 * s * (1 + g.abs()), g.abs() * s], 1)
+    a = torch.cat([argument(g, act)] * (2 if act == SWIGLU else 1), 1)
+    err = 0.75 * terms * (a + 24) * U + 2.0 ** -120
+    check(db[None], ref, err, "fp32")
+    check(dx, ref, err + 2.0 ** -8 * (ref.abs() + err), "bf16")
