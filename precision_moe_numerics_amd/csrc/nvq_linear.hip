@@ -19,7 +19,8 @@ __device__ __forceinline__ float act_bwd(float dout, float z) {
     }
     if (ACT == NVQ_ACT_GELU_TANH) {
         const float q = sigmoidf(1.5957691216057308f * (z + 0.044715f * z * z * z));
-        return dout * (q + z * q * (1.0f - q) * 1.5957691216057308f * (1.0f + 0.134145f * z * z));
+        // (past |z| = 2^64 the square would be inf, times q (1 - q) = 0)
+        return dout * (q + z * q * (1.0f - q) * 1.5957691216057308f * (1.0f + 0.134145f * fminf(z * z, 1e30f)));
     }
     if (ACT == NVQ_ACT_SILU) {
         const float s = sigmoidf(z);

@@ -128,3 +128,30 @@ def test_gradients_relative_to_their_terms(act):
     err = 0.75 * terms * (a + 24) * U + 2.0 ** -120
     check(db[None], ref, err, "fp32")
     check(dx, ref, err + 2.0 ** -8 * (ref.abs() + err), "bf16")
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_values_and_gradients_of_huge_pre_activations(act):
+    """Every power of two up to 2^127 with both signs: finite, and what the formulas give (past |z| = 100 exactly z or 0,
+    and dout or 0)."""
+    p = 2.0 ** torch.arange(4, 128, dtype=torch.float64)
+    z = torch.cat([p, -p]).to(BF16)
+    N = z.numel()
+    got, z64 = act_of(z.float(), torch.ones(N), act, 5, N, 8, F32)
+    g = z64[:, :N]
+    ref, parts = tail_ref(z64, act, N)
+    # of a positive argument past 40 only that it is past 40 matters
+    a = argument(g, act)
+    err = (torch.where(g > 0, a.clamp_max(40.0), a.clamp_max(1e6)) + 24) * U
+    check(got[None], ref, err * ref.abs() + 2.0 ** -110, "value")
+    full = z64.to(BF16).cuda()
+    rows = full.shape[1]
+    dx, _, db = nvq.linear_act_bwd_bf16(torch.full((1, N), 0.75, dtype=BF16, device="cuda"),
+                                        torch.zeros((1, 8), dtype=BF16, device="cuda"),
+                                        torch.zeros((rows, 8), dtype=BF16, device="cuda"),
+                                        z=full if act != NONE else None, act=act, need_dw=False, need_dbias=True)
+    ref = 0.75 * torch.cat([q.expand(1, N) for q in parts], 1)
+    # (the terms of a derivative are at most 1 + argument times its sigmoid or tail, and cancel by less than that)
+    slack = torch.cat([err * (1 + torch.where(g < 0, a.clamp_max(1e6), 0.0))] * len(parts), 1)
+    check(db[None], ref, slack * ref.abs() + 2.0 ** -100, "gradient")
+    assert (dx == 0).all()
