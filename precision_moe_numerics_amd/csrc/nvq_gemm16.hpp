@@ -507,6 +507,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
         b_lim = gb ? p.b_bytes : (int64_t)klen * ldb2;
         bo = (col0 + col_r(TN)) * 2 + (gb ? 0 : row_r(TN, 0) * ldb2);
     }
+    if (MODE == kWgrad && p.accumulate && klen == 0) return;  // old + 0 would turn -0 into +0
     const int nk = (klen + kBK - 1) / kBK;
     // K-strided pieces: by row number, or through a gather (its entries by scalar loads)
     auto issue_r = [&](auto R_tag, const uint16_t* base, int64_t lim, uint32_t o, int ld, bool gat,

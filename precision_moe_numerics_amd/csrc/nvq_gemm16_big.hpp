@@ -528,6 +528,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
         if (MODE == kWgrad) {
             T = cw.get(p);
             cw.next(p, G, total, m_count);
+            if (p.accumulate && T.klen == 0) continue;  // old + 0 would turn -0 into +0
         } else {
             const int32_t* q = ring[wave][popped++ & 3];
             T.row0 = __builtin_amdgcn_readfirstlane(q[0]);

@@ -232,7 +232,7 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
         }
         NVQ_CHECK_LAUNCH();
     }
-    if (dbias)
+    if (dbias && (M > 0 || !accumulate))  // (no rows add nothing: old + 0 would turn -0 into +0)
         hipLaunchKernelGGL(k_fold_bias, dim3((unsigned)((R + 63) / 64)), dim3(64 * kFoldWaves), 0, s, part,
                            (M + bwd_rows(M, N) - 1) / bwd_rows(M, N), R, accumulate, dbias);
     const uint16_t* dzp = same ? static_cast<const uint16_t*>(dout) : dz;

@@ -155,3 +155,32 @@ def test_values_and_gradients_of_huge_pre_activations(act):
     slack = torch.cat([err * (1 + torch.where(g < 0, a.clamp_max(1e6), 0.0))] * len(parts), 1)
     check(db[None], ref, slack * ref.abs() + 2.0 ** -100, "gradient")
     assert (dx == 0).all()
+
+
+# ------------------------------------------------------------------ nothing to add, nothing to do
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens,M,N", [([0, 5, 0], 264, 136), ([0, 40] * 40, 1032, 1544)])
+def test_accumulating_nothing_keeps_every_bit(lens, M, N, dtype):
+    """An empty segment leaves its matrix as it was: -0 stays -0 (adding a sum of 0 would make it +0), NaN payloads stay.
+    The two sizes take 128 x 128 and 256 x 256 tiles."""
+    off = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    R, E = sum(lens), len(lens)
+    g = torch.Generator().manual_seed(3)
+    a, b = (torch.randn((R, c), generator=g).to(BF16).cuda() for c in (M, N))
+    out = torch.full((E, M, N), -0.0, dtype=dtype, device="cuda")
+    out[0, 0, :4] = NAN
+    raw = out.view(torch.int16 if dtype is BF16 else torch.int32)
+    raw[0, 1, :4] = raw[0, 0, :4] + 1
+    before = raw.clone()
+    nvq.moe_grouped_gemm_bf16(nvq.WGRAD, a, b, off, out=out, accumulate=True)
+    empty = torch.tensor([n == 0 for n in lens], device="cuda")
+    assert torch.equal(raw[empty], before[empty])
+    assert (out[~empty].abs().amax((1, 2)) > 0).all()
+
+
+def test_accumulating_no_rows_keeps_every_bit():
+    """The dense form: no rows add nothing to dw and dbias."""
+    x, w = torch.zeros((0, 64), dtype=BF16, device="cuda"), torch.zeros((72, 64), dtype=BF16, device="cuda")
+    dw, db = torch.full((72, 64), -0.0, device="cuda"), torch.full((72,), -0.0, device="cuda")
+    nvq.linear_act_bwd_bf16(torch.zeros((0, 72), dtype=BF16, device="cuda"), x, w, dw=dw, dbias=db, accumulate=True)
+    assert (dw.view(torch.int32) == -2 ** 31).all() and (db.view(torch.int32) == -2 ** 31).all()
