@@ -127,7 +127,7 @@ int moe_expert_fwd_bf16(const uint16_t* x, int64_t T, int64_t d, const int32_t* 
     nvq_moe_buffers m{};
     Carver need(nullptr);
     if (ws_bytes < fwd16_carve(need, T, k, E, d_ff, bufs, &rws, &gws, &m)) return NVQ_ERR_WORKSPACE;
-    if (T == 0) return NVQ_OK;
+    if (T == 0 && !(bufs && bufs->offsets)) return NVQ_OK;  // (a caller's offsets become all 0, by the routing)
     Carver cv(ws);
     fwd16_carve(cv, T, k, E, d_ff, bufs, &rws, &gws, &m);
     hipStream_t s = as_stream(stream);

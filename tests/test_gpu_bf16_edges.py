@@ -184,3 +184,21 @@ def test_accumulating_no_rows_keeps_every_bit():
     dw, db = torch.full((72, 64), -0.0, device="cuda"), torch.full((72,), -0.0, device="cuda")
     nvq.linear_act_bwd_bf16(torch.zeros((0, 72), dtype=BF16, device="cuda"), x, w, dw=dw, dbias=db, accumulate=True)
     assert (dw.view(torch.int32) == -2 ** 31).all() and (db.view(torch.int32) == -2 ** 31).all()
+
+
+def test_offsets_of_an_empty_batch():
+    """The exported offsets of no tokens are all 0, in new tensors and in a caller's buffer that holds an older batch's."""
+    E, d, f = 5, 64, 72
+    w1, w2 = torch.zeros((E, 2 * f, d), dtype=BF16, device="cuda"), torch.zeros((E, d, f), dtype=BF16, device="cuda")
+    x, ids = torch.zeros((0, d), dtype=BF16, device="cuda"), torch.zeros((0, 2), dtype=torch.int32, device="cuda")
+    dirty = [torch.full((E + 1,), 77, dtype=torch.int32, device="cuda") for _ in range(8)]
+    del dirty  # what torch.empty may give next
+    y, it = nvq.moe_expert_fwd_bf16(x, ids, w1, w2, export=True, save_gu=True)
+    assert y.shape == (0, 2, d) and it["h"].shape == (0, f) and it["gu"].shape == (0, 2 * f)
+    assert (it["offsets"] == 0).all()
+    own = torch.full((E + 1,), 77, dtype=torch.int32, device="cuda")
+    ws = torch.empty(int(nvq.lib().moe_expert_fwd_bf16_workspace_size(0, d, 2, E, f)), dtype=torch.uint8, device="cuda")
+    rc = nvq.lib().moe_expert_fwd_bf16(None, 0, d, None, 2, E, f, w1.data_ptr(), w2.data_ptr(), None,
+                                       nvq.C.byref(nvq.MoeBuffers(offsets=own.data_ptr())), ws.data_ptr(), ws.numel(),
+                                       torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and (own == 0).all()
