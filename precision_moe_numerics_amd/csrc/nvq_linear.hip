@@ -204,12 +204,13 @@ int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, con
         !gemm16_dims_ok(kWgrad, false, M, 1, R, K, 0) ||
         !grid_ok((N + kBwdCols - 1) / kBwdCols * ((M + bwd_rows(M, N) - 1) / bwd_rows(M, N)), 256))
         return NVQ_ERR_DIM;
-    if (!ws || (!dx && !dw && !dbias) || (dx && !w)) return NVQ_ERR_NULL;
+    if (!ws || (M > 0 && !dx && !dw && !dbias) || (dx && !w)) return NVQ_ERR_NULL;
     if (M > 0 && (!dout || (dw && !x) || (act != NVQ_ACT_NONE && !z))) return NVQ_ERR_NULL;
     if (!aligned16(dout) || !aligned16(x) || !aligned16(w) || !aligned16(z) || !aligned16(dx) || !aligned16(dw) ||
         !aligned16(dbias) || !aligned256(ws))
         return NVQ_ERR_ALIGN;
     if (ws_bytes < linear_act_bwd_bf16_workspace_size(M, N, K, act)) return NVQ_ERR_WORKSPACE;
+    if (M == 0 && !dw && !dbias) return NVQ_OK;
     hipStream_t s = as_stream(stream);
     Carver cv(ws);
     uint16_t* dz;

@@ -172,3 +172,14 @@ def test_reference_gradients_against_differences(act):
         kink = (z.abs() <= h) if act == 1 else torch.zeros_like(num, dtype=torch.bool)
         # h^2 / 6 |act'''| with |act'''| <= 3 (1 + |u|), and 2^-52 / h of the values
         assert (((f - num).abs() <= 2.0 ** -30 * (1 + z.abs().amax())) | kink).all()
+
+
+def test_dense_backward_of_no_rows():
+    """With no rows dx has no storage and so no address: not a missing output."""
+    L = nvq.lib()
+
+    def bwd(M, dx=None, w=_p(0), ws=_p(1)):
+        return L.linear_act_bwd_bf16(None, 0, None, w, None, M, 64, 64, 4, dx, None, 1, 0, None, ws, BIG, None)
+
+    assert bwd(0) == OK and bwd(0, dx=_p(2)) == OK
+    assert bwd(16) == NULL and bwd(0, ws=None) == NULL and bwd(0, dx=_p(2), w=None) == NULL

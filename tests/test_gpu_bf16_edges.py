@@ -202,3 +202,12 @@ def test_offsets_of_an_empty_batch():
                                        nvq.C.byref(nvq.MoeBuffers(offsets=own.data_ptr())), ws.data_ptr(), ws.numel(),
                                        torch.cuda.current_stream().cuda_stream)
     assert rc == 0 and (own == 0).all()
+
+
+@pytest.mark.parametrize("act", [NONE, SILU, SWIGLU])
+def test_dense_backward_of_no_rows_for_dx_alone(act):
+    rows = 144 if act == SWIGLU else 72
+    w, x = torch.zeros((rows, 64), dtype=BF16, device="cuda"), torch.zeros((0, 64), dtype=BF16, device="cuda")
+    z = torch.zeros((0, rows), dtype=BF16, device="cuda")
+    dx, dw, db = nvq.linear_act_bwd_bf16(torch.zeros((0, 72), device="cuda"), x, w, z=z, act=act, need_dw=False)
+    assert dx.shape == (0, 64) and dw is None and db is None
