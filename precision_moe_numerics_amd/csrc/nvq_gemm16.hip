@@ -16,7 +16,10 @@ constexpr int kMaxE = 4096;
 // LDS (four experts per thread), then every thread fills entries t, t + 1024,
 // ... by binary search. Offsets are clamped to [0, rows] and a decreasing one
 // counts as an empty segment, so no entry points outside the rows and none is
-// written past `cap`.
+// written past `cap`. Offsets that fall and rise again can make sums past 2^31,
+// which wrap: the entries found then still lie in their segments (a search ends
+// at first[lo] <= i < first[lo + 1], which no wrap lies between), and a negative
+// total counts as no tiles.
 __global__ __launch_bounds__(kTabThreads) void k_tile_table(const int32_t* __restrict__ seg, int E, int rows, int tm,
                                                             int cap, int32_t* __restrict__ count,
                                                             Tile* __restrict__ tiles) {
@@ -38,7 +41,7 @@ __global__ __launch_bounds__(kTabThreads) void k_tile_table(const int32_t* __res
         if (4 * t + j < E) first[4 * t + j] = base;
         base += n[j];
     }
-    total = min(total, cap);
+    total = max(min(total, cap), 0);
     if (t == 0) {
         first[E] = total;
         *count = total;

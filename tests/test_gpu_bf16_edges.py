@@ -211,3 +211,21 @@ def test_dense_backward_of_no_rows_for_dx_alone(act):
     z = torch.zeros((0, rows), dtype=BF16, device="cuda")
     dx, dw, db = nvq.linear_act_bwd_bf16(torch.zeros((0, 72), device="cuda"), x, w, z=z, act=act, need_dw=False)
     assert dx.shape == (0, 64) and dw is None and db is None
+
+
+@pytest.mark.parametrize("mode", [nvq.FWD, nvq.DGRAD])
+def test_offsets_whose_tiles_pass_32_bits(mode):
+    """Offsets that go up to R and down to 0 again by turns, 2048 times: 2^31 and more tiles of clamped segments. No
+    tile is taken from outside the table, no row from outside [0, R). (All rows are row 0, stored to row 1.)"""
+    R, E, N, K = 5 << 26, 4096, 264, 8
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = R
+    src = torch.zeros(R, dtype=torch.int32, device="cuda")
+    dst = torch.ones(R, dtype=torch.int32, device="cuda")
+    a = torch.ones((1, K), dtype=BF16, device="cuda")
+    b = torch.ones((E, N, K) if mode == nvq.FWD else (E, K, N), dtype=BF16, device="cuda")
+    out = torch.full((3, N), 5.0, dtype=BF16, device="cuda")
+    nvq.moe_grouped_gemm_bf16(mode, a, b, off, a_gather=src, out_scatter=dst, out=out)
+    torch.cuda.synchronize()
+    assert (out[0] == 5.0).all() and (out[2] == 5.0).all()
+    assert ((out[1] == 5.0) | (out[1] == K)).all()
