@@ -445,12 +445,14 @@ int moe_grouped_gemm_nvfp4_bwd(int mode, const uint8_t* a_codes, const uint8_t* 
 /* compared with ([AIC] "Key Takeaways", "Architecture highlights": only the */
 /* expert forward is 4-bit). Operands are bf16, products accumulate in fp32  */
 /* and are rounded once. In all calls of this section: outputs must not      */
-/* overlap inputs or the workspace (residual == out is allowed: each element  */
-/* is read before it is written), and infinities and NaN propagate as in the  */
-/* formulas. The same call on the same values gives the same bits. Sizes whose */
-/* launch would hold 2^32 work-items are refused (NVQ_ERR_DIM): T * C / 8 for */
-/* the combine; 64 T, past C = 1024 256 T, for its backward; 64 T for the     */
-/* routers' backward; 4 M ceil(N / 512) for the linear backward.             */
+/* overlap inputs or the workspace (residual == out is allowed for a bf16    */
+/* out: each element is read before it is written), and infinities and NaN   */
+/* propagate as in the formulas (so x * Phi(x) and x * sigmoid(x) are NaN at */
+/* -inf; ReLU and its gradient select: 0 at -inf). The same call on the same */
+/* values gives the same bits. Sizes whose launch would hold 2^32 work-items */
+/* are refused (NVQ_ERR_DIM): T * C / 8 for the combine; 64 T, past C = 1024 */
+/* 256 T, for its backward; 64 T for the routers' backward; 4 M ceil(N /     */
+/* 512) for the linear backward.                                             */
 /* ------------------------------------------------------------------------ */
 
 /* Products grouped by expert. Logical token rows r = 0 .. R-1 lie in expert

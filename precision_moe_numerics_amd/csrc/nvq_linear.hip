@@ -165,6 +165,7 @@ extern "C" {
 int linear_act_bf16(const uint16_t* x, const uint16_t* w, const float* bias, const uint16_t* residual, int64_t M,
                     int64_t N, int64_t K, int act, void* out, int out_dtype, uint16_t* z, nvq_stream_t stream) {
     if (!act_ok(act) || (out_dtype != NVQ_OUT_BF16 && out_dtype != NVQ_OUT_F32)) return NVQ_ERR_UNSUPPORTED;
+    if (residual && residual == out && out_dtype != NVQ_OUT_BF16) return NVQ_ERR_UNSUPPORTED;  // rows would overlap others
     if (!linear_dims_ok(M, N, K, act)) return NVQ_ERR_DIM;
     if (!w || (M > 0 && (!x || !out))) return NVQ_ERR_NULL;
     if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(out) ||

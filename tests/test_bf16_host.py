@@ -183,3 +183,10 @@ def test_dense_backward_of_no_rows():
 
     assert bwd(0) == OK and bwd(0, dx=_p(2)) == OK
     assert bwd(16) == NULL and bwd(0, ws=None) == NULL and bwd(0, dx=_p(2), w=None) == NULL
+
+
+def test_a_residual_in_place_has_the_outputs_type():
+    """residual == out is for bf16 outputs: an fp32 out over a bf16 residual would overwrite rows not yet read."""
+    L = nvq.lib()
+    assert L.linear_act_bf16(_p(0), _p(1), None, _p(2), 16, 64, 64, 0, _p(2), 1, None, None) == UNSUPPORTED
+    assert L.linear_act_bf16(None, _p(1), None, _p(2), 16, 64, 64, 0, _p(2), 0, None, None) == NULL
