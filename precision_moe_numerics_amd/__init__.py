@@ -783,12 +783,16 @@ def linear_act_bf16(x, w, bias=None, act=ACT_NONE, residual=None, out_dtype=torc
 def linear_act_bwd_bf16(dout, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=True, need_dbias=False,
                         dw_dtype=torch.float32, dx=None, dw=None, dbias=None, accumulate=False, ws=None):
     """Backward of linear_act_bf16 from dout (bf16 or fp32 [M, N]) and the saved z: (dx bf16 [M, K], dw [shape of w],
-    dbias fp32 [rows of w]), None where not needed. accumulate adds to the given dw and dbias."""
+    dbias fp32 [rows of w]), None where not needed. x may be None without dw, w without dx. accumulate adds to the given
+    dw and dbias."""
     bf, f32 = torch.bfloat16, torch.float32
-    dev, (M, K) = _main(x, bf, "x", 2)
-    rows, N = _linear_sizes(w, act)
     _dims(dout, 2, "dout")
+    dev, (M, N) = _main(dout, dout.dtype, "dout", 2)
+    rows = 2 * N if act == ACT_SWIGLU else N
     need_dx, need_dw, need_dbias = need_dx or dx is not None, need_dw or dw is not None, need_dbias or dbias is not None
+    if (x is None and need_dw) or (w is None and need_dx):
+        raise NvqError("dw needs x and dx needs w")
+    K = 8 if x is None and w is None else _dims(w, 2, "w")[1] if x is None else _dims(x, 2, "x")[1]
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         raise NvqError("accumulate needs dw and dbias to add to")
     gd = _float_mode(dout.dtype, "dout")
@@ -800,7 +804,7 @@ def linear_act_bwd_bf16(dout, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=
     if dbias is None and need_dbias:
         dbias = torch.empty((rows,), dtype=f32, device=dev)
     ws, wp, wn = _scratch(lib().linear_act_bwd_bf16_workspace_size(M, N, K, act), dev, ws)
-    _launch("linear_act_bwd_bf16", dev, _arg(dout, dout.dtype, "dout", (M, N), dev), gd, x.data_ptr(),
+    _launch("linear_act_bwd_bf16", dev, dout.data_ptr(), gd, _arg(x, bf, "x", (M, K), dev),
             _arg(w, bf, "w", (rows, K), dev), _arg(z, bf, "z", (M, rows), dev), M, N, K, act,
             _arg(dx, bf, "dx", (M, K), dev), _arg(dw, f32 if wd == OUT_F32 else bf, "dw", (rows, K), dev), wd,
             int(accumulate), _arg(dbias, f32, "dbias", (rows,), dev), wp, wn)

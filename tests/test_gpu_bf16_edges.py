@@ -229,3 +229,21 @@ def test_offsets_whose_tiles_pass_32_bits(mode):
     torch.cuda.synchronize()
     assert (out[0] == 5.0).all() and (out[2] == 5.0).all()
     assert ((out[1] == 5.0) | (out[1] == K)).all()
+
+
+@pytest.mark.parametrize("act", [NONE, GELU, SWIGLU])
+def test_dense_backward_without_the_operand_of_a_gradient_not_asked_for(act):
+    """dx needs w, dw needs x, dbias neither, as in the C call; what a gradient needs may not be missing."""
+    M, N, K = 50, 72, 64
+    rows = 2 * N if act == SWIGLU else N
+    g = torch.Generator().manual_seed(5)
+    x, w, z, dout = (torch.randn(s, generator=g).to(BF16).cuda() for s in ((M, K), (rows, K), (M, rows), (M, N)))
+    z = None if act == NONE else z
+    dx, dw, db = nvq.linear_act_bwd_bf16(dout, x, w, z=z, act=act, need_dbias=True)
+    assert torch.equal(nvq.linear_act_bwd_bf16(dout, None, w, z=z, act=act, need_dw=False)[0], dx)
+    assert torch.equal(nvq.linear_act_bwd_bf16(dout, x, None, z=z, act=act, need_dx=False)[1], dw)
+    only = nvq.linear_act_bwd_bf16(dout, None, None, z=z, act=act, need_dx=False, need_dw=False, need_dbias=True)
+    assert only[0] is None and only[1] is None and torch.equal(only[2], db)
+    for bad in (dict(x=None, w=w), dict(x=x, w=None), dict(x=x, w=w[:-8]), dict(x=x[:-1], w=w), dict(x=x.float(), w=w)):
+        with pytest.raises(nvq.NvqError):
+            nvq.linear_act_bwd_bf16(dout, bad["x"], bad["w"], z=z, act=act)
