@@ -530,9 +530,12 @@ int linear_act_bf16(const uint16_t* x, const uint16_t* w, const float* bias, con
  *   dbias[n] = sum_m dz[m][n]  fp32, from the unrounded dz
  *   dx = dz . w     bf16 [M, K]
  *   dw = dz^T . x   bf16 or fp32, shape of w
- * with dz rounded to bf16 as an operand of the two products. Any of dx, dw,
- * dbias may be NULL (not all, unless M is 0); x is needed for dw, w for dx. accumulate != 0
- * adds to dw and dbias. The residual's gradient is dout. relu'(0) = 0. */
+ * with dz rounded to bf16 as an operand of the two products (2^-8 of it: an
+ * fp32 dw of an fp32 dout without activation keeps 2^-16 where dout goes in as
+ * two bf16 parts, hi and dout - hi, the second call accumulating). Any of dx,
+ * dw, dbias may be NULL (not all, unless M is 0); x is needed for dw, w for dx.
+ * accumulate != 0 adds to dw and dbias. The residual's gradient is dout.
+ * relu'(0) = 0. */
 size_t linear_act_bwd_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int act);
 int linear_act_bwd_bf16(const void* dout, int dout_dtype, const uint16_t* x, const uint16_t* w, const uint16_t* z,
                         int64_t M, int64_t N, int64_t K, int act, uint16_t* dx, void* dw, int dw_dtype,

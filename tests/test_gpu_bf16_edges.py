@@ -247,3 +247,23 @@ def test_dense_backward_without_the_operand_of_a_gradient_not_asked_for(act):
     for bad in (dict(x=None, w=w), dict(x=x, w=None), dict(x=x, w=w[:-8]), dict(x=x[:-1], w=w), dict(x=x.float(), w=w)):
         with pytest.raises(nvq.NvqError):
             nvq.linear_act_bwd_bf16(dout, bad["x"], bad["w"], z=z, act=act)
+
+
+def test_dense_backward_of_an_fp32_dout_in_two_parts():
+    """dz is a bf16 operand: 2^-8 of it is lost. An fp32 dout split into bf16 hi + lo and given in two calls, the second
+    accumulating, leaves 2^-16 (lo is off by half a step of itself, and |lo| <= 2^-8 |dout|)."""
+    M, N, K = 300, 72, 64
+    g = torch.Generator().manual_seed(6)
+    x, w = (torch.randn(s, generator=g).to(BF16).cuda() for s in ((M, K), (N, K)))
+    dout = torch.randn((M, N), generator=g).cuda()
+    hi = dout.to(BF16)
+    lo = (dout - hi.float()).to(BF16)
+    _, dw, db = nvq.linear_act_bwd_bf16(hi, x, w, need_dx=False, need_dbias=True)
+    nvq.linear_act_bwd_bf16(lo, x, w, need_dx=False, dw=dw, dbias=db, accumulate=True)
+    d, x64 = dout.double().cpu(), x.double().cpu()
+    s = d.abs().T @ x64.abs()
+    check(dw, d.T @ x64, (1.01 * 2.0 ** -16 + (M + 1) * U) * s, "dw")
+    check(db, d.sum(0), (1.01 * 2.0 ** -16 + (M + 1) * U) * d.abs().sum(0), "dbias")
+    # one call loses what the contract says and no more
+    _, one, _ = nvq.linear_act_bwd_bf16(dout, x, w, need_dx=False)
+    check(one, d.T @ x64, (1.01 * 2.0 ** -8 + M * U) * s, "dw in one call")
