@@ -267,3 +267,42 @@ def test_dense_backward_of_an_fp32_dout_in_two_parts():
     # one call loses what the contract says and no more
     _, one, _ = nvq.linear_act_bwd_bf16(dout, x, w, need_dx=False)
     check(one, d.T @ x64, (1.01 * 2.0 ** -8 + M * U) * s, "dw in one call")
+
+
+# ------------------------------------------------------------------ calls at once
+def test_calls_with_scratch_on_two_streams_at_once():
+    """Calls that keep tables, routing or partial sums in scratch memory, interleaved on two streams with different
+    segments: each gives what it gives alone. Tile tables of 256 x 256 and 128 x 128 tiles, the whole expert forward, the
+    dense backward's dz and bias sums."""
+    def rnd(seed, *shape, std=1.0):
+        return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * std).to(BF16).cuda()
+
+    def side(i):
+        lens = [[600, 0, 64, 1023, 1, 400], [1, 700, 300, 0, 87, 1000]][i]
+        off = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+        R, E, T, k = sum(lens), len(lens), 700, 2
+        x, w, ws = rnd(10 + i, R, 72), rnd(20 + i, E, 5512, 72), rnd(22 + i, E, 72, 1032)
+        ids = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(50 + 1000 * i + t))[:k]
+                           for t in range(T)]).to(torch.int32).cuda()
+        xt, w1, w2 = rnd(30 + i, T, 136), rnd(32 + i, E, 2 * 264, 136, std=0.1), rnd(34 + i, E, 136, 264, std=0.1)
+        lx, lw, lz, lg = rnd(40 + i, 900, 136), rnd(42 + i, 2 * 520, 136), rnd(44 + i, 900, 2 * 520), rnd(46 + i, 900, 520)
+        return [lambda: nvq.moe_grouped_gemm_bf16(nvq.FWD, x, w, off),
+                lambda: nvq.moe_grouped_gemm_bf16(nvq.DGRAD, x, ws, off),
+                lambda: nvq.moe_expert_fwd_bf16(xt, ids, w1, w2),
+                lambda: torch.cat([t.flatten().float() for t in nvq.linear_act_bwd_bf16(lg, lx, lw, z=lz, act=SWIGLU,
+                                                                                        need_dbias=True)])]
+
+    calls = [side(0), side(1)]
+    alone = [[c() for c in calls[i]] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for rep in range(8):
+        for j in range(4):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    got[i].append((j, calls[i][j]()))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for j, out in got[i]:
+            assert torch.equal(out, alone[i][j]), (i, j)
