@@ -27,10 +27,12 @@ static size_t fwd16_carve(Carver& c, int64_t T, int k, int64_t E, int64_t d_ff, 
     return c.need;
 }
 
-static bool fwd16_dims_ok(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff) {
+static bool fc1_dims_ok(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff) {
     if (T < 0 || k < 1 || E < 1 || k > E || T > ((int64_t)1 << 31) / k) return false;
-    return gemm16_dims_ok(kFwd, true, T * k, E, 0, d_ff, d) && gemm16_dims_ok(kFwd, false, T * k, E, 0, d, d_ff) &&
-           T * d * 2 <= kMaxBytes;
+    return gemm16_dims_ok(kFwd, true, T * k, E, 0, d_ff, d) && T * d * 2 <= kMaxBytes;
+}
+static bool fwd16_dims_ok(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff) {
+    return fc1_dims_ok(T, d, k, E, d_ff) && gemm16_dims_ok(kFwd, false, T * k, E, 0, d, d_ff);
 }
 
 static Args fc1_args(const uint16_t* x, int64_t T, int64_t d, const int32_t* offsets, const int32_t* s2a, int k,
@@ -91,7 +93,7 @@ size_t moe_fc1_bf16_workspace_size(int64_t A, int64_t E) { return gemm16_ws_byte
 int moe_fc1_swiglu_bf16(const uint16_t* x, int64_t T, int64_t d, const int32_t* offsets,
                         const int32_t* sorted2assign, int k, int64_t E, int64_t d_ff, const uint16_t* w1,
                         uint16_t* h, uint16_t* gu, void* ws, size_t ws_bytes, nvq_stream_t stream) {
-    if (!fwd16_dims_ok(T, d, k, E, d_ff)) return NVQ_ERR_DIM;
+    if (!fc1_dims_ok(T, d, k, E, d_ff)) return NVQ_ERR_DIM;
     if (!offsets || !w1 || !ws || (T > 0 && (!x || !sorted2assign || !h))) return NVQ_ERR_NULL;
     if (!aligned16(x) || !aligned16(w1) || !aligned16(h) || !aligned16(gu) || !aligned256(ws)) return NVQ_ERR_ALIGN;
     if (ws_bytes < moe_fc1_bf16_workspace_size(T * k, E)) return NVQ_ERR_WORKSPACE;

@@ -190,3 +190,12 @@ def test_a_residual_in_place_has_the_outputs_type():
     L = nvq.lib()
     assert L.linear_act_bf16(_p(0), _p(1), None, _p(2), 16, 64, 64, 0, _p(2), 1, None, None) == UNSUPPORTED
     assert L.linear_act_bf16(None, _p(1), None, _p(2), 16, 64, 64, 0, _p(2), 0, None, None) == NULL
+
+
+def test_fc1_is_not_refused_for_the_size_of_fc2():
+    """2^24 tiles of 128 x 128 in fc2's output, 2^17 in fc1's: within fc1's limits (refused here for a missing operand)."""
+    L = nvq.lib()
+    T, d, k, E, f = (1 << 17) - 1, 1 << 14, 128, 128, 64
+    assert L.moe_fc1_swiglu_bf16(None, T, d, _p(1), _p(2), k, E, f, _p(3), _p(4), None, _p(5), BIG, None) == NULL
+    assert L.moe_expert_fwd_bf16(None, T, d, _p(1), k, E, f, _p(2), _p(3), _p(4), None, _p(5), BIG, None) == DIM
+    assert L.moe_fc1_swiglu_bf16(None, T + 1, d, _p(1), _p(2), k, E, f, _p(3), _p(4), None, _p(5), BIG, None) == DIM
