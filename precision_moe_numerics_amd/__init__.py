@@ -696,6 +696,9 @@ def moe_grouped_gemm_bf16(mode, a, b, seg_offsets, a_gather=None, a_div=1, b_gat
         out = torch.empty(shape, dtype=out_dtype, device=dev)
     elif out_scatter is not None:
         shape = (_dims(out, 2, "out")[0], N)
+    for gather, div in ((a_gather, a_div), (b_gather, b_div)):
+        if gather is not None and not 0 < div < 1 << 31:  # (ctypes would keep the low 32 bits)
+            raise NvqError(f"a gather's divisor must be a positive 32-bit number, not {div}")
     i32 = torch.int32
     w, wp, wn = _scratch(lib().moe_grouped_gemm_bf16_workspace_size(mode, E, R), dev, ws)
     _launch("moe_grouped_gemm_bf16", dev, mode, a.data_ptr(), a_rows, _arg(a_gather, i32, "a_gather", (R,), dev), a_div,

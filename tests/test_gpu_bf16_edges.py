@@ -306,3 +306,16 @@ def test_calls_with_scratch_on_two_streams_at_once():
     for i in range(2):
         for j, out in got[i]:
             assert torch.equal(out, alone[i][j]), (i, j)
+
+
+def test_gather_divisors_are_32_bit():
+    """A divisor past 32 bits is refused, not cut to its low bits (2^32 + 2 would divide by 2)."""
+    a, b = torch.zeros((8, 64), dtype=BF16, device="cuda"), torch.zeros((1, 64, 64), dtype=BF16, device="cuda")
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    g = torch.zeros(8, dtype=torch.int32, device="cuda")
+    for div in (0, -1, 2 ** 31, 2 ** 32 + 2):
+        with pytest.raises(nvq.NvqError):
+            nvq.moe_grouped_gemm_bf16(nvq.FWD, a, b, off, a_gather=g, a_div=div)
+        with pytest.raises(nvq.NvqError):
+            nvq.moe_grouped_gemm_bf16(nvq.WGRAD, a, a, off, b_gather=g, b_div=div)
+    nvq.moe_grouped_gemm_bf16(nvq.FWD, a, b, off, a_gather=g, a_div=2 ** 31 - 1)
