@@ -161,9 +161,17 @@ bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int6
 
 // Whether 256 x 256 tiles (one persistent workgroup per CU) beat 128 x 128 ones (two workgroups per CU), by the rounds
 // that the chip makes over them. A K step of a big tile takes a CU 13 units, one of two small tiles at once 11; a CU that
-// has one small tile only, 7. Measured, small against big: 2048 x 4096 x 4096 73 us, 88; 4096^3 152, 112; 3000 x 7000 x
-// 1000 76, 62; 6000 x 6000 x 600 79, 67; fc1 of 384 experts at 4096 tokens 1326, 1413, at 8192 1909, 1490; weight
-// gradients of 270 matrices of 192 x 152 22, 42, of 384 of 4096 x 7168 1493, 1131.
+// has one small tile only, 7. Measured, small against big, us, bf16 outputs of FWD: 2048 x 4096 x 4096 73, 88; 4096^3 152,
+// 112; 3000 x 7000 x 1000 76, 62; 6000 x 6000 x 600 79, 67; fc1 of 384 experts at 4096 tokens 1326, 1413, at 8192 1909,
+// 1490. Weight gradients, of E experts with R rows each, fp32 outputs, then bf16:
+//   384 of 4096 x 1024, R =   64   1329, 1240   1036,  716        8 of 2048 x 4096, R = 2048   340, 289   314, 266
+//                       R =  128   1971, 1282   1353,  988        8 of 4096 x 1024, R = 2048   164, 150   139, 138
+//                       R =  341   2636, 2017   1959, 1579      270 of  192 x  152, R =  128    19,  38    17,  36
+//                       R = 1024   4306, 3738   3748, 3387        1 of 1024 x 4096, R = 4096    52, 118    50, 117
+//   384 of 2048 x 4096, R =  341   5311, 4134   3569, 3020        1 of 2048 x 4096, R = 4096    70, 120    68, 118
+//    64 of 1024 x 1024, R =  256    100,   76     57,   57        1 of 4096 x 4096, R = 4096   149, 133   141, 131
+//   384 of 4096 x 1024, R =  341, accumulating   3867, 3618   2785, 2821
+// The rule takes the faster side of each, or one within 1.5 %; outputs twice as wide change none of them.
 static bool big_tiles(double big, double small, int cus) {
     const double t_small = small <= cus ? 7.0 : 11.0 * std::max(1.0, small / (2.0 * cus));
     return 13.0 * std::max(1.0, std::ceil(big / cus)) < t_small;

@@ -2,13 +2,19 @@
 // the grouped products of the unquantized expert layer (nvq_moe16.hip) and the
 // dense product with its epilogue (nvq_linear.hip).
 //
-// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) for three operand
-// arrangements, with bf16 operands and fp32 accumulation:
+// Three kernels compute out[m][n] = sum_k A(m, k) B(n, k) with bf16 operands and
+// fp32 accumulation; launch_gemm16 chooses one by the sizes:
+//   k_gemm16         128 x 128 tiles, two workgroups per CU (here);
+//   k_gemm16_big     256 x 256 tiles in one persistent stream per CU
+//                    (nvq_gemm16_big.hpp);
+//   k_gemm16_skinny  FWD of a few rows per expert (nvq_gemm16_skinny.hpp).
+// Operand arrangements:
 //   FWD    A rows and B rows hold k contiguously (x W^T);
 //   DGRAD  A as above, B holds n contiguously (g W, W as the forward keeps it);
 //   WGRAD  A and B hold m and n contiguously, k runs over token rows (g^T x).
 // Rows come in expert segments (or one dense block), may be gathered on the
-// way in and scattered on the way out.
+// way in and scattered on the way out. Here too: what the kernels share, the
+// loads into LDS, the fragments, the activations and the epilogues.
 #pragma once
 
 #include <type_traits>
@@ -238,8 +244,8 @@ __device__ __forceinline__ void store_pair(void* out, int64_t base, int n, int N
 // Epilogue of a weight gradient. Every output is stored (empty experts too) and a tile's K is short, so the stores are
 // half the work: 2 KiB at a time go through the wave's own LDS (16 rows of 64 bf16 or 32 fp32, 16-byte chunk c of row r
 // at slot c ^ (r & 7)) so that eight neighbouring lanes hold 128 bytes of one row, bf16: twice 64. Neighbouring lanes in
-// neighbouring rows, as the accumulators lie, take the CU's store path a cycle per lane (384 experts of 2048 x 4096, 341
-// rows each: 2.29 ms against 2.48; the products alone 1.50). A piece is read back before the one ahead of it is stored.
+// neighbouring rows, as the accumulators lie, take the CU's store path a cycle per lane (384 experts of 4096 x 1024 in
+// fp32, 341 rows on average: 2.29 ms against 2.48; the products alone 1.50). A piece is read back before the one ahead of it is stored.
 // `full`: all rows and columns lie inside the output.
 constexpr int kRowBuf = 2048;
 template <bool F32, int MF, int NF>

@@ -5,7 +5,7 @@
 // That gradient, dz, is rounded to bf16 once, as the operand of both products
 // (the bias gradient takes it unrounded): the layer's operands are bf16, and a
 // second bf16 term for what the rounding drops would double both products, 133
-// of 153 us at 4091 x 1024 x 4096 SwiGLU. It costs 2.3e-3 of the 2-norm of dx
+// of 151 us at 4091 x 1024 x 4096 SwiGLU. It costs 2.3e-3 of the 2-norm of dx
 // and a bf16 dw there, where the rounding of the results alone is 1.7e-3, and
 // 1.7e-3 of an fp32 dw. Without an activation a caller can split an fp32 dout.
 #include "nvq_gemm16.hpp"
