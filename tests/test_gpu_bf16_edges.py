@@ -319,3 +319,38 @@ def test_gather_divisors_are_32_bit():
         with pytest.raises(nvq.NvqError):
             nvq.moe_grouped_gemm_bf16(nvq.WGRAD, a, a, off, b_gather=g, b_div=div)
     nvq.moe_grouped_gemm_bf16(nvq.FWD, a, b, off, a_gather=g, a_div=2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("lens,N,K", [([3, 0, 2], 200, 72), ([400, 0, 300], 1032, 456), ([600, 0, 64, 1023, 1, 400], 5512, 72)])
+def test_rows_before_the_first_and_behind_the_last_segment_are_left(lens, N, K):
+    """Segments that start past row 0 and end before the last row: the rows outside, whose gather and scatter entries are
+    traps, are neither read nor written, by the products of a few rows, of 128 x 128 and of 256 x 256 tiles."""
+    def rnd(seed, *shape):
+        return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(BF16).cuda()
+
+    before, behind, E, k = 5, 9, len(lens), 1
+    n = sum(lens)
+    R = before + n + behind
+    off = (torch.tensor([0] + lens, dtype=torch.int32).cumsum(0) + before).to(torch.int32).cuda()
+    inner = slice(before, before + n)
+    trap = torch.full((R,), 2 ** 30, dtype=torch.int32, device="cuda")
+    idx = trap.clone()
+    idx[inner] = torch.randperm(R, generator=torch.Generator().manual_seed(1))[:n].to(torch.int32).cuda()
+    a, plain = rnd(2, R, K), off - before
+    for mode in (nvq.FWD, nvq.DGRAD):
+        b = rnd(3, E, *((N, K) if mode == nvq.FWD else (K, N)))
+        out = torch.full((R, N), 77.0, dtype=BF16, device="cuda")
+        nvq.moe_grouped_gemm_bf16(mode, a, b, off, a_gather=idx, out_scatter=idx, out=out)
+        want = torch.full_like(out, 77.0)
+        want[idx[inner].long()] = nvq.moe_grouped_gemm_bf16(mode, a[idx[inner].long()], b, plain)
+        assert torch.equal(out, want)
+    w1 = rnd(4, E, 2 * N, K)
+    h, gu = torch.full((R, N), 77.0, dtype=BF16, device="cuda"), torch.full((R, 2 * N), 77.0, dtype=BF16, device="cuda")
+    nvq.moe_fc1_swiglu_bf16(a, off, idx, k, w1, h=h, gu=gu)
+    h2, gu2 = nvq.moe_fc1_swiglu_bf16(a[idx[inner].long()], plain, torch.arange(n, dtype=torch.int32, device="cuda"), k, w1,
+                                      save_gu=True)
+    for got, ref in ((h, h2), (gu, gu2)):
+        assert torch.equal(got[inner], ref) and (got[:before] == 77.0).all() and (got[before + n:] == 77.0).all()
+    dw = nvq.moe_grouped_gemm_bf16(nvq.WGRAD, a, h, off, a_gather=idx)
+    ref = nvq.moe_grouped_gemm_bf16(nvq.WGRAD, a[idx[inner].long()], h[inner].contiguous(), plain)
+    assert torch.equal(dw, ref)
