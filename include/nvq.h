@@ -568,6 +568,68 @@ int moe_router_sigmoid_topk_bwd(const float* w, const float* logits, const int32
                                 int64_t T, int64_t E, int k, float* dlogits, nvq_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* The products in 8-bit integers: symmetric codes with one fp32 scale per   */
+/* row, a token of the activations or an output channel of the weights, for  */
+/* layers that are served from int8 weights. A product's sum is exact in     */
+/* int32 (every code from -128 to 127); its fp32 value is                    */
+/* sum * x_scale * w_scale, each factor rounded once. Outputs must not       */
+/* overlap inputs or the workspace (residual == out is allowed for a bf16    */
+/* out). The same call on the same values gives the same bits.               */
+/* ------------------------------------------------------------------------ */
+
+/* Codes and scales of bf16 rows x [R, C]: a = max |x| of the row, scale =
+ * a / 127 in fp32, code = 127 x / a to the nearest integer, ties to even,
+ * decided as the exact quotient. An all-zero row has scale 1; a row that holds
+ * an infinity or NaN has scale NaN and zero codes, so that everything computed
+ * from it is NaN. Weights [E, N, K] are E * N rows. codes [R, C], scales [R].
+ * Limits: C % 16 == 0, C <= 2^22, R < 2^24. All pointers 16-byte aligned. */
+int int8_quantize(const uint16_t* x, int64_t R, int64_t C, int8_t* codes, float* scales, nvq_stream_t stream);
+/* out[r][c] = code * scale, rounded to fp32, then to bf16 for NVQ_OUT_BF16.
+ * Limits as above, and R * C / 16 < 2^32 - 256. */
+int int8_dequantize(const int8_t* codes, const float* scales, int64_t R, int64_t C, void* out, int out_dtype,
+                    nvq_stream_t stream);
+
+/* Dense product with its epilogue, as linear_act_bf16:
+ *   z[m][n] = (sum_k xq[m][k] wq[n][k]) * x_scales[m] * w_scales[n] + bias[n]
+ *   out = act(z) + residual
+ * xq [M, K], x_scales [M], wq [N, K], w_scales [N] (NVQ_ACT_SWIGLU: 2N rows, the
+ * gate half first), bias fp32 [rows of wq] (nullable), residual bf16 [M, N]
+ * (nullable), out [M, N] bf16 or fp32. Limits (else NVQ_ERR_DIM): K % 16 == 0,
+ * K < 2^17, N % 8 == 0, N <= 2^22, wq below 4 GiB - 512, M < 2^31 - 256, output tiles
+ * (128 x 128, SwiGLU 128 x 64) below 2^24, M * N < 2^40. */
+int linear_act_int8(const int8_t* xq, const float* x_scales, const int8_t* wq, const float* w_scales, const float* bias,
+                    const uint16_t* residual, int64_t M, int64_t N, int64_t K, int act, void* out, int out_dtype,
+                    nvq_stream_t stream);
+
+/* The expert forward in int8: as moe_expert_fwd_bf16 with
+ *   Xq = int8_quantize of x [T, d], per token
+ *   g, u = Xq[sorted2assign[r] / k] . w1_e^T (scaled), w1 [E, 2*d_ff, d] with
+ *          w1_scales [E, 2*d_ff], gate rows first
+ *   h[r] = bf16(g * sigmoid(g) * u)
+ *   Hq = int8_quantize of h, per row
+ *   y[sorted2assign[r]] = bf16(Hq[r] . w2_e^T (scaled)), w2 [E, d, d_ff], w2_scales [E, d]
+ * y [T, k, d], unweighted. Rows of y whose expert id is out of range are left
+ * untouched. bufs (nullable): caller-owned xq_codes [T, d] (int8), xq_tscale [T]
+ * (the scales), offsets, sorted2assign, h [T*k, d_ff], hq_codes [T*k, d_ff] and
+ * hq_tscale [T*k]; its other fields must be NULL / 0 (else NVQ_ERR_UNSUPPORTED).
+ * Limits: d and d_ff multiples of 16 below 2^17, 1 <= k <= E <= 4096, T*k < 2^24,
+ * T*d and one expert's weights below 4 GiB - 512; tiles as above. */
+size_t moe_expert_fwd_int8_workspace_size(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff);
+int moe_expert_fwd_int8(const uint16_t* x, int64_t T, int64_t d, const int32_t* topk_ids, int k, int64_t E,
+                        int64_t d_ff, const int8_t* w1, const float* w1_scales, const int8_t* w2,
+                        const float* w2_scales, uint16_t* y, const nvq_moe_buffers* bufs, void* ws, size_t ws_bytes,
+                        nvq_stream_t stream);
+/* Its products (A = T*k rows; offsets and sorted2assign as from moe_route; rows
+ * from offsets[E] on are not read, and their outputs are left as they were). */
+size_t moe_gemm_int8_workspace_size(int64_t A, int64_t E);
+int moe_fc1_swiglu_int8(const int8_t* xq, const float* x_scales, int64_t T, int64_t d, const int32_t* offsets,
+                        const int32_t* sorted2assign, int k, int64_t E, int64_t d_ff, const int8_t* w1,
+                        const float* w1_scales, uint16_t* h, void* ws, size_t ws_bytes, nvq_stream_t stream);
+int moe_fc2_int8(const int8_t* hq, const float* h_scales, int64_t A, int64_t d_ff, const int32_t* offsets,
+                 const int32_t* sorted2assign, int64_t E, int64_t d, const int8_t* w2, const float* w2_scales,
+                 uint16_t* y, void* ws, size_t ws_bytes, nvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Converter checks. Every code, scale byte and bf16 output above comes from */
 /* a handful of gfx950 conversion instructions (and two software encoders);  */
 /* their exactness against the format rules (NVFP4 about 4.5 bits per value */

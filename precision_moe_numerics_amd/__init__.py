@@ -116,6 +116,16 @@ _OPTIONAL = {
     "moe_combine_bwd_bf16": ([_vp, _vp, _vp, _vp, _i64, _i64, C.c_int, _i64, _vp, _vp, _vp], C.c_int),
     "moe_router_softmax_topk_bwd": ([_vp, _vp, _vp, _i64, _i64, C.c_int, _vp, _vp], C.c_int),
     "moe_router_sigmoid_topk_bwd": ([_vp, _vp, _vp, _vp, _i64, _i64, C.c_int, _vp, _vp], C.c_int),
+    "int8_quantize": ([_vp, _i64, _i64, _vp, _vp, _vp], C.c_int),
+    "int8_dequantize": ([_vp, _vp, _i64, _i64, _vp, C.c_int, _vp], C.c_int),
+    "linear_act_int8": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, C.c_int, _vp, C.c_int, _vp], C.c_int),
+    "moe_gemm_int8_workspace_size": ([_i64, _i64], _sz),
+    "moe_fc1_swiglu_int8": ([_vp, _vp, _i64, _i64, _vp, _vp, C.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp],
+                            C.c_int),
+    "moe_fc2_int8": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp], C.c_int),
+    "moe_expert_fwd_int8_workspace_size": ([_i64, _i64, C.c_int, _i64, _i64], _sz),
+    "moe_expert_fwd_int8": ([_vp, _i64, _i64, _vp, C.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+                            C.c_int),
     "nvfp4_quantize_noalloc": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp, C.c_int, C.c_uint64, C.c_uint32, _vp],
                                C.c_int),
 }
@@ -863,3 +873,126 @@ def moe_router_sigmoid_topk_bwd(weights, logits, topk_ids, dweights, dlogits=Non
             _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev), _arg(dweights, f32, "dweights", (T, k), dev), T, E, k,
             _arg(dlogits, f32, "dlogits", (T, E), dev))
     return dlogits
+
+
+# ------------------------------------------------------------------ the products in int8
+def _pair(q, name):
+    try:
+        codes, scales = q
+        return codes, scales
+    except (TypeError, ValueError):
+        raise NvqError(f"{name} must be a pair (int8 codes, fp32 scales)") from None
+
+
+def int8_quantize(x, codes=None, scales=None):
+    """bf16 x [..., C] -> (int8 codes [..., C], fp32 scales [...]), one scale per row: scale = max|x| / 127, codes to the
+    nearest, ties to even (include/nvq.h)."""
+    _need(x, torch.bfloat16, "x")
+    if x.dim() < 1:
+        raise NvqError("x must have at least one dimension")
+    dev, lead, Cdim = x.device, x.shape[:-1], x.shape[-1]
+    R = lead.numel()
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.empty(lead, dtype=torch.float32, device=dev)
+    _launch("int8_quantize", dev, x.data_ptr(), R, Cdim, _arg(codes, torch.int8, "codes", x.shape, dev),
+            _arg(scales, torch.float32, "scales", lead, dev))
+    return codes, scales
+
+
+def int8_dequantize(codes, scales, out_dtype=torch.float32, out=None):
+    """int8 codes [..., C], fp32 scales [...] -> codes * scales in out_dtype (fp32 or bf16)."""
+    _need(codes, torch.int8, "codes")
+    if codes.dim() < 1:
+        raise NvqError("codes must have at least one dimension")
+    dev, lead = codes.device, codes.shape[:-1]
+    od = _float_mode(out_dtype if out is None else out.dtype, "out_dtype")
+    if out is None:
+        out = torch.empty(codes.shape, dtype=out_dtype, device=dev)
+    _launch("int8_dequantize", dev, codes.data_ptr(), _arg(scales, torch.float32, "scales", lead, dev), lead.numel(),
+            codes.shape[-1], _arg(out, out.dtype, "out", codes.shape, dev), od)
+    return out
+
+
+def linear_act_int8(xq, wq, bias=None, act=ACT_NONE, residual=None, out_dtype=torch.bfloat16, out=None):
+    """act((x @ w.T) + bias) + residual in int8 (include/nvq.h): xq = (codes [M, K], scales [M]), wq = (codes [N, K],
+    scales [N]) (ACT_SWIGLU: 2N rows), bias fp32, residual bf16 [M, N] -> out [M, N] in out_dtype."""
+    i8, f32 = torch.int8, torch.float32
+    (x, xs), (w, wsc) = _pair(xq, "xq"), _pair(wq, "wq")
+    dev, (M, K) = _main(x, i8, "xq", 2)
+    rows, N = _linear_sizes(w, act)
+    od = _float_mode(out_dtype if out is None else out.dtype, "out_dtype")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _launch("linear_act_int8", dev, x.data_ptr(), _arg(xs, f32, "x scales", (M,), dev),
+            _arg(w, i8, "wq", (rows, K), dev), _arg(wsc, f32, "w scales", (rows,), dev),
+            _arg(bias, f32, "bias", (rows,), dev), _arg(residual, torch.bfloat16, "residual", (M, N), dev), M, N, K, act,
+            _arg(out, out.dtype, "out", (M, N), dev), od)
+    return out
+
+
+def moe_fc1_swiglu_int8(xq, offsets, sorted2assign, k, w1q, h=None, ws=None):
+    """xq = (codes [T, d], scales [T]); w1q = (codes [E, 2 d_ff, d], scales [E, 2 d_ff]) -> h bf16 [T*k, d_ff] in sorted
+    order. Rows from offsets[E] on are left as they were (undefined in a new `h`)."""
+    i8, f32 = torch.int8, torch.float32
+    (x, xs), (w1, w1s) = _pair(xq, "xq"), _pair(w1q, "w1q")
+    dev, (T, d) = _main(x, i8, "xq", 2)
+    E, rows, _ = _dims(w1, 3, "w1q")
+    d_ff, A = rows // 2, T * k
+    if h is None:
+        h = torch.empty((A, d_ff), dtype=torch.bfloat16, device=dev)
+    w, wp, wn = _scratch(lib().moe_gemm_int8_workspace_size(A, E), dev, ws)
+    _launch("moe_fc1_swiglu_int8", dev, x.data_ptr(), _arg(xs, f32, "x scales", (T,), dev), T, d,
+            _arg(offsets, torch.int32, "offsets", (E + 1,), dev), _arg(sorted2assign, torch.int32, "sorted2assign", (A,), dev),
+            k, E, d_ff, _arg(w1, i8, "w1q", (E, 2 * d_ff, d), dev), _arg(w1s, f32, "w1 scales", (E, 2 * d_ff), dev),
+            _arg(h, torch.bfloat16, "h", (A, d_ff), dev), wp, wn)
+    return h
+
+
+def moe_fc2_int8(hq, offsets, sorted2assign, w2q, y=None, ws=None):
+    """hq = (codes [A, d_ff], scales [A]); w2q = (codes [E, d, d_ff], scales [E, d]) -> y bf16 [A, d] in assignment order
+    (rows of dropped assignments untouched, undefined in a new `y`)."""
+    i8, f32 = torch.int8, torch.float32
+    (hc, hs), (w2, w2s) = _pair(hq, "hq"), _pair(w2q, "w2q")
+    dev, (A, d_ff) = _main(hc, i8, "hq", 2)
+    E, d, _ = _dims(w2, 3, "w2q")
+    if y is None:
+        y = torch.empty((A, d), dtype=torch.bfloat16, device=dev)
+    w, wp, wn = _scratch(lib().moe_gemm_int8_workspace_size(A, E), dev, ws)
+    _launch("moe_fc2_int8", dev, hc.data_ptr(), _arg(hs, f32, "h scales", (A,), dev), A, d_ff,
+            _arg(offsets, torch.int32, "offsets", (E + 1,), dev), _arg(sorted2assign, torch.int32, "sorted2assign", (A,), dev),
+            E, d, _arg(w2, i8, "w2q", (E, d, d_ff), dev), _arg(w2s, f32, "w2 scales", (E, d), dev),
+            _arg(y, torch.bfloat16, "y", (A, d), dev), wp, wn)
+    return y
+
+
+def moe_expert_fwd_int8(x, topk_ids, w1q, w2q, export=False, y=None, ws=None):
+    """INT8 expert forward. x bf16 [T, d]; topk_ids int32 [T, k]; w1q = (codes [E, 2 d_ff, d], scales [E, 2 d_ff]),
+    w2q = (codes [E, d, d_ff], scales [E, d]), as from int8_quantize -> y bf16 [T, k, d] (unweighted; rows of dropped
+    assignments untouched, undefined in a new `y`), plus a dict of the intermediates (xq_codes, xq_tscale, offsets,
+    sorted2assign, h, hq_codes, hq_tscale; the two tscale hold one scale per row) when export is set."""
+    i8, f32, bf = torch.int8, torch.float32, torch.bfloat16
+    (w1, w1s), (w2, w2s) = _pair(w1q, "w1q"), _pair(w2q, "w2q")
+    dev, (T, d) = _main(x, bf, "x", 2)
+    k = _dims(topk_ids, 2, "topk_ids")[1]
+    E, rows, _ = _dims(w1, 3, "w1q")
+    d_ff, A = rows // 2, T * k
+    if y is None:
+        y = torch.empty((T, k, d), dtype=bf, device=dev)
+    inter, bufs = {}, None
+    if export:
+        inter = dict(xq_codes=torch.empty((T, d), dtype=i8, device=dev), xq_tscale=torch.empty(T, dtype=f32, device=dev),
+                     offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+                     sorted2assign=torch.full((A,), -1, dtype=torch.int32, device=dev),
+                     h=torch.zeros((A, d_ff), dtype=bf, device=dev),
+                     hq_codes=torch.zeros((A, d_ff), dtype=i8, device=dev),
+                     hq_tscale=torch.zeros(A, dtype=f32, device=dev))
+        bufs = MoeBuffers(**{f: (inter[f].data_ptr() if f in inter else None) for f, _ in MoeBuffers._fields_[:-1]},
+                          gemm_workgroups=0)
+    w, wp, wn = _scratch(lib().moe_expert_fwd_int8_workspace_size(T, d, k, E, d_ff), dev, ws)
+    _launch("moe_expert_fwd_int8", dev, x.data_ptr(), T, d, _arg(topk_ids, torch.int32, "topk_ids", (T, k), dev), k, E,
+            d_ff, _arg(w1, i8, "w1q", (E, 2 * d_ff, d), dev), _arg(w1s, f32, "w1 scales", (E, 2 * d_ff), dev),
+            _arg(w2, i8, "w2q", (E, d, d_ff), dev), _arg(w2s, f32, "w2 scales", (E, d), dev),
+            _arg(y, bf, "y", (T, k, d), dev), C.byref(bufs) if bufs is not None else None, wp, wn)
+    return (y, inter) if export else y

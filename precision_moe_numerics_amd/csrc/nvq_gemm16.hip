@@ -62,21 +62,21 @@ __global__ __launch_bounds__(kTabThreads) void k_tile_table(const int32_t* __res
     }
 }
 
-template <int MODE, int EPI, bool AHEAD>
+template <int MODE, int EPI, bool AHEAD, bool I8>
 void run(Args p, int64_t m_tiles_cap, hipStream_t s) {
     constexpr int TNO = EPI == kEpiGlu ? 64 : 128;
     p.n_tiles = (p.N + TNO - 1) / TNO;
     p.total = (int)(m_tiles_cap * p.n_tiles);
     const unsigned grid = ((unsigned)p.total + 7u) & ~7u;  // xcd_id: whole rounds of the 8 XCDs
-    hipLaunchKernelGGL((k_gemm16<MODE, EPI, 128, 128, 2, 2, AHEAD>), dim3(grid), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_gemm16<MODE, EPI, 128, 128, 2, 2, AHEAD, I8>), dim3(grid), dim3(256), 0, s, p);
 }
 // Reading a stage ahead pays where a CU has one workgroup, whose reads nothing else covers (512 x 1024 x 4096 47 us
 // without, 37 with; 2048^3 27.6, 25.3); with two it costs (16384 x 384 x 4096 65, 69; the weight gradient of 4091 x 2048
 // x 4096 74, 78), but for the transposed reads of dgrad (8192 rows, 8 experts of 2048 x 4096 163, 153).
-template <int MODE, int EPI>
+template <int MODE, int EPI, bool I8 = false>
 void run_ahead(const Args& p, int64_t m_tiles_cap, bool one, hipStream_t s) {
-    if (one) run<MODE, EPI, true>(p, m_tiles_cap, s);
-    else run<MODE, EPI, false>(p, m_tiles_cap, s);
+    if (one) run<MODE, EPI, true, I8>(p, m_tiles_cap, s);
+    else run<MODE, EPI, false, I8>(p, m_tiles_cap, s);
 }
 
 // Multiplier and shift of div_by.
@@ -92,42 +92,42 @@ static void set_div(uint32_t d, uint32_t* mul, int32_t* shift) {
     *shift = s - 1;
 }
 
-template <int MODE, int EPI>
+template <int MODE, int EPI, bool I8 = false>
 void run_big(Args p, int64_t m_tiles_cap, hipStream_t s) {
     constexpr int TNO = EPI == kEpiGlu ? kBigT / 2 : kBigT;
     p.n_tiles = (p.N + TNO - 1) / TNO;
     p.total = (int)(m_tiles_cap * p.n_tiles);
     const unsigned grid = std::min(((unsigned)p.total + 7u) & ~7u, std::max((unsigned)device_cus() & ~7u, 8u));
     set_div((uint32_t)(kGroupM * p.n_tiles), &p.group_mul, &p.group_shift);
-    hipLaunchKernelGGL((k_gemm16_big<MODE, EPI>), dim3(grid), dim3(64 * kBigWaves), 0, s, p);
+    hipLaunchKernelGGL((k_gemm16_big<MODE, EPI, I8>), dim3(grid), dim3(64 * kBigWaves), 0, s, p);
 }
 
-template <int EPI, int MB, int KS>
+template <int EPI, int MB, int KS, bool I8>
 void run_skinny(Args p, hipStream_t s) {
     constexpr int TN = (EPI == kEpiGlu ? 8 : 16) * (kSkWaves / KS);
     p.n_tiles = (p.N + TN - 1) / TN;
     int64_t mt = (p.rows + 16 * MB - 1) / (16 * MB);
     if (p.seg) mt = std::min<int64_t>(p.rows, mt + p.E);
-    hipLaunchKernelGGL((k_gemm16_skinny<EPI, MB, KS>), dim3((unsigned)(mt * p.n_tiles)), dim3(64 * kSkWaves), 0, s, p);
+    hipLaunchKernelGGL((k_gemm16_skinny<EPI, MB, KS, I8>), dim3((unsigned)(mt * p.n_tiles)), dim3(64 * kSkWaves), 0, s, p);
 }
 // K in as few parts as give the chip waves enough, some 2048: a part costs its share of the sum through LDS (fc2 of 64
 // tokens, 384 experts: 522 us in 2 parts, 653 in 4, 986 in 8; 16 rows x 4096 x 4096, 256 blocks: 35, 20 and 12).
-template <int EPI, int MB>
+template <int EPI, int MB, bool I8>
 void run_skinny_k(const Args& p, hipStream_t s) {
     const int64_t mt = (p.rows + 16 * MB - 1) / (16 * MB);
     const int64_t blocks = (p.seg ? std::min<int64_t>(p.rows, mt + p.E) : mt) * ((p.N + 15) / 16);
-    if (blocks >= 1024) run_skinny<EPI, MB, 2>(p, s);
-    else if (blocks >= 512) run_skinny<EPI, MB, 4>(p, s);
-    else run_skinny<EPI, MB, 8>(p, s);
+    if (blocks >= 1024) run_skinny<EPI, MB, 2, I8>(p, s);
+    else if (blocks >= 512) run_skinny<EPI, MB, 4, I8>(p, s);
+    else run_skinny<EPI, MB, 8, I8>(p, s);
 }
 // Rows of x a workgroup takes: those of a typical expert, up to 64 where that still gives the chip workgroups (64 rows
 // x 4096 x 4096: 23 us with 64, 27 with 32; 128 x 1024 x 4096: 23 and 15).
-template <int EPI>
+template <int EPI, bool I8>
 void run_skinny_rows(const Args& p, int64_t active, hipStream_t s) {
     const int64_t per = (p.rows + active - 1) / active, blocks = EPI == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
-    if (per <= 16) run_skinny_k<EPI, 1>(p, s);
-    else if (per > 32 && (p.rows + 63) / 64 * blocks >= 256) run_skinny_k<EPI, 4>(p, s);
-    else run_skinny_k<EPI, 2>(p, s);
+    if (per <= 16) run_skinny_k<EPI, 1, I8>(p, s);
+    else if (per > 32 && (p.rows + 63) / 64 * blocks >= 256) run_skinny_k<EPI, 4, I8>(p, s);
+    else run_skinny_k<EPI, 2, I8>(p, s);
 }
 
 }  // namespace g16
@@ -177,13 +177,14 @@ static bool big_tiles(double big, double small, int cus) {
     return 13.0 * std::max(1.0, std::ceil(big / cus)) < t_small;
 }
 
-void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
+template <bool I8>
+static void launch(int mode, int epi, Args p, void* ws, hipStream_t s) {
     set_div(p.a_div, &p.a_mul, &p.a_shift);
     set_div(p.b_div, &p.b_mul, &p.b_shift);
     const int64_t n_big = (p.N + (epi == kEpiGlu ? 127 : 255)) / (epi == kEpiGlu ? 128 : 256);
     const int64_t n_small = (p.N + (epi == kEpiGlu ? 63 : 127)) / (epi == kEpiGlu ? 64 : 128);
     const int cus = device_cus();
-    if (mode == kWgrad) {
+    if (!I8 && mode == kWgrad) {
         const int64_t mb = (p.M + 255) / 256 * (int64_t)p.E, ms = (p.M + 127) / 128 * (int64_t)p.E;
         if (big_tiles((double)mb * n_big, (double)ms * n_small, cus)) {
             p.m_tiles = (p.M + 255) / 256;
@@ -206,9 +207,9 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
         const double tiles = (double)(active + p.rows / 128) * n_small;
         // (its workgroups are at most five per tile: the bound keeps a launch below 2^32 work-items)
         if (tiles < (1 << 18) && skinny < 0.55 * ((p.K + 63) / 64) * std::max(1.0, tiles / 512)) {
-            if (epi == kEpiGlu) run_skinny_rows<kEpiGlu>(p, active, s);
-            else if (epi == kEpiAct) run_skinny_rows<kEpiAct>(p, active, s);
-            else run_skinny_rows<kEpiOut>(p, active, s);
+            if (epi == kEpiGlu) run_skinny_rows<kEpiGlu, I8>(p, active, s);
+            else if (epi == kEpiAct) run_skinny_rows<kEpiAct, I8>(p, active, s);
+            else run_skinny_rows<kEpiOut, I8>(p, active, s);
             return;
         }
     }
@@ -233,17 +234,20 @@ void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) {
         mt = (p.rows + tm - 1) / tm;
     }
     if (big) {
-        if (mode == kDgrad) run_big<kDgrad, kEpiOut>(p, mt, s);
-        else if (epi == kEpiGlu) run_big<kFwd, kEpiGlu>(p, mt, s);
-        else if (epi == kEpiAct) run_big<kFwd, kEpiAct>(p, mt, s);
-        else run_big<kFwd, kEpiOut>(p, mt, s);
+        if (!I8 && mode == kDgrad) run_big<kDgrad, kEpiOut>(p, mt, s);
+        else if (epi == kEpiGlu) run_big<kFwd, kEpiGlu, I8>(p, mt, s);
+        else if (epi == kEpiAct) run_big<kFwd, kEpiAct, I8>(p, mt, s);
+        else run_big<kFwd, kEpiOut, I8>(p, mt, s);
         return;
     }
     const bool one = m_tiles(128) * n_small <= cus;  // tile per CU
-    if (mode == kDgrad) run<kDgrad, kEpiOut, true>(p, mt, s);
-    else if (epi == kEpiGlu) run_ahead<kFwd, kEpiGlu>(p, mt, one, s);
-    else if (epi == kEpiAct) run_ahead<kFwd, kEpiAct>(p, mt, one, s);
-    else run_ahead<kFwd, kEpiOut>(p, mt, one, s);
+    if (!I8 && mode == kDgrad) run<kDgrad, kEpiOut, true, false>(p, mt, s);
+    else if (epi == kEpiGlu) run_ahead<kFwd, kEpiGlu, I8>(p, mt, one, s);
+    else if (epi == kEpiAct) run_ahead<kFwd, kEpiAct, I8>(p, mt, one, s);
+    else run_ahead<kFwd, kEpiOut, I8>(p, mt, one, s);
 }
+
+void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) { launch<false>(mode, epi, p, ws, s); }
+void launch_gemm8(int epi, Args p, void* ws, hipStream_t s) { launch<true>(kFwd, epi, p, ws, s); }
 
 }  // namespace nvq

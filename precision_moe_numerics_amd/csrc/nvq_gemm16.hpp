@@ -8,6 +8,8 @@
 //   k_gemm16_big     256 x 256 tiles in one persistent stream per CU
 //                    (nvq_gemm16_big.hpp);
 //   k_gemm16_skinny  FWD of a few rows per expert (nvq_gemm16_skinny.hpp).
+// All three also multiply int8 operands with a scale per row of either (FWD
+// only; int32 accumulation, the scales in the epilogue): see mfma64.
 // Operand arrangements:
 //   FWD    A rows and B rows hold k contiguously (x W^T);
 //   DGRAD  A as above, B holds n contiguously (g W, W as the forward keeps it);
@@ -66,7 +68,24 @@ struct Args {
     int32_t M, N, K;          // WGRAD: M x N outputs; FWD, DGRAD: N columns (GLU: N outputs), K
     int32_t m_tiles, n_tiles, total;  // tiles: of an expert's rows (WGRAD), of columns, in all (segments: at most)
     int32_t out_f32, accumulate, act;
+    // int8 operands: the scale of each source row of a and of each row of b (all experts'); lda, ldb and K are then in
+    // units of two bytes, as everything that moves operands counts
+    const float* a_scale;
+    const float* b_scale;
 };
+
+// The products of 16 rows of either operand over 64 bytes of K, bf16 or int8: the operands lie alike in memory, LDS and
+// registers (16 bytes of a row per lane), so only this instruction and the accumulators' type differ. An int8 sum is
+// exact: K < 2^17 terms of at most 2^14.
+template <bool I8>
+using Acc = std::conditional_t<I8, i32x4, f32x4>;
+template <bool I8>
+__device__ __forceinline__ Acc<I8> mfma64(bf16x8 b, bf16x8 a, Acc<I8> c) {
+    if constexpr (I8)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+}
 
 // ------------------------------------------------------------------ LDS staging
 // 16 bytes per lane from a buffer straight into LDS at lds_addr + 16 * lane.
@@ -214,6 +233,7 @@ __device__ __forceinline__ f32x4 load4_bf16(const uint16_t* p) {
 struct Pos {
     int64_t out_base;  // WGRAD: first element of the expert's matrix
     int row0, row_end, col0, pair_step;
+    int e;             // int8: the expert
     __device__ __forceinline__ int row(int i) const { return row0 + 16 * (i & 3) + 128 * (i >> 2); }
     __device__ __forceinline__ int col(int pair) const { return col0 + pair_step * pair; }
 };
@@ -303,10 +323,23 @@ __device__ __forceinline__ void epilogue_wgrad(const Args& p, const f32x4 (&acc)
     }
 }
 
-template <int EPI, int ACT, int MF, int NF>
-__device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[MF][NF], const Pos& o, int lane) {
+// v / d for 0 <= v < 2^31: with 2^(s-1) < d <= 2^s and mul = floor(2^(31+s) / d) + 1 < 2^32 (host), exactly
+// (v * mul) >> (31 + s); d = 1 is shift -1. (A hardware division is some twenty instructions.)
+__device__ __forceinline__ uint32_t div_by(uint32_t v, uint32_t mul, int shift) {
+    return shift < 0 ? v : __umulhi(v, mul) >> shift;
+}
+
+// Scale of logical row m of a (int8).
+__device__ __forceinline__ float row_scale(const Args& p, int m) {
+    return p.a_scale[p.a_gather ? div_by((uint32_t)p.a_gather[m], p.a_mul, p.a_shift) : (uint32_t)m];
+}
+
+template <int EPI, int ACT, typename V, int MF, int NF>
+__device__ __forceinline__ void epilogue_act(const Args& p, const V (&acc)[MF][NF], const Pos& o, int lane) {
+    constexpr bool I8 = std::is_same_v<V, i32x4>;
     const int N = p.N;
     const int c4 = (lane >> 4) * 4;
+    const float* bs = I8 ? p.b_scale + (int64_t)o.e * (EPI == kEpiGlu ? 2 : 1) * N : nullptr;
     constexpr int NP = EPI == kEpiGlu ? NF / 4 : NF / 2;  // pairs of output blocks
     constexpr int CH = MF < 4 ? MF : 4;                   // rows whose residual is loaded together
 #pragma unroll
@@ -331,6 +364,12 @@ __device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[M
             if (m >= o.row_end) continue;
             const int64_t r = EPI == kEpiOut && p.scatter ? p.scatter[m] : m;
             const int64_t base = o.out_base + r * N;
+            const float xs = I8 ? row_scale(p, m) : 1.0f;
+            // the value of accumulators whose first column is (scale) row n of b
+            auto value = [&](const V& a, int n) {
+                if constexpr (I8) return __builtin_convertvector(a, f32x4) * xs * *reinterpret_cast<const f32x4*>(bs + n);
+                else return a;
+            };
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
                 const int n = o.col(q);
@@ -339,12 +378,13 @@ __device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[M
                 for (int t = 0; t < 2; ++t) {
                     const int nn = n + 16 * t + c4;
                     if (EPI == kEpiOut) {
-                        v[t] = acc[i][2 * q + t];
+                        v[t] = value(acc[i][2 * q + t], min(nn, N - 4));
                     } else if (EPI == kEpiAct) {
-                        v[t] = acc[i][2 * q + t];
+                        v[t] = value(acc[i][2 * q + t], min(nn, N - 4));
                         if (p.bias) v[t] += *reinterpret_cast<const f32x4*>(p.bias + min(nn, N - 4));
                     } else {
-                        f32x4 g = acc[i][4 * q + 2 * t], u = acc[i][4 * q + 2 * t + 1];
+                        f32x4 g = value(acc[i][4 * q + 2 * t], min(nn, N - 4));
+                        f32x4 u = value(acc[i][4 * q + 2 * t + 1], N + min(nn, N - 4));
                         if (p.bias) {
                             g += *reinterpret_cast<const f32x4*>(p.bias + min(nn, N - 4));
                             u += *reinterpret_cast<const f32x4*>(p.bias + N + min(nn, N - 4));
@@ -364,10 +404,10 @@ __device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[M
                     f32x4 g[2], u[2];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        g[t] = acc[i][4 * q + 2 * t];
-                        u[t] = acc[i][4 * q + 2 * t + 1];
+                        const int nn = min(n + 16 * t + c4, N - 4);
+                        g[t] = value(acc[i][4 * q + 2 * t], nn);
+                        u[t] = value(acc[i][4 * q + 2 * t + 1], N + nn);
                         if (p.bias) {
-                            const int nn = min(n + 16 * t + c4, N - 4);
                             g[t] += *reinterpret_cast<const f32x4*>(p.bias + nn);
                             u[t] += *reinterpret_cast<const f32x4*>(p.bias + N + nn);
                         }
@@ -390,8 +430,8 @@ __device__ __forceinline__ void epilogue_act(const Args& p, const f32x4 (&acc)[M
 }
 
 // One scalar branch on the activation, outside the unrolled stores.
-template <int EPI, int MF, int NF>
-__device__ __forceinline__ void epilogue(const Args& p, const f32x4 (&acc)[MF][NF], const Pos& o, int lane) {
+template <int EPI, typename V, int MF, int NF>
+__device__ __forceinline__ void epilogue(const Args& p, const V (&acc)[MF][NF], const Pos& o, int lane) {
     if constexpr (EPI != kEpiAct) {
         epilogue_act<EPI, NVQ_ACT_NONE>(p, acc, o, lane);
     } else {
@@ -412,12 +452,6 @@ __device__ __forceinline__ T sload(const T* base, int64_t i) {
     return ((ct*)base)[i];
 }
 
-// v / d for 0 <= v < 2^31: with 2^(s-1) < d <= 2^s and mul = floor(2^(31+s) / d) + 1 < 2^32 (host), exactly
-// (v * mul) >> (31 + s); d = 1 is shift -1. (A hardware division is some twenty instructions.)
-__device__ __forceinline__ uint32_t div_by(uint32_t v, uint32_t mul, int shift) {
-    return shift < 0 ? v : __umulhi(v, mul) >> shift;
-}
-
 // Virtual id of a workgroup: consecutive ids on one XCD (workgroups are dealt to
 // the 8 XCDs round robin), ids 0 .. n - 1 spread over all of them. -1 where the
 // grid has more workgroups than ids.
@@ -435,7 +469,7 @@ __device__ __forceinline__ int xcd_id(int n) {
 // of the 128 x 128 tile share a CU and cover each other's waits. AHEAD: a step
 // reads the stage after its own into a second set of registers under the first
 // half of its products, and fetches the one three steps on.
-template <int MODE, int EPI, int TM, int TN, int WM, int WN, bool AHEAD>
+template <int MODE, int EPI, int TM, int TN, int WM, int WN, bool AHEAD, bool I8>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     constexpr int NW = WM * WN;
     constexpr int MF = TM / WM / 16, NF = TN / WN / 16;
@@ -560,11 +594,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
         }
     };
 
-    f32x4 acc[MF][NF];
+    Acc<I8> acc[MF][NF];
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < NF; ++j) acc[i][j] = (Acc<I8>){0, 0, 0, 0};
 
     if (nk > 0) issue(0);
     if (nk > 1) issue(1);
@@ -595,7 +629,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
         for (int i = 0; i < MF; ++i)
 #pragma unroll
             for (int j = 0; j < NF; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[ks][j], f.a[ks][i], acc[i][j], 0, 0, 0);
+                acc[i][j] = mfma64<I8>(f.b[ks][j], f.a[ks][i], acc[i][j]);
     };
     // this wave's loads of stage s have landed, those of stage s + 1 may be under way
     auto landed = [&](int s) {
@@ -655,6 +689,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     o.row_end = row_end;
     o.col0 = col0 + wn * (TNO / WN);
     o.pair_step = 32;
+    o.e = e;
     if constexpr (MODE == kWgrad) {
         const bool full = o.row0 + TM / WM <= o.row_end && o.col0 + TN / WN <= p.N;
         if (p.out_f32) epilogue_wgrad<true>(p, acc, o, rows_lds[wave], full, lane);
@@ -670,6 +705,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
 // tile counts are filled in here). `ws` holds gemm16_ws_bytes for segmented
 // FWD and DGRAD. mode is g16::kFwd, kDgrad or kWgrad.
 void launch_gemm16(int mode, int epi, g16::Args p, void* ws, hipStream_t s);
+// The same in int8 (FWD): p.a and p.b hold int8, p.a_scale and p.b_scale their scales; lda, ldb and K count pairs.
+void launch_gemm8(int epi, g16::Args p, void* ws, hipStream_t s);
 size_t gemm16_ws_bytes(int64_t rows, int64_t E);
 // Whether every tile count and lane offset of the product fits (see the limits in nvq.h).
 bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int64_t N, int64_t K);

@@ -288,15 +288,14 @@ __device__ __forceinline__ void big_read_b(FragB& f, const uint8_t* half, int wa
 // The eight products of an A half (blocks i0 ..) and a B half (blocks j0 ..)
 // in K half ks, with READS LDS reads (already written, into registers these
 // products do not use) spread between them.
-template <bool MUL, int READS>
-__device__ __forceinline__ void big_mul(f32x4 (*acc)[4], int i0, int j0, const FragA& a, const FragB& b, int ks) {
+template <bool MUL, int READS, bool I8>
+__device__ __forceinline__ void big_mul(Acc<I8> (*acc)[4], int i0, int j0, const FragA& a, const FragB& b, int ks) {
     if (MUL) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                acc[i0 + i][j0 + j] =
-                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[j][ks], a.v[i][ks], acc[i0 + i][j0 + j], 0, 0, 0);
+                acc[i0 + i][j0 + j] = mfma64<I8>(b.v[j][ks], a.v[i][ks], acc[i0 + i][j0 + j]);
 #pragma unroll
         for (int r = 0; r < READS; ++r) {
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -322,7 +321,7 @@ __device__ __forceinline__ void big_mul(f32x4 (*acc)[4], int i0, int j0, const F
 // half, everything but the newest five halves (10 loads of the wave) has
 // landed; a half has six quarters of some 512 matrix cycles to arrive.
 // (Ten slots, the whole LDS and eight quarters, measured no faster.)
-template <int MODE, int EPI>
+template <int MODE, int EPI, bool I8>
 __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kHalf];
     __shared__ int32_t rows_lds[kBigWaves][64];
@@ -372,6 +371,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
                 q[0] = T.row0;
                 q[1] = T.row_end;
                 q[2] = T.col0;
+                if (I8) q[3] = T.e;
             }
         }
         lw.next(p, G, total, m_count);
@@ -437,11 +437,11 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
         constexpr int NA = decltype(na_tag)::value;
         constexpr int RA = Load::A_R ? 8 : 4, RB = Load::B_R ? 8 : 4;  // LDS reads of half the A, all the B fragments
         const int nk = (T.klen + kBigK - 1) / kBigK;
-        f32x4 acc[NA ? 4 * NA : 1][4];
+        Acc<I8> acc[NA ? 4 * NA : 1][4];
 #pragma unroll
         for (int i = 0; i < 4 * NA; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < 4; ++j) acc[i][j] = (Acc<I8>){0, 0, 0, 0};
         // loads older than the newest five halves, where stores of the tile before may lie between
         auto settled = [&](bool steady) {
             if (steady) wait_vm<kNew>();
@@ -459,36 +459,36 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
             stage_barrier();
             fetch(kB0, base, 0);
             if (NA > 0) big_read_a<Load::A_R>(a, A0, 1, wave, lane);
-            big_mul<(NA > 0), RA>(acc, 0, 0, a, b0, 0);
+            big_mul<(NA > 0), RA, I8>(acc, 0, 0, a, b0, 0);
             fetch(kB0, base, 1);
             if (NA > 0) big_read_b<Load::B_R>(b1, B1, wave, lane);
-            big_mul<(NA > 0), RB>(acc, 0, 0, a, b0, 1);
+            big_mul<(NA > 0), RB, I8>(acc, 0, 0, a, b0, 1);
             // quarter 1
             settled(s > 1);
             stage_barrier();
             fetch(kA0, slot_of(1), 0);
-            big_mul<(NA > 0), 0>(acc, 0, 2, a, b1, 0);
+            big_mul<(NA > 0), 0, I8>(acc, 0, 2, a, b1, 0);
             fetch(kA0, slot_of(1), 1);
             if (NA > 1) big_read_a<Load::A_R>(a, A1, 0, wave, lane);
-            big_mul<(NA > 0), (NA > 1 ? RA : 0)>(acc, 0, 2, a, b1, 1);
+            big_mul<(NA > 0), (NA > 1 ? RA : 0), I8>(acc, 0, 2, a, b1, 1);
             // quarter 2 (nothing new is needed, and B1 was read before the last barrier)
             typename Load::Entries ea = {0, 0, 0, 0, 0, 0, 0, 0}, eb = ea;
             if (gat_a) ea = ld.entries(p.a_gather, ld.k + kBigK, wave);  // for the next stage
             fetch(kB1, slot_of(2), 0);
             if (NA > 1) big_read_a<Load::A_R>(a, A1, 1, wave, lane);
-            big_mul<(NA > 1), RA>(acc, 4, 2, a, b1, 0);
+            big_mul<(NA > 1), RA, I8>(acc, 4, 2, a, b1, 0);
             fetch(kB1, slot_of(2), 1);
-            big_mul<(NA > 1), 0>(acc, 4, 2, a, b1, 1);
+            big_mul<(NA > 1), 0, I8>(acc, 4, 2, a, b1, 1);
             // quarter 3
             settled(s > 0);
             stage_barrier();
             if (gat_b) eb = ld.entries(p.b_gather, ld.k + kBigK, wave);
             fetch(kA1, slot_of(3), 0);
             big_read_b<Load::B_R>(b1, nB0, wave, lane);
-            big_mul<(NA > 1), RB>(acc, 4, 0, a, b0, 0);
+            big_mul<(NA > 1), RB, I8>(acc, 4, 0, a, b0, 0);
             fetch(kA1, slot_of(3), 1);
             big_read_a<Load::A_R>(a, nA0, 0, wave, lane);
-            big_mul<(NA > 1), RA>(acc, 4, 0, a, b0, 1);
+            big_mul<(NA > 1), RA, I8>(acc, 4, 0, a, b0, 1);
             ld.advance(p);
             if (settle()) {
                 if (gat_a) ea = ld.entries(p.a_gather, ld.k, wave);
@@ -515,6 +515,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
             o.row_end = T.row_end;
             o.col0 = T.col0 + wn * 32;
             o.pair_step = 128;
+            o.e = T.e;
             if constexpr (MODE == kWgrad) {
                 if (p.out_f32) epilogue_wgrad<true>(p, acc, o, row_buf[wave], full, lane);
                 else epilogue_wgrad<false>(p, acc, o, row_buf[wave], full, lane);
@@ -535,7 +536,8 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
             T.row_end = __builtin_amdgcn_readfirstlane(q[1]);
             T.col0 = __builtin_amdgcn_readfirstlane(q[2]);
             T.klen = p.K;
-            T.e = T.k0 = 0;
+            T.e = I8 ? __builtin_amdgcn_readfirstlane(q[3]) : 0;
+            T.k0 = 0;
         }
         const int rows = T.row_end - (T.row0 + wm * 64);
         if (rows > 128) tile(T, std::integral_constant<int, 2>{});

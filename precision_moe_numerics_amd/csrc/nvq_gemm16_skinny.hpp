@@ -55,9 +55,10 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int rows, i
 // straight into registers, a batch of steps at once, the weights past the
 // caches (they are read once); rows of x that do not exist cost no traffic. The
 // sums of the KS parts meet in LDS and are added in order.
-template <int EPI, int MB, int KS>
+template <int EPI, int MB, int KS, bool I8>
 __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
-    __shared__ float red[kSkWaves][MB][16][17];
+    using Sum = std::conditional_t<I8, int, float>;
+    __shared__ Sum red[kSkWaves][MB][16][17];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int nt = blockIdx.x % p.n_tiles, mt = blockIdx.x / p.n_tiles;
@@ -94,9 +95,9 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
     const int steps = (p.K + 31) / 32;
     const int part = ((steps + KS - 1) / KS + 1) & ~1;  // even: whole 128-byte lines
     const int s_end = min((part_k + 1) * part, steps);
-    f32x4 acc[MB];
+    Acc<I8> acc[MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) acc[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < MB; ++i) acc[i] = (Acc<I8>){0, 0, 0, 0};
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     for (int s0 = part_k * part; s0 < s_end; s0 += kSkBatch) {
         u32x4 bv[kSkBatch], av[kSkBatch][MB];
@@ -113,8 +114,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
         for (int j = 0; j < kSkBatch; ++j)
 #pragma unroll
             for (int i = 0; i < MB; ++i)
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bv[j]),
-                                                                 __builtin_bit_cast(bf16x8, av[j][i]), acc[i], 0, 0, 0);
+                acc[i] = mfma64<I8>(__builtin_bit_cast(bf16x8, bv[j]), __builtin_bit_cast(bf16x8, av[j][i]), acc[i]);
     }
     // lane: columns 4 (lane / 16) + t of row lane % 16
 #pragma unroll
@@ -123,10 +123,10 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
         for (int t = 0; t < 4; ++t) red[wave][i][4 * (lane >> 4) + t][r] = acc[i][t];
     __syncthreads();
     auto total = [&](int b, int i, int n, int m) {
-        float s = red[b * KS][i][n][m];
+        Sum s = red[b * KS][i][n][m];
 #pragma unroll
         for (int w = 1; w < KS; ++w) s += red[b * KS + w][i][n][m];
-        return s;
+        return (float)s;
     };
     auto put = [&](void* out, int64_t idx, float v, bool f32) {
         if (f32) static_cast<float*>(out)[idx] = v;
@@ -139,6 +139,9 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
         if (m >= row_end || col >= p.N) continue;
         const int64_t base = (EPI == kEpiOut && p.scatter ? (int64_t)p.scatter[m] : m) * p.N;
         float v = total(b, i, n, mr);
+        const float* bs = I8 ? p.b_scale + (int64_t)e * rows_per * p.N + col : nullptr;
+        const float xs = I8 ? row_scale(p, m) : 1.0f;
+        if (I8) v = v * xs * bs[0];
         if (EPI == kEpiAct) {
             if (p.bias) v += p.bias[col];
             if (p.z) put(p.z, base + col, v, false);
@@ -151,6 +154,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_gemm16_skinny(Args p) {
             }
         } else if (EPI == kEpiGlu) {
             float g = v, up = total(b, i, n + 8, mr);
+            if (I8) up = up * xs * bs[p.N];
             if (p.bias) {
                 g += p.bias[col];
                 up += p.bias[p.N + col];
