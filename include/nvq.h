@@ -630,6 +630,43 @@ int moe_fc2_int8(const int8_t* hq, const float* h_scales, int64_t A, int64_t d_f
                  uint16_t* y, void* ws, size_t ws_bytes, nvq_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* A whole mixture-of-experts layer for a few tokens (single tokens being    */
+/* decoded): router, chosen experts and combine in one call, for T <= 64.    */
+/*   logits = x . w_router^T (exact products, sums kept in fp64)              */
+/*   topk_ids, weights: as moe_router_softmax_topk (NVQ_ROUTER_SOFTMAX) or    */
+/*     moe_router_sigmoid_topk (NVQ_ROUTER_SIGMOID) choose from the logits,   */
+/*     which are not rounded in between; bias [E] fp32 (nullable: 0)          */
+/*   h = bf16(silu(W1g x) * (W1u x)) for every chosen expert                  */
+/*   out[t] = residual[t] + sum_s weights[t][s] * (W2 h), rounded once        */
+/* Only the weights are quantized; x and h are bf16, and what one token gets */
+/* does not depend on the others. w_router bf16 [E, d], residual (nullable)  */
+/* and out [T, d] bf16, topk_ids [T, k] int32 and weights [T, k] fp32 are    */
+/* outputs. Expert weights as for moe_expert_fwd_bf16, _int8 and _nvfp4; what */
+/* an expert's weights hold reaches only the tokens that chose it. Limits     */
+/* (else NVQ_ERR_DIM): 0 <= T <= 64, 1 <= k <= min(E, 64), E <= 1024, d and   */
+/* d_ff multiples of 8 (bf16), 16 (int8) or 32 (NVFP4) up to 2^22, one        */
+/* expert's matrix, w_router and T*k*d_ff bf16 values below 4 GiB - 512. All */
+/* pointers 16-byte aligned, ws 256-byte. Outputs must not overlap inputs or  */
+/* the workspace (residual == out is allowed). Non-finite logits: ids are     */
+/* distinct and in range, but otherwise undefined.                           */
+/* ------------------------------------------------------------------------ */
+enum { NVQ_ROUTER_SOFTMAX = 0, NVQ_ROUTER_SIGMOID = 1 };
+size_t moe_layer_decode_workspace_size(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff);
+int moe_layer_decode_bf16(const uint16_t* x, int64_t T, int64_t d, const uint16_t* w_router, const float* bias, int router,
+                          int k, int64_t E, int64_t d_ff, const uint16_t* w1, const uint16_t* w2,
+                          const uint16_t* residual, uint16_t* out, int32_t* topk_ids, float* weights, void* ws,
+                          size_t ws_bytes, nvq_stream_t stream);
+int moe_layer_decode_int8(const uint16_t* x, int64_t T, int64_t d, const uint16_t* w_router, const float* bias, int router,
+                          int k, int64_t E, int64_t d_ff, const int8_t* w1, const float* w1_scales, const int8_t* w2,
+                          const float* w2_scales, const uint16_t* residual, uint16_t* out, int32_t* topk_ids,
+                          float* weights, void* ws, size_t ws_bytes, nvq_stream_t stream);
+int moe_layer_decode_nvfp4(const uint16_t* x, int64_t T, int64_t d, const uint16_t* w_router, const float* bias, int router,
+                           int k, int64_t E, int64_t d_ff, const uint8_t* w1_codes, const uint8_t* w1_scales,
+                           const float* w1_tscale, const uint8_t* w2_codes, const uint8_t* w2_scales,
+                           const float* w2_tscale, const uint16_t* residual, uint16_t* out, int32_t* topk_ids,
+                           float* weights, void* ws, size_t ws_bytes, nvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Converter checks. Every code, scale byte and bf16 output above comes from */
 /* a handful of gfx950 conversion instructions (and two software encoders);  */
 /* their exactness against the format rules (NVFP4 about 4.5 bits per value */

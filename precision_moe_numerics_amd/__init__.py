@@ -20,6 +20,7 @@ RTN, SR = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 DGRAD, WGRAD, FWD = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_SWIGLU = range(6)
+ROUTER_SOFTMAX, ROUTER_SIGMOID = 0, 1
 (CVT_DQ_F16, CVT_FP4_F32, CVT_SCAN_E2M1, CVT_SCAN_E4M3_HW, CVT_SCAN_E4M3_SW, CVT_SCAN_BF16_HW,
  CVT_SCAN_BF16_SW, CVT_SR, CVT_DQ_MX_BF16, CVT_SR_E2M1_SWEEP, CVT_SR_E4M3_SWEEP, CVT_E4M3_PAIR_F32) = range(12)
 
@@ -126,6 +127,13 @@ _OPTIONAL = {
     "moe_expert_fwd_int8_workspace_size": ([_i64, _i64, C.c_int, _i64, _i64], _sz),
     "moe_expert_fwd_int8": ([_vp, _i64, _i64, _vp, C.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
                             C.c_int),
+    "moe_layer_decode_workspace_size": ([_i64, _i64, C.c_int, _i64, _i64], _sz),
+    "moe_layer_decode_bf16": ([_vp, _i64, _i64, _vp, _vp, C.c_int, C.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _sz, _vp], C.c_int),
+    "moe_layer_decode_int8": ([_vp, _i64, _i64, _vp, _vp, C.c_int, C.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _vp, _vp, _sz, _vp], C.c_int),
+    "moe_layer_decode_nvfp4": ([_vp, _i64, _i64, _vp, _vp, C.c_int, C.c_int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, _vp, _vp, _vp, _sz, _vp], C.c_int),
     "nvfp4_quantize_noalloc": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp, C.c_int, C.c_uint64, C.c_uint32, _vp],
                                C.c_int),
 }
@@ -996,3 +1004,66 @@ def moe_expert_fwd_int8(x, topk_ids, w1q, w2q, export=False, y=None, ws=None):
             _arg(w2, i8, "w2q", (E, d, d_ff), dev), _arg(w2s, f32, "w2 scales", (E, d), dev),
             _arg(y, bf, "y", (T, k, d), dev), C.byref(bufs) if bufs is not None else None, wp, wn)
     return (y, inter) if export else y
+
+
+# ------------------------------------------------------------------ the whole layer for a few tokens
+def _layer_decode(name, x, w_router, k, E, d_ff, w, bias, router, residual, out, ids, weights, ws):
+    bf, f32 = torch.bfloat16, torch.float32
+    dev, (T, d) = _main(x, bf, "x", 2)
+    if out is None:
+        out = torch.empty((T, d), dtype=bf, device=dev)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=f32, device=dev)
+    addresses = [_arg(t, dtype, n, shape, dev) for t, dtype, n, shape in w]
+    s, sp, sn = _scratch(lib().moe_layer_decode_workspace_size(T, d, k, E, d_ff), dev, ws)
+    _launch(name, dev, x.data_ptr(), T, d, _arg(w_router, bf, "w_router", (E, d), dev), _arg(bias, f32, "bias", (E,), dev),
+            router, k, E, d_ff, *addresses, _arg(residual, bf, "residual", (T, d), dev), _arg(out, bf, "out", (T, d), dev),
+            _arg(ids, torch.int32, "ids", (T, k), dev), _arg(weights, f32, "weights", (T, k), dev), sp, sn)
+    return out, ids, weights
+
+
+def moe_layer_decode_bf16(x, w_router, k, w1, w2, bias=None, router=ROUTER_SOFTMAX, residual=None, out=None, ids=None,
+                          weights=None, ws=None):
+    """A whole expert layer for up to 64 tokens (include/nvq.h): router, chosen experts and combine. x bf16 [T, d]; w_router
+    bf16 [E, d]; w1 bf16 [E, 2 d_ff, d]; w2 bf16 [E, d, d_ff]; bias fp32 [E]; residual bf16 [T, d]
+    -> (out bf16 [T, d], ids int32 [T, k], weights fp32 [T, k])."""
+    bf, d = torch.bfloat16, _dims(x, 2, "x")[1]
+    E, rows, _ = _dims(w1, 3, "w1")
+    f = rows // 2
+    return _layer_decode("moe_layer_decode_bf16", x, w_router, k, E, f,
+                         ((w1, bf, "w1", (E, 2 * f, d)), (w2, bf, "w2", (E, d, f))),
+                         bias, router, residual, out, ids, weights, ws)
+
+
+def moe_layer_decode_int8(x, w_router, k, w1q, w2q, bias=None, router=ROUTER_SOFTMAX, residual=None, out=None, ids=None,
+                          weights=None, ws=None):
+    """moe_layer_decode_bf16 on int8 weights (only the weights are quantized): w1q = (codes [E, 2 d_ff, d], scales
+    [E, 2 d_ff]), w2q = (codes [E, d, d_ff], scales [E, d]), as from int8_quantize."""
+    i8, f32, d = torch.int8, torch.float32, _dims(x, 2, "x")[1]
+    (w1, s1), (w2, s2) = _pair(w1q, "w1q"), _pair(w2q, "w2q")
+    E, rows, _ = _dims(w1, 3, "w1q")
+    f = rows // 2
+    return _layer_decode("moe_layer_decode_int8", x, w_router, k, E, f,
+                         ((w1, i8, "w1q", (E, 2 * f, d)), (s1, f32, "w1 scales", (E, 2 * f)),
+                          (w2, i8, "w2q", (E, d, f)), (s2, f32, "w2 scales", (E, d))),
+                         bias, router, residual, out, ids, weights, ws)
+
+
+def moe_layer_decode_nvfp4(x, w_router, k, w1q, w2q, bias=None, router=ROUTER_SOFTMAX, residual=None, out=None, ids=None,
+                           weights=None, ws=None):
+    """moe_layer_decode_bf16 on NVFP4 weights (only the weights are quantized): w1q and w2q = (codes, scales, tscale) as
+    from nvfp4_quantize(batched=True) of [E, 2 d_ff, d] and [E, d, d_ff]."""
+    u8, f32, d = torch.uint8, torch.float32, _dims(x, 2, "x")[1]
+    try:
+        (w1, s1, t1), (w2, s2, t2) = w1q, w2q
+    except (TypeError, ValueError):
+        raise NvqError("w1q and w2q must be triples (codes, scales, tscale)") from None
+    E, rows, _ = _dims(w1, 3, "w1q")
+    f = rows // 2
+    return _layer_decode("moe_layer_decode_nvfp4", x, w_router, k, E, f,
+                         ((w1, u8, "w1 codes", (E, 2 * f, d // 2)), (s1, u8, "w1 scales", (E, 2 * f, d // 16)),
+                          (t1, f32, "w1 tscale", (E,)), (w2, u8, "w2 codes", (E, d, f // 2)),
+                          (s2, u8, "w2 scales", (E, d, f // 16)), (t2, f32, "w2 tscale", (E,))),
+                         bias, router, residual, out, ids, weights, ws)
