@@ -1,18 +1,20 @@
 // nvq_decode.hip -- a whole mixture-of-experts layer for a few tokens (up to
 // 64, single tokens being decoded): router, chosen experts and weighted combine
-// on bf16, int8 or NVFP4 weights.
+// on bf16, int8 or NVFP4 weights, in two launches.
 //
-//   logits = x Wr^T                       k_decode_router
-//   ids, weights = top-k of the logits;
-//   h = silu(g) * u of every (expert, token) pair   k_decode_fc1
-//   out = residual + sum_s weight * (W2 h)          k_decode_fc2
+//   k_decode_router   logits = x Wr^T
+//   k_decode_layer    ids, weights = top-k of the logits;
+//                     h = silu(g) * u of every (expert, token) pair;
+//                     out = residual + sum_s weight * (W2 h)
 //
-// Bound by reading the chosen experts' weights once. The activations stay bf16
-// in all three formats: they are a few rows, and quantizing them would save
-// nothing. A weight reaches the matrix pipe as a bf16 value that holds it
-// exactly (int8 codes have 8 significant bits, e2m1 * e4m3 has 6); the channel's
-// or tensor's fp32 scale is applied to the fp32 sum. h is rounded to bf16, the
-// matrix pipe's type, once.
+// Bound by reading the chosen experts' weights once. The activations are not
+// quantized: they are a few rows, and it would save nothing. A weight reaches
+// the matrix pipe as a bf16 value that holds it exactly (int8 codes have 8
+// significant bits, e2m1 * e4m3 has 6); the channel's or tensor's fp32 scale is
+// applied to the fp32 sum. h goes to the matrix pipe as two bf16 parts, its
+// rounding and the rounding of what that left (2^-17 of it in all; one part
+// would be 2^-9, as much as out's own rounding), which costs only products and
+// these are far from the limit.
 #include "nvq_argmax.hpp"
 #include "nvq_device.hpp"
 #include "nvq_host.hpp"
@@ -38,6 +40,13 @@ constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr uint32_t kNowhere = 0xFFFFFFE0u;
 constexpr int64_t kMaxBytes = 0xFFFFFE00ll;
 
+// Device-wide counters of one call, cleared by k_decode_router.
+struct Counters {
+    uint32_t pick, picked;  // tasks of the choice taken, finished
+    uint32_t fc1, done;     // of fc1
+    uint32_t fc2;           // of fc2
+};
+
 struct Args {
     const uint16_t* x;
     const uint16_t* wr;
@@ -49,10 +58,15 @@ struct Args {
     uint16_t* out;
     int32_t* ids;
     float* weights;
-    double* logits;           // [T, E]
-    uint16_t* h;              // [T k, f], rows in expert order
-    int T, d, E, k, f, sigmoid;
+    double* logits;           // [parts, T, E]: sums over parts of K
+    uint16_t* h;              // [T k, f / 8, 2, 8], rows in expert order: each eight values' high, then low parts
+    Counters* count;
+    int T, d, E, k, f, sigmoid, parts;
 };
+
+// A value that all lanes of a wave hold, as a scalar: branches on it are the wave's, not a lane's. Every loop here that
+// holds a barrier ends on such a value.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
@@ -65,6 +79,8 @@ template <int FMT>
 struct Fmt {
     static constexpr int kVals = FMT == kBf16 ? 8 : FMT == kInt8 ? 16 : 32;  // in 16 bytes
     static constexpr int kFrags = kVals / 8;
+    static constexpr int NB = FMT == kBf16 ? 1 : FMT == kInt8 ? 2 : 4;  // fc1: groups of 16 weight rows of a wave
+    static constexpr int D1 = FMT == kBf16 ? 8 : 4, D2 = FMT == kNvfp4 ? 4 : 8;  // steps in flight in fc1, fc2
     static __host__ __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)(K / kVals) * 16u; }
 };
 
@@ -106,14 +122,6 @@ __device__ __forceinline__ bf16x8 decode(const W16& w, int i) {
     }
 }
 
-template <int FMT>
-__device__ __forceinline__ f32x4 product(const W16& w, const X16<FMT>& x, f32x4 acc) {
-#pragma unroll
-    for (int i = 0; i < Fmt<FMT>::kFrags; ++i)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode<FMT>(w, i), __builtin_bit_cast(bf16x8, x.v[i]), acc, 0, 0, 0);
-    return acc;
-}
-
 // The matrices of one expert: `rows` rows of K values.
 template <int FMT>
 struct Matrix {
@@ -144,33 +152,46 @@ __device__ __forceinline__ X16<FMT> load_x(__amdgpu_buffer_rsrc_t x, uint32_t ro
     return r;
 }
 
+// A barrier that orders LDS only: loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 w, u32x4 x, f32x4 acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+}
+
 // ------------------------------------------------------------------ router logits
-// One workgroup: 16 experts, 16 tokens, K over the waves. The sum of 32 products that one instruction adds is rounded
-// to fp32, 2^-24 of it; from there on the sums are fp64, so that of two close logits the larger one is chosen.
-__global__ __launch_bounds__(kThreads, 2) void k_decode_router(Args p) {
-    __shared__ double red[kWaves][16][17];
+// One workgroup: 16 experts, 16 tokens, a part of K, shared by its four waves. The sum of 32 products that one
+// instruction adds is rounded to fp32, 2^-24 of it; from there on the sums are fp64, so that of two close logits the
+// larger one is chosen. K is cut so that a token's logits are some 200 workgroups: with one per 16 experts (24 of 384)
+// the launch took 6.6 us.
+constexpr int kRouterWaves = 4;
+__global__ __launch_bounds__(64 * kRouterWaves) void k_decode_router(Args p) {
+    __shared__ double red[kRouterWaves][16][17];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
+    if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x == 0) *p.count = Counters{};
     const uint32_t rb = (uint32_t)p.d * 2u;
     const auto wr = rsrc(p.wr, (uint32_t)p.E * rb), xr = rsrc(p.x, (uint32_t)p.T * rb);
-    const int steps = (p.d + 31) / 32, part = (steps + kWaves - 1) / kWaves;
-    const int s1 = min((wave + 1) * part, steps);
+    const int steps = (p.d + 31) / 32, waves = p.parts * kRouterWaves, part = (steps + waves - 1) / waves;
+    const int first = ((int)blockIdx.z * kRouterWaves + wave) * part, s1 = min(first + part, steps);
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int s0 = wave * part; s0 < s1; s0 += 8) {
-        u32x4 w[8], x[8];
+    for (int s0 = first; s0 < s1; s0 += 4) {
+        u32x4 w[4], x[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
             const uint32_t o = (uint32_t)(s0 + j) * 64 + q * 16;
             const bool ok = s0 + j < s1 && o < rb;
             w[j] = __builtin_amdgcn_raw_buffer_load_b128(wr, ok && e0 + r < p.E ? (e0 + r) * rb + o : kNowhere, 0, 0);
             x[j] = __builtin_amdgcn_raw_buffer_load_b128(xr, ok && t0 + r < p.T ? (t0 + r) * rb + o : kNowhere, 0, 0);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-            const f32x4 a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[j]),
-                                                                    __builtin_bit_cast(bf16x8, x[j]), z, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+            const f32x4 a = mfma(__builtin_bit_cast(bf16x8, w[j]), x[j], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] += (double)a[i];
         }
@@ -178,63 +199,105 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_router(Args p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave][r][4 * q + i] = acc[i];
     __syncthreads();
-    if (threadIdx.x < 256) {
-        const int e = threadIdx.x & 15, t = threadIdx.x >> 4;
-        double v = red[0][t][e];
+    const int e = threadIdx.x & 15, t = threadIdx.x >> 4;
+    double v = red[0][t][e];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += red[w][t][e];
-        if (e0 + e < p.E && t0 + t < p.T) p.logits[(int64_t)(t0 + t) * p.E + e0 + e] = v;
-    }
+    for (int w = 1; w < kRouterWaves; ++w) v += red[w][t][e];
+    if (e0 + e < p.E && t0 + t < p.T) p.logits[((int64_t)blockIdx.z * p.T + t0 + t) * p.E + e0 + e] = v;
 }
 
 // ------------------------------------------------------------------ the choice
-// Ids and weights of token t by one wave, as the routers choose (logits in fp64): lane j < k returns the j-th.
-// P: expert slots per lane. Non-finite logits order somehow; the ids stay distinct and in range.
+// Largest value over the wave, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max(v, dpp_u32<0xB1>(v));
+    v = max(v, dpp_u32<0x4E>(v));
+    v = max(v, dpp_u32<0x141>(v));
+    v = max(v, dpp_u32<0x140>(v));
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return max(max(a, b), max(c, d));
+}
+__device__ __forceinline__ double read_lane(double v, int lane) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+// Logits (sigmoid: scores) of tokens t0 .. t0 + n - 1 into LDS, val[token - t0], by all threads: a thread adds the parts of
+// one logit, all loaded at once.
+constexpr int kMaxParts = 8;
+__device__ __forceinline__ void add_parts(const Args& p, int t0, int n, double (*val)[kMaxE]) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n * p.E; i += kThreads) {
+        const int t = i / p.E, e = i - t * p.E;
+        const double* src = p.logits + (int64_t)(t0 + t) * p.E + e;
+        const int64_t step = (int64_t)p.T * p.E;
+        double v[kMaxParts], l = 0.0;
+#pragma unroll
+        for (int z = 0; z < kMaxParts; ++z) v[z] = src[min(z, p.parts - 1) * step];
+#pragma unroll
+        for (int z = 0; z < kMaxParts; ++z) l += z < p.parts ? v[z] : 0.0;
+        val[t][e] = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : l;
+    }
+}
+
+// Ids and weights of a token by one wave, as the routers choose from val: lane j < k returns the j-th. P: expert slots per
+// lane. A round compares the upper halves of the lanes' best keys; only where two lanes tie there does it compare whole
+// keys. Non-finite logits order somehow; the ids stay distinct and in range.
 template <int P>
-__device__ __forceinline__ void choose(const Args& p, int t, int lane, int* id, float* weight) {
-    const double* lt = p.logits + (int64_t)t * p.E;
-    auto score = [&](double l) { return p.sigmoid ? 1.0 / (1.0 + exp(-l)) : l; };
+__device__ __forceinline__ void choose(const Args& p, const double* val, int lane, int* id, float* weight) {
     uint64_t key[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) {
         const int e = lane + 64 * j;
         key[j] = 0;  // below the key of every number
         if (e < p.E) {
-            const double v = score(lt[e]) + (p.bias ? (double)p.bias[e] : 0.0);
+            const double v = val[e] + (p.bias ? (double)p.bias[e] : 0.0);
             key[j] = order_key(v == v ? v : -__builtin_inf());
         }
     }
-    int mine = 0;
-    for (int r = 0; r < p.k; ++r) {
-        uint64_t bk = 0;
-        int bj = 0;
+    uint64_t best = 0;
+    int slot = 0;
+    auto rank = [&]() {  // the lane's best: strictly greater, so the lowest slot among equal keys stays
+        best = 0;
+        slot = 0;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            const bool gt = key[j] > bk;  // strict: the lowest slot among equal keys stays
-            bk = gt ? key[j] : bk;
-            bj = gt ? j : bj;
+            const bool gt = key[j] > best;
+            best = gt ? key[j] : best;
+            slot = gt ? j : slot;
         }
-        int be = bk ? lane + 64 * bj : 0x7FFFFFFF;
-        group_argmax<64>(bk, be);
-        if ((be & 63) == lane) {
-#pragma unroll
-            for (int j = 0; j < P; ++j) key[j] = j == be / 64 ? 0 : key[j];
+    };
+    rank();
+    int mine = 0;
+    for (int r = 0; r < p.k; ++r) {
+        const uint32_t top = wave_max((uint32_t)(best >> 32));
+        const uint64_t at = __ballot((uint32_t)(best >> 32) == top);
+        int win;
+        if ((at & (at - 1)) == 0) {
+            const int owner = __builtin_ctzll(at);
+            win = owner + 64 * __builtin_amdgcn_readlane(slot, owner);
+        } else {
+            uint64_t bk = best;
+            win = best ? lane + 64 * slot : 0x7FFFFFFF;
+            group_argmax<64>(bk, win);
+            win = __builtin_amdgcn_readfirstlane(win);
         }
-        mine = lane == r ? be : mine;
-    }
-    const bool chosen = lane < p.k;
-    const double l = chosen ? lt[mine] : -__builtin_inf();
-    double v;
-    if (p.sigmoid) {
-        v = chosen ? score(l) : 0.0;
-    } else {
-        double m = l;
+        const int ws = win / 64;
+        const bool owner = lane == (win & 63);
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) m = fmax(m, __shfl_xor(m, off, 64));
-        v = chosen ? exp(l - m) : 0.0;
+        for (int j = 0; j < P; ++j) key[j] = owner && j == ws ? 0 : key[j];
+        rank();
+        mine = lane == r ? win : mine;
     }
-    double sum = 0.0;
-    for (int j = 0; j < p.k; ++j) sum += __shfl(v, j, 64);
+    double v = lane < p.k ? val[mine] : 0.0;  // the chosen logits, or scores
+    if (!p.sigmoid) {
+        double m = read_lane(v, 0);
+        for (int j = 1; j < p.k; ++j) m = fmax(m, read_lane(v, j));
+        v = exp(v - m);
+    }
+    double sum = 0.0;  // in the order of the choice
+    for (int j = 0; j < p.k; ++j) sum += read_lane(v, j);
     *id = mine;
     *weight = (float)(v / sum);
 }
@@ -307,173 +370,326 @@ __device__ __forceinline__ int build(Table& tb, const Args& p, const int32_t* id
         tb.wt[row] = weights[a];
     }
     __syncthreads();
-    return total >> 16;
+    return (int)uniform((uint32_t)total) >> 16;
 }
 
-// ------------------------------------------------------------------ fc1 + SwiGLU
-// A task is one block of tokens and NB groups of 8 gate rows and their 8 up rows; KS waves share a group's K. Every
-// workgroup walks tasks blockIdx.x, + gridDim.x, ...; the sums of the KS parts meet in LDS and are added in order.
+// ------------------------------------------------------------------ the layer
+// Work is cut into tasks that the workgroups take from device-wide counters in order: a workgroup waits only for tasks
+// that running workgroups hold, so a call ends however few of its workgroups are resident at a time (another call's may
+// hold the rest of the chip, and wait as well).
+//
+//   choice   more than 8 tokens: 8 tokens a task, one per wave (up to 8 tokens every workgroup chooses for itself,
+//            which costs it less than waiting)
+//   fc1      one block of tokens and 8 NB gate rows with their up rows; the waves share K
+//   fc2      16 columns of out; the waves share the (block, K step) pairs of all chosen experts in contiguous runs, and
+//            where a run leaves a block its wave adds weight * sum to its own token rows in LDS
+//
+// Which workgroup does a task does not show in its result, and every sum has a fixed order.
+constexpr int kOwnChoice = kWaves;
+
+// By one thread. (The offset that the compiler cannot see through keeps it from first adding up over the wave, which
+// would wait for the result, and with it for every load in flight, on the spot.)
+__device__ __forceinline__ uint32_t take(uint32_t* counter) {
+    uint32_t zero = 0;
+    asm volatile("" : "+v"(zero));
+    counter += zero;
+    return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// All threads: everything this workgroup stored becomes visible to workgroups that see `counter` counted up by n.
+__device__ __forceinline__ void publish(uint32_t* counter, uint32_t n) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+        __hip_atomic_fetch_add(counter, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+// All threads: waits until `counter` has reached n; what was published before it did is visible then.
+__device__ __forceinline__ void await(uint32_t* counter, uint32_t n) {
+    if (threadIdx.x == 0) {
+        while (__hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < n) __builtin_amdgcn_s_sleep(1);
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    }
+    __syncthreads();
+}
+
+// fc1's operands of a wave in flight: D1 steps.
+template <int FMT>
+struct Stage1 {
+    W16 w[Fmt<FMT>::D1][Fmt<FMT>::NB];
+    X16<FMT> x[Fmt<FMT>::D1];
+};
+struct Task1 {  // all scalars
+    int e, n, row0, c0;
+};
+
 template <int FMT, int P>
-__global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
-    constexpr int NB = FMT == kBf16 ? 1 : FMT == kInt8 ? 2 : 4, KS = kWaves / NB, D = FMT == kNvfp4 ? 4 : 8;
+__global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
+    constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, D2 = Fmt<FMT>::D2, NF = Fmt<FMT>::kFrags;
+    union Scratch {
+        float part[2][kWaves][NB][16][17];  // fc1: each wave's sums
+        float rows[kWaves][kMaxT][17];      // fc2: each wave's token rows
+        struct {
+            int32_t ids[kMaxA];
+            float weights[kMaxA];
+            double val[kWaves][kMaxE];
+        } c;                                // the choice
+    };
     __shared__ Table tb;
-    __shared__ float red[2][kWaves][16][17];
-    __shared__ int32_t ids_lds[kMaxA];
-    __shared__ float w_lds[kMaxA];
+    __shared__ Scratch sc;
+    __shared__ uint32_t next[2];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    for (int t = wave; t < p.T; t += kWaves) {
+    uint32_t ticket = 0;  // thread 0's
+    if (threadIdx.x == 0) ticket = take(&p.count->fc1);
+
+    // ---- the choice
+    auto choose_for = [&](int t0, int32_t* ids, float* weights) {  // tokens t0 .. t0 + 7, one per wave
+        add_parts(p, t0, min(p.T - t0, kWaves), sc.c.val);
+        __syncthreads();
+        const int t = t0 + wave;
+        if (t >= p.T) return;
         int id;
         float w;
-        choose<P>(p, t, lane, &id, &w);
+        choose<P>(p, sc.c.val[wave], lane, &id, &w);
         if (lane < p.k) {
-            ids_lds[t * p.k + lane] = id;
-            w_lds[t * p.k + lane] = w;
-            if (blockIdx.x == 0) {
-                p.ids[t * p.k + lane] = id;
-                p.weights[t * p.k + lane] = w;
-            }
+            ids[t * p.k + lane] = id;
+            weights[t * p.k + lane] = w;
         }
+    };
+    int V;
+    if (p.T <= kOwnChoice) {
+        choose_for(0, sc.c.ids, sc.c.weights);
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int a = threadIdx.x; a < p.T * p.k; a += kThreads) {
+                p.ids[a] = sc.c.ids[a];
+                p.weights[a] = sc.c.weights[a];
+            }
+        V = build(tb, p, sc.c.ids, sc.c.weights);
+    } else {
+        const uint32_t tasks = (uint32_t)(p.T + kWaves - 1) / kWaves;
+        for (;;) {
+            if (threadIdx.x == 0) next[0] = take(&p.count->pick);
+            __syncthreads();
+            const uint32_t c = uniform(next[0]);
+            if (c >= tasks) break;
+            choose_for((int)c * kWaves, p.ids, p.weights);
+            publish(&p.count->picked, 1);
+            // Nothing may come between thread 0's part of publish and its next take but this barrier: without it the
+            // compiler makes one block of the two, and a loop around the rest that lane 0 leaves for that block while
+            // the other lanes of its wave go round and wait for it there.
+            __syncthreads();
+        }
+        await(&p.count->picked, tasks);
+        V = build(tb, p, p.ids, p.weights);
+    }
+
+    // ---- fc1
+    const int JB = (p.f + 8 * NB - 1) / (8 * NB), N1 = V * JB;
+    const auto xr = rsrc(p.x, (uint32_t)p.T * (uint32_t)p.d * 2u);
+    const uint32_t rb1 = Fmt<FMT>::row_bytes(p.d);
+    const int steps1 = (int)(rb1 + 63) / 64, part1 = (steps1 + kWaves - 1) / kWaves;
+    const int chunks = (part1 + D1 - 1) / D1, s_first = wave * part1, s_end = min(s_first + part1, steps1);
+    if (threadIdx.x == 0) {
+        next[0] = ticket;
+        next[1] = take(&p.count->fc1);
     }
     __syncthreads();
-    const int V = build(tb, p, ids_lds, w_lds);
-    const int JB = (p.f + 8 * NB - 1) / (8 * NB);
-    const auto xr = rsrc(p.x, (uint32_t)p.T * (uint32_t)p.d * 2u);
-    const uint32_t rb = Fmt<FMT>::row_bytes(p.d);
-    const int steps = (int)(rb + 63) / 64, part = (steps + KS - 1) / KS;
-    const int s_first = wave % KS * part, s_end = min(s_first + part, steps);
-    int flip = 0;
-    for (int task = blockIdx.x; task < V * JB; task += gridDim.x) {
+    int cur = (int)uniform(next[0]), nxt = (int)uniform(next[1]);
+    __syncthreads();
+    auto set = [&](int task) {
         const Block b = tb.blocks[task / JB];
-        const int e = __builtin_amdgcn_readfirstlane((int)b.e), n = __builtin_amdgcn_readfirstlane(b.n);
-        const int row0 = __builtin_amdgcn_readfirstlane((int)b.row0), c0 = task % JB * 8 * NB;
-        const Matrix<FMT> m(p.w1, p.s1, e, 2 * p.f, p.d);
-        const int col = c0 + wave / KS * 8 + (r & 7);
-        const uint32_t wrow = r < 8 ? col : p.f + col;
-        const bool w_ok = col < p.f, x_ok = r < n;
-        const uint32_t xrow = x_ok ? tb.tok[row0 + r] : 0;
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s0 = s_first; s0 < s_end; s0 += D) {
-            W16 w[D];
-            X16<FMT> x[D];
+        return Task1{(int)uniform(b.e), (int)uniform(b.n), (int)uniform(b.row0), task % JB * 8 * NB};
+    };
+    auto fetch = [&](Stage1<FMT>& st, int j, const Task1& t, uint32_t xrow, int s) {
+        const Matrix<FMT> m(p.w1, p.s1, t.e, 2 * p.f, p.d);
+        const uint32_t o = (uint32_t)s * 64 + q * 16;
+        const bool ok = s < s_end && o < rb1;
+        const int col = t.c0 + (r & 7);
 #pragma unroll
-            for (int j = 0; j < D; ++j) {
-                const uint32_t o = (uint32_t)(s0 + j) * 64 + q * 16;
-                const bool ok = s0 + j < s_end && o < rb;
-                w[j] = m.load(wrow, o, ok && w_ok);
-                x[j] = load_x<FMT>(xr, xrow, p.d, o, ok && x_ok);
-            }
+        for (int g = 0; g < NB; ++g)
+            st.w[j][g] = m.load((r < 8 ? 0 : p.f) + col + 8 * g, o, ok && col + 8 * g < p.f);
+        st.x[j] = load_x<FMT>(xr, xrow, p.d, o, ok && r < t.n);
+    };
+    auto token = [&](const Task1& t) { return (uint32_t)tb.tok[t.row0 + min(r, t.n - 1)]; };
+    uint32_t finished = 0;
+    if (cur < N1) {
+        Stage1<FMT> st;
+        Task1 t = set(cur);
+        uint32_t xrow = token(t);
 #pragma unroll
-            for (int j = 0; j < D; ++j) acc = product<FMT>(w[j], x[j], acc);
-        }
-        // lane: rows 4 q + i of the group (gate 0 .. 7, up 8 .. 15), token r
+        for (int j = 0; j < D1; ++j) fetch(st, j, t, xrow, s_first + j);
+        int flip = 0;
+        while (cur < N1) {
+            if (threadIdx.x == 0) ticket = take(&p.count->fc1);
+            const bool more = nxt < N1;
+            const Task1 tn = set(more ? nxt : cur);
+            const uint32_t xnext = token(tn);
+            f32x4 acc[NB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) red[flip][wave][r][4 * q + i] = acc[i];
-        __syncthreads();
-        if (threadIdx.x < 16 * 8 * NB) {
-            const int cc = threadIdx.x % (8 * NB), i = threadIdx.x / (8 * NB), g8 = cc / 8, j = cc % 8;
-            if (i < n && c0 + cc < p.f) {
-                float g = red[flip][g8 * KS][i][j], u = red[flip][g8 * KS][i][8 + j];
+            for (int g = 0; g < NB; ++g) acc[g] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+            for (int c = 0; c < chunks; ++c) {
+                const bool last = c + 1 == chunks;
+                const Task1 tl = last ? tn : t;
+                const uint32_t xl = last ? xnext : xrow;
+                const int sl = !last ? s_first + (c + 1) * D1 : more ? s_first : s_end;
 #pragma unroll
-                for (int w = 1; w < KS; ++w) {
-                    g += red[flip][g8 * KS + w][i][j];
-                    u += red[flip][g8 * KS + w][i][8 + j];
+                for (int j = 0; j < D1; ++j) {
+#pragma unroll
+                    for (int i = 0; i < NF; ++i)
+#pragma unroll
+                        for (int g = 0; g < NB; ++g) acc[g] = mfma(decode<FMT>(st.w[j][g], i), st.x[j].v[i], acc[g]);
+                    fetch(st, j, tl, xl, sl + j);
                 }
-                if (FMT == kInt8) {
-                    const float* s = static_cast<const float*>(p.s1) + (int64_t)e * 2 * p.f + c0 + cc;
-                    g *= s[0];
-                    u *= s[p.f];
-                } else if (FMT == kNvfp4) {
-                    g *= p.t1[e];
-                    u *= p.t1[e];
-                }
-                const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-                p.h[(int64_t)(row0 + i) * p.f + c0 + cc] = (uint16_t)bf16x2_rne(h, h);
             }
+            // lane: rows 4 q + i of the group (gate 0 .. 7, up 8 .. 15), token r
+            if (r < t.n) {
+#pragma unroll
+                for (int g = 0; g < NB; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc.part[flip][wave][g][r][4 * q + i] = acc[g][i];
+            }
+            if (threadIdx.x == 0) next[flip] = ticket;
+            lds_barrier();
+            if (wave < 2 * NB) {
+                const int cc = threadIdx.x % (8 * NB), i = threadIdx.x / (8 * NB), g8 = cc / 8, j = cc % 8;
+                const int col = t.c0 + cc;
+                if (i < t.n && col < p.f) {
+                    float g = sc.part[flip][0][g8][i][j], u = sc.part[flip][0][g8][i][8 + j];
+#pragma unroll
+                    for (int w = 1; w < kWaves; ++w) {
+                        g += sc.part[flip][w][g8][i][j];
+                        u += sc.part[flip][w][g8][i][8 + j];
+                    }
+                    if (FMT == kInt8) {
+                        const float* s = static_cast<const float*>(p.s1) + (int64_t)t.e * 2 * p.f + col;
+                        g *= s[0];
+                        u *= s[p.f];
+                    } else if (FMT == kNvfp4) {
+                        g *= p.t1[t.e];
+                        u *= p.t1[t.e];
+                    }
+                    const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+                    const uint32_t hi = bf16x2_rne(h, h) & 0xFFFFu;
+                    // (of an infinite h the first part is all)
+                    const float left = (hi & 0x7F80u) == 0x7F80u ? 0.0f : h - bf16_to_f32(hi);
+                    uint16_t* o = p.h + ((int64_t)(t.row0 + i) * p.f + col / 8 * 8) * 2 + col % 8;
+                    o[0] = (uint16_t)hi;
+                    o[8] = (uint16_t)bf16x2_rne(left, left);
+                }
+            }
+            ++finished;
+            cur = nxt;
+            nxt = (int)uniform(next[flip]);
+            t = tn;
+            xrow = xnext;
+            flip ^= 1;  // (the next task's sums go to the other half while slow threads still read this one)
         }
-        flip ^= 1;  // (the next task's sums go to the other half while slow threads still read this one)
     }
-}
+    if (finished) publish(&p.count->done, finished);
+    else __syncthreads();
 
-// ------------------------------------------------------------------ fc2 + combine
-// A workgroup owns 16 columns of out. Its waves share the (block, K step) pairs of all chosen experts in equal
-// contiguous runs; where a run leaves a block, the wave adds weight * sum to its own token rows in LDS. The waves' rows
-// are added in order at the end.
-template <int FMT>
-__global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
-    constexpr int D = FMT == kNvfp4 ? 4 : 8;
-    __shared__ Table tb;
-    __shared__ float red[kWaves][kMaxT][17];
-    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    for (int i = threadIdx.x; i < kWaves * kMaxT * 17; i += kThreads) (&red[0][0][0])[i] = 0.0f;
-    const int V = build(tb, p, p.ids, p.weights);
-    const int n0 = blockIdx.x * 16;
-    const auto hr = rsrc(p.h, (uint32_t)(p.T * p.k) * (uint32_t)p.f * 2u);
-    const uint32_t rb = Fmt<FMT>::row_bytes(p.f);
-    const int S = (int)(rb + 63) / 64;
-    const int total = V * S, part = (total + kWaves - 1) / kWaves;
-    const int first = min(wave * part, total), end = min(first + part, total);
-    const bool w_ok = n0 + r < p.d;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    int lv = first / S, ls = first - lv * S;  // load position
-    int cv = lv, cs = ls;                     // product position
-    for (int i0 = first; i0 < end; i0 += D) {
-        W16 w[D];
-        X16<FMT> x[D];
-#pragma unroll
-        for (int j = 0; j < D; ++j) {
-            const bool live = i0 + j < end;
-            const Block b = tb.blocks[live ? lv : 0];
-            const int e = __builtin_amdgcn_readfirstlane((int)b.e), n = __builtin_amdgcn_readfirstlane(b.n);
-            const int row0 = __builtin_amdgcn_readfirstlane((int)b.row0);
+    // ---- fc2 + combine
+    const auto hr = rsrc(p.h, (uint32_t)(p.T * p.k) * (uint32_t)p.f * 4u);
+    const uint32_t rb2 = Fmt<FMT>::row_bytes(p.f);
+    const int S = (int)(rb2 + 63) / 64, total = V * S, part2 = (total + kWaves - 1) / kWaves;
+    const int first = min(wave * part2, total), end = min(first + part2, total);
+    const int N2 = (p.d + 15) / 16;
+    bool waited = false;
+    for (;;) {
+        if (threadIdx.x == 0) next[0] = take(&p.count->fc2);
+        __syncthreads();
+        const int task = (int)uniform(next[0]);
+        if (task >= N2) break;
+        const int n0 = task * 16;
+        const bool w_ok = n0 + r < p.d;
+        for (int i = threadIdx.x; i < kWaves * kMaxT * 17; i += kThreads) (&sc.rows[0][0][0])[i] = 0.0f;
+        W16 w[D2];
+        u32x4 x[D2][NF][2];
+        int wv = first / S, ws = first - wv * S, xv = wv, xs = ws, cv = wv, cs = ws;  // next weights, h, products
+        auto fetch_w = [&](int j, bool live) {
+            const int e = __builtin_amdgcn_readfirstlane((int)tb.blocks[live ? wv : 0].e);
             const Matrix<FMT> m(p.w2, p.s2, e, p.d, p.f);
-            const uint32_t o = (uint32_t)ls * 64 + q * 16;
-            const bool ok = live && o < rb;
-            w[j] = m.load((uint32_t)(n0 + r), o, ok && w_ok);
-            x[j] = load_x<FMT>(hr, (uint32_t)(row0 + r), p.f, o, ok && r < n);
-            if (++ls == S) {
-                ls = 0;
-                ++lv;
+            const uint32_t o = (uint32_t)ws * 64 + q * 16;
+            w[j] = m.load((uint32_t)(n0 + r), o, live && o < rb2 && w_ok);
+            if (++ws == S) {
+                ws = 0;
+                ++wv;
             }
-        }
+        };
+        auto fetch_x = [&](int j, bool live) {
+            const Block b = tb.blocks[live ? xv : 0];
+            const int n = __builtin_amdgcn_readfirstlane(b.n), row0 = __builtin_amdgcn_readfirstlane((int)b.row0);
+            const uint32_t o = (uint32_t)xs * 64 + q * 16;
+            const uint32_t at = (uint32_t)(row0 + r) * (uint32_t)p.f * 4u + o / 16 * (NF * 32);
 #pragma unroll
-        for (int j = 0; j < D; ++j) {
-            if (i0 + j >= end) break;
-            acc = product<FMT>(w[j], x[j], acc);
-            if (++cs == S || i0 + j + 1 == end) {
-                const Block b = tb.blocks[cv];
-                if (r < b.n) {
-                    const float wt = tb.wt[b.row0 + r];
-                    float* o = red[wave][tb.tok[b.row0 + r]] + 4 * q;
+            for (int i = 0; i < NF; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float v = acc[i];
-                        if (FMT == kInt8) {
-                            const int c = min(n0 + 4 * q + i, p.d - 1);
-                            v *= static_cast<const float*>(p.s2)[(int64_t)b.e * p.d + c];
-                        } else if (FMT == kNvfp4) {
-                            v *= p.t2[b.e];
-                        }
-                        o[i] = __builtin_fmaf(wt, v, o[i]);
+                for (int half = 0; half < 2; ++half)
+                    x[j][i][half] = __builtin_amdgcn_raw_buffer_load_b128(
+                        hr, live && o < rb2 && r < n ? at + 32 * i + 16 * half : kNowhere, 0, 0);
+            if (++xs == S) {
+                xs = 0;
+                ++xv;
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < D2; ++j) fetch_w(j, first + j < end);
+        if (waited) __syncthreads();
+        else await(&p.count->done, (uint32_t)N1);
+        waited = true;
+#pragma unroll
+        for (int j = 0; j < D2; ++j) fetch_x(j, first + j < end);
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i0 = first; i0 < end; i0 += D2) {
+#pragma unroll
+            for (int j = 0; j < D2; ++j) {
+                if (i0 + j < end) {
+#pragma unroll
+                    for (int i = 0; i < NF; ++i) {
+                        const bf16x8 v = decode<FMT>(w[j], i);
+                        acc = mfma(v, x[j][i][0], acc);
+                        acc = mfma(v, x[j][i][1], acc);
                     }
                 }
-                acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-                cs = 0;
-                ++cv;
+                const bool live = i0 + D2 + j < end;
+                fetch_w(j, live);
+                fetch_x(j, live);
+                if (i0 + j < end && (++cs == S || i0 + j + 1 == end)) {
+                    const Block b = tb.blocks[cv];
+                    if (r < b.n) {
+                        const float wt = tb.wt[b.row0 + r];
+                        float* o = sc.rows[wave][tb.tok[b.row0 + r]] + 4 * q;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float v = acc[i];
+                            if (FMT == kInt8) {
+                                const int c = min(n0 + 4 * q + i, p.d - 1);
+                                v *= static_cast<const float*>(p.s2)[(int64_t)b.e * p.d + c];
+                            } else if (FMT == kNvfp4) {
+                                v *= p.t2[b.e];
+                            }
+                            o[i] = __builtin_fmaf(wt, v, o[i]);
+                        }
+                    }
+                    acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+                    cs = 0;
+                    ++cv;
+                }
             }
         }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.T * 16; i += kThreads) {
-        const int t = i >> 4, c = i & 15;
-        if (n0 + c >= p.d) continue;
-        float v = red[0][t][c];
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.T * 16; i += kThreads) {
+            const int t = i >> 4, c = i & 15;
+            if (n0 + c >= p.d) continue;
+            float v = sc.rows[0][t][c];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += red[w][t][c];
-        const int64_t at = (int64_t)t * p.d + n0 + c;
-        if (p.residual) v += bf16_to_f32(p.residual[at]);
-        p.out[at] = (uint16_t)bf16x2_rne(v, v);
+            for (int w2 = 1; w2 < kWaves; ++w2) v += sc.rows[w2][t][c];
+            const int64_t at = (int64_t)t * p.d + n0 + c;
+            if (p.residual) v += bf16_to_f32(p.residual[at]);
+            p.out[at] = (uint16_t)bf16x2_rne(v, v);
+        }
+        __syncthreads();
     }
 }
 
@@ -485,28 +701,40 @@ bool dims_ok(int64_t T, int64_t d, int64_t E, int k, int64_t f) {
     if (d < m || d % m != 0 || d > (1 << 22) || f < m || f % m != 0 || f > (1 << 22)) return false;
     // one expert's matrix, the router's weights and the activations are one buffer descriptor each
     return 2 * f * (int64_t)Fmt<FMT>::row_bytes((int)d) <= kMaxBytes && d * (int64_t)Fmt<FMT>::row_bytes((int)f) <= kMaxBytes &&
-           E * d * 2 <= kMaxBytes && T * k * f * 2 <= kMaxBytes;
+           E * d * 2 <= kMaxBytes && T * k * f * 4 <= kMaxBytes;
 }
-size_t carve(Carver& c, int64_t T, int k, int64_t E, int64_t f, Args* p) {
-    p->logits = c.take<double>((size_t)(T * E));
-    p->h = c.take<uint16_t>((size_t)(T * k * f));
+// Parts of K of the router's product: some 200 workgroups in all, of at least four steps a wave.
+int router_parts(int64_t T, int64_t d, int64_t E) {
+    const int64_t blocks = std::max<int64_t>(1, (E + 15) / 16 * ((T + 15) / 16));
+    return (int)std::max<int64_t>(1, std::min({(200 + blocks - 1) / blocks, d / (32 * 4 * kRouterWaves), (int64_t)kMaxParts}));
+}
+size_t carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t f, Args* p) {
+    p->parts = router_parts(T, d, E);
+    p->count = c.take<Counters>(1);
+    p->logits = c.take<double>((size_t)(p->parts * T * E));
+    p->h = c.take<uint16_t>((size_t)(2 * T * k * f));
     return c.need;
 }
 
 template <int FMT, int P>
-void launch_fc1(const Args& p, hipStream_t s) {
-    constexpr int NB = FMT == kBf16 ? 1 : FMT == kInt8 ? 2 : 4;
-    const int64_t tasks = (int64_t)std::min(p.T * p.k, p.E + p.T * p.k / 16) * ((p.f + 8 * NB - 1) / (8 * NB));
+void launch_layer(const Args& p, hipStream_t s) {
+    constexpr int NB = Fmt<FMT>::NB;
+    // as many workgroups as have a task, at most one per CU (their registers and LDS let no more be resident)
+    const int64_t blocks = std::min(p.T * p.k, p.E + p.T * p.k / 16);
+    const int64_t tasks = std::max<int64_t>(blocks * ((p.f + 8 * NB - 1) / (8 * NB)), (p.d + 15) / 16);
     const unsigned grid = (unsigned)std::min<int64_t>(tasks, device_cus());
-    hipLaunchKernelGGL((k_decode_fc1<FMT, P>), dim3(grid), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_decode_layer<FMT, P>), dim3(grid), dim3(kThreads), 0, s, p);
 }
 template <int FMT>
 int run(const Args& p, hipStream_t s) {
-    hipLaunchKernelGGL(k_decode_router, dim3((unsigned)(p.E + 15) / 16, (unsigned)(p.T + 15) / 16), dim3(kThreads), 0, s, p);
-    if (p.E <= 128) launch_fc1<FMT, 2>(p, s);
-    else if (p.E <= 512) launch_fc1<FMT, 8>(p, s);
-    else launch_fc1<FMT, 16>(p, s);
-    hipLaunchKernelGGL(k_decode_fc2<FMT>, dim3((unsigned)(p.d + 15) / 16), dim3(kThreads), 0, s, p);
+    const dim3 grid((unsigned)(p.E + 15) / 16, (unsigned)(p.T + 15) / 16, (unsigned)p.parts);
+    hipLaunchKernelGGL(k_decode_router, grid, dim3(64 * kRouterWaves), 0, s, p);
+    if (p.E <= 64) launch_layer<FMT, 1>(p, s);
+    else if (p.E <= 128) launch_layer<FMT, 2>(p, s);
+    else if (p.E <= 256) launch_layer<FMT, 4>(p, s);
+    else if (p.E <= 384) launch_layer<FMT, 6>(p, s);
+    else if (p.E <= 512) launch_layer<FMT, 8>(p, s);
+    else launch_layer<FMT, 16>(p, s);
     return launch_status();
 }
 
@@ -526,10 +754,10 @@ int layer(const uint16_t* x, int64_t T, int64_t d, const uint16_t* w_router, con
         return NVQ_ERR_ALIGN;
     Args p{};
     Carver need(nullptr);
-    if (ws_bytes < carve(need, T, k, E, f, &p)) return NVQ_ERR_WORKSPACE;
+    if (ws_bytes < carve(need, T, d, k, E, f, &p)) return NVQ_ERR_WORKSPACE;
     if (T == 0) return NVQ_OK;
     Carver cv(ws);
-    carve(cv, T, k, E, f, &p);
+    carve(cv, T, d, k, E, f, &p);
     p.x = x; p.wr = w_router; p.bias = bias;
     p.w1 = w1; p.s1 = s1; p.t1 = t1;
     p.w2 = w2; p.s2 = s2; p.t2 = t2;
@@ -547,11 +775,10 @@ using namespace nvq;
 extern "C" {
 
 size_t moe_layer_decode_workspace_size(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff) {
-    (void)d;
-    if (T < 0 || T > kMaxT || k < 1 || k > kMaxK || E < 1 || E > kMaxE || d_ff < 0 || d_ff > (1 << 22)) return 0;
+    if (T < 0 || T > kMaxT || d < 0 || d > (1 << 22) || k < 1 || k > kMaxK || E < 1 || E > kMaxE || d_ff < 0 || d_ff > (1 << 22)) return 0;
     Carver c(nullptr);
     Args p{};
-    return carve(c, T, k, E, d_ff, &p);
+    return carve(c, T, d, k, E, d_ff, &p);
 }
 
 int moe_layer_decode_bf16(const uint16_t* x, int64_t T, int64_t d, const uint16_t* w_router, const float* bias, int router,
