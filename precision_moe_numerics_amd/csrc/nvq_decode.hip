@@ -9,12 +9,18 @@
 //
 // Bound by reading the chosen experts' weights once. The activations are not
 // quantized: they are a few rows, and it would save nothing. A weight reaches
-// the matrix pipe as a bf16 value that holds it exactly (int8 codes have 8
-// significant bits, e2m1 * e4m3 has 6); the channel's or tensor's fp32 scale is
-// applied to the fp32 sum. h goes to the matrix pipe as two bf16 parts, its
-// rounding and the rounding of what that left (2^-17 of it in all; one part
+// the matrix pipe as a 16-bit value that holds it exactly (int8 codes have 8
+// significant bits: bf16; e2m1 * e4m3 has 6 and lies in [2^-10, 2688]: fp16);
+// the channel's or tensor's fp32 scale is applied to the fp32 sum.
+//
+// The other operand. bf16 and int8 weights: x as it is, and h as two bf16 parts,
+// its rounding and the rounding of what that left (2^-17 of it in all; one part
 // would be 2^-9, as much as out's own rounding), which costs only products and
-// these are far from the limit.
+// these are far from the limit. NVFP4 weights: x in fp16 times a power of two
+// per token that takes its largest value to [2^14, 2^15), which holds its 8 bits
+// down to 2^-29 of that and is off by at most 2^-40 of it below; and h rounded to
+// fp16 once (2^-12 of it), times a power of two that no h of the token and expert
+// can exceed, from the 1-norm of x and the expert's largest possible weight.
 #include "nvq_argmax.hpp"
 #include "nvq_device.hpp"
 #include "nvq_host.hpp"
@@ -43,8 +49,12 @@ constexpr int64_t kMaxBytes = 0xFFFFFE00ll;
 // Device-wide counters of one call, cleared by k_decode_router.
 struct Counters {
     uint32_t pick, picked;  // tasks of the choice taken, finished
-    uint32_t fc1, done;     // of fc1
-    uint32_t fc2;           // of fc2
+    uint32_t fc1, done;     // shares of fc1 taken, tasks of it finished
+    uint32_t fc2;           // shares of fc2 taken
+};
+// x of a token for NVFP4 weights is its fp16 values times 2^shift; the sum of these values' magnitudes is below 2^norm.
+struct TokenScale {
+    int32_t shift, norm;
 };
 
 struct Args {
@@ -59,9 +69,11 @@ struct Args {
     int32_t* ids;
     float* weights;
     double* logits;           // [parts, T, E]: sums over parts of K
-    uint16_t* h;              // [T k, f / 8, 2, 8], rows in expert order: each eight values' high, then low parts
+    uint16_t* h;              // [T k, f], rows in expert order; bf16: each eight values' high, then low parts
+    uint16_t* xh;             // NVFP4: [T, d] fp16 (both in the order of half_slot)
+    TokenScale* xs;
     Counters* count;
-    int T, d, E, k, f, sigmoid, parts;
+    int T, d, E, k, f, sigmoid, parts, max_blocks;
 };
 
 // A value that all lanes of a wave hold, as a scalar: branches on it are the wave's, not a lane's. Every loop here that
@@ -79,8 +91,9 @@ template <int FMT>
 struct Fmt {
     static constexpr int kVals = FMT == kBf16 ? 8 : FMT == kInt8 ? 16 : 32;  // in 16 bytes
     static constexpr int kFrags = kVals / 8;
-    static constexpr int NB = FMT == kBf16 ? 1 : FMT == kInt8 ? 2 : 4;  // fc1: groups of 16 weight rows of a wave
-    static constexpr int D1 = FMT == kBf16 ? 8 : 4, D2 = FMT == kNvfp4 ? 4 : 8;  // steps in flight in fc1, fc2
+    static constexpr int NB = FMT == kBf16 ? 1 : 2;         // fc1: groups of 16 weight rows of a wave
+    static constexpr int D1 = FMT == kBf16 ? 8 : 4, D2 = 8;  // steps in flight in fc1, fc2
+    static constexpr int kParts = FMT == kNvfp4 ? 1 : 2;    // 16-bit parts of h
     static __host__ __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)(K / kVals) * 16u; }
 };
 
@@ -93,11 +106,29 @@ struct X16 {
     u32x4 v[Fmt<FMT>::kFrags];
 };
 
-// Fragment i (8 values) of 16 bytes of weights, in bf16.
+// Slot of value j of eight in the fp16 operands: the pairs in which NVFP4 codes are decoded, (0 2) (4 6) (1 3) (5 7).
+__host__ __device__ constexpr int half_slot(int j) { return (j & 1) * 4 + (j >> 1); }
+
+// Eight E2M1 codes times an E4M3 scale in fp16, exact, in the order of half_slot. The upper byte of an E2M1 value's fp16
+// holds all of it: a byte permute looks up four magnitudes at a time, a bit select adds the signs, four more permutes
+// spread the bytes over halves. 16 full-rate operations for 8 values; four conversions and products (the converter runs
+// at a quarter of the rate) would take as long as 20, fp32 conversions as 28.
+__device__ __forceinline__ u32x4 decode_fp4(uint32_t w, half2v scale) {
+    constexpr uint32_t kLo = 0x3E3C3800u, kHi = 0x46444240u;  // 0 .5 1 1.5, 2 3 4 6
+    const uint32_t even = __builtin_amdgcn_perm(kHi, kLo, w & 0x07070707u);
+    const uint32_t odd = __builtin_amdgcn_perm(kHi, kLo, (w >> 4) & 0x07070707u);
+    const uint32_t e = (even & 0x7F7F7F7Fu) | ((w << 4) & 0x80808080u), o = (odd & 0x7F7F7F7Fu) | (w & 0x80808080u);
+    auto put = [&](uint32_t bytes, uint32_t sel) {
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0u, bytes, sel)) * scale);
+    };
+    return (u32x4){put(e, 0x010C000Cu), put(e, 0x030C020Cu), put(o, 0x010C000Cu), put(o, 0x030C020Cu)};
+}
+
+// Fragment i (8 values) of 16 bytes of weights, in bf16 or (NVFP4) fp16.
 template <int FMT>
-__device__ __forceinline__ bf16x8 decode(const W16& w, int i) {
+__device__ __forceinline__ u32x4 decode(const W16& w, int i) {
     if constexpr (FMT == kBf16) {
-        return __builtin_bit_cast(bf16x8, w.w);
+        return w.w;
     } else if constexpr (FMT == kInt8) {
         u32x4 o;
 #pragma unroll
@@ -106,20 +137,19 @@ __device__ __forceinline__ bf16x8 decode(const W16& w, int i) {
             const float a = (float)(int8_t)(p & 0xFFu), b = (float)(int8_t)((p >> 8) & 0xFFu);
             o[j] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);  // exact: the upper halves
         }
-        return __builtin_bit_cast(bf16x8, o);
+        return o;
     } else {
-        const auto s2 = e4m3_pair_to_f32(w.sc);
-        const float s = s2[i >> 1];
-        u32x4 o;
-        auto put = [&](int j, nvq_f32x2 v) {
-            o[j] = __builtin_amdgcn_perm(__float_as_uint(v[1] * s), __float_as_uint(v[0] * s), 0x07060302u);
-        };
-        put(0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.w[i], 1.0f, 0));
-        put(1, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.w[i], 1.0f, 1));
-        put(2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.w[i], 1.0f, 2));
-        put(3, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.w[i], 1.0f, 3));
-        return __builtin_bit_cast(bf16x8, o);
+        const half2v s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.sc, 1.0f, false);
+        return decode_fp4(w.w[i], half2v{s[i >> 1], s[i >> 1]});
     }
+}
+template <int FMT>
+__device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 acc) {
+    if constexpr (FMT == kNvfp4)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, x), acc, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0,
+                                                       0, 0);
 }
 
 // The matrices of one expert: `rows` rows of K values.
@@ -159,26 +189,74 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-__device__ __forceinline__ f32x4 mfma(bf16x8 w, u32x4 x, f32x4 acc) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
-}
-
 // ------------------------------------------------------------------ router logits
 // One workgroup: 16 experts, 16 tokens, a part of K, shared by its four waves. The sum of 32 products that one
 // instruction adds is rounded to fp32, 2^-24 of it; from there on the sums are fp64, so that of two close logits the
 // larger one is chosen. K is cut so that a token's logits are some 200 workgroups: with one per 16 experts (24 of 384)
 // the launch took 6.6 us.
-constexpr int kRouterWaves = 4;
-__global__ __launch_bounds__(64 * kRouterWaves) void k_decode_router(Args p) {
+constexpr int kRouterWaves = 4, kRouterThreads = 64 * kRouterWaves;
+
+// x of token t in fp16 for NVFP4 weights (one workgroup).
+__device__ __forceinline__ void scale_token(const Args& p, int t) {
+    __shared__ uint32_t tops[kRouterWaves];
+    __shared__ float sums[kRouterWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, units = p.d / 8;
+    const u32x4* src = reinterpret_cast<const u32x4*>(p.x + (int64_t)t * p.d);
+    u32x4* dst = reinterpret_cast<u32x4*>(p.xh + (int64_t)t * p.d);
+    uint32_t m = 0;
+#pragma unroll 2
+    for (int u = threadIdx.x; u < units; u += kRouterThreads) {
+        const u32x4 v = src[u];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
+    }
+    m = wave_max_u32(m);
+    if (lane == 0) tops[wave] = m;
+    __syncthreads();
+    m = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    // a row without a largest finite value keeps its size: what it holds becomes infinities and NaN
+    const int shift = m && m < 0x7F80u ? __builtin_amdgcn_frexp_expf(bf16_to_f32(m)) - 15 : 0;
+    float sum = 0.0f;
+#pragma unroll 2
+    for (int u = threadIdx.x; u < units; u += kRouterThreads) {
+        const u32x4 v = src[u];
+        half8 o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = v[j >> 1];
+            const float f = __builtin_amdgcn_ldexpf(__uint_as_float((j & 1) ? b & 0xFFFF0000u : b << 16), -shift);
+            sum += fabsf(f);
+            o[half_slot(j)] = (_Float16)f;
+        }
+        dst[u] = __builtin_bit_cast(u32x4, o);
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    if (lane == 0) sums[wave] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        p.xs[t] = {shift, __builtin_amdgcn_frexp_expf(sum)};
+    }
+}
+
+template <bool HALF>
+__global__ __launch_bounds__(kRouterThreads) void k_decode_router(Args p) {
     __shared__ double red[kRouterWaves][16][17];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
-    if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x == 0) *p.count = Counters{};
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = Counters{};
+    int b = blockIdx.x;
+    if (HALF) {
+        if (b < p.T) return scale_token(p, b);
+        b -= p.T;
+    }
+    const int eb = (p.E + 15) / 16, tb = (p.T + 15) / 16;
+    const int e0 = b % eb * 16, t0 = b / eb % tb * 16, z = b / (eb * tb);
     const uint32_t rb = (uint32_t)p.d * 2u;
     const auto wr = rsrc(p.wr, (uint32_t)p.E * rb), xr = rsrc(p.x, (uint32_t)p.T * rb);
     const int steps = (p.d + 31) / 32, waves = p.parts * kRouterWaves, part = (steps + waves - 1) / waves;
-    const int first = ((int)blockIdx.z * kRouterWaves + wave) * part, s1 = min(first + part, steps);
+    const int first = (z * kRouterWaves + wave) * part, s1 = min(first + part, steps);
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
     for (int s0 = first; s0 < s1; s0 += 4) {
         u32x4 w[4], x[4];
@@ -191,7 +269,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void k_decode_router(Args p) {
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const f32x4 a = mfma(__builtin_bit_cast(bf16x8, w[j]), x[j], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+            const f32x4 a = mfma<kBf16>(w[j], x[j], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] += (double)a[i];
         }
@@ -203,7 +281,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void k_decode_router(Args p) {
     double v = red[0][t][e];
 #pragma unroll
     for (int w = 1; w < kRouterWaves; ++w) v += red[w][t][e];
-    if (e0 + e < p.E && t0 + t < p.T) p.logits[((int64_t)blockIdx.z * p.T + t0 + t) * p.E + e0 + e] = v;
+    if (e0 + e < p.E && t0 + t < p.T) p.logits[((int64_t)z * p.T + t0 + t) * p.E + e0 + e] = v;
 }
 
 // ------------------------------------------------------------------ the choice
@@ -245,14 +323,14 @@ __device__ __forceinline__ void add_parts(const Args& p, int t0, int n, double (
 // lane. A round compares the upper halves of the lanes' best keys; only where two lanes tie there does it compare whole
 // keys. Non-finite logits order somehow; the ids stay distinct and in range.
 template <int P>
-__device__ __forceinline__ void choose(const Args& p, const double* val, int lane, int* id, float* weight) {
+__device__ __forceinline__ void choose(const Args& p, const double* val, const float* bias, int lane, int* id, float* weight) {
     uint64_t key[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) {
         const int e = lane + 64 * j;
         key[j] = 0;  // below the key of every number
         if (e < p.E) {
-            const double v = val[e] + (p.bias ? (double)p.bias[e] : 0.0);
+            const double v = val[e] + (double)bias[e];
             key[j] = order_key(v == v ? v : -__builtin_inf());
         }
     }
@@ -313,15 +391,28 @@ struct Table {
     uint64_t mask[kMaxE];  // tokens of each expert
     int32_t base[kMaxE];   // its first row
     Block blocks[kMaxV];
-    float wt[kMaxA];
+    float wt[kMaxA];       // routing weight; NVFP4: times w2's tensor scale
     uint8_t tok[kMaxA];
-    int32_t scan[2][kWaves];
+    int32_t scan[kWaves];
+};
+// NVFP4, per row: g and u are the sums times t1 times 2^shift; h is its fp16 value times 2^exp.
+struct RowScale {
+    float t1;
+    int16_t shift, exp;
 };
 // From ids and weights (global, as another launch or `choose` of this workgroup left them). All threads take part;
 // returns the number of blocks.
-__device__ __forceinline__ int build(Table& tb, const Args& p, const int32_t* ids, const float* weights) {
+template <int FMT>
+__device__ __forceinline__ int build(Table& tb, RowScale* rows, const Args& p, const int32_t* ids, const float* weights) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int A = p.T * p.k;
+    struct Scales {
+        float t1, t2;
+        TokenScale x;
+    };
+    auto scales = [&](int a) { return Scales{p.t1[ids[a]], p.t2[ids[a]], p.xs[a / p.k]}; };
+    Scales early = {};  // of row t, on their way while the table is made
+    if (FMT == kNvfp4 && t < A) early = scales(t);
     for (int e = t; e < p.E; e += kThreads) tb.mask[e] = 0;
     __syncthreads();
     for (int a = t; a < A; a += kThreads)
@@ -341,12 +432,12 @@ __device__ __forceinline__ int build(Table& tb, const Args& p, const int32_t* id
         const int v = __shfl_up(incl, off, 64);
         incl += lane >= off ? v : 0;
     }
-    if (lane == 63) tb.scan[0][wave] = incl;
+    if (lane == 63) tb.scan[wave] = incl;
     __syncthreads();
     int before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        const int v = tb.scan[0][w];
+        const int v = tb.scan[w];
         before += w < wave ? v : 0;
         total += v;
     }
@@ -368,15 +459,25 @@ __device__ __forceinline__ int build(Table& tb, const Args& p, const int32_t* id
         const int row = tb.base[e] + __popcll(tb.mask[e] & ((1ull << tk) - 1));
         tb.tok[row] = (uint8_t)tk;
         tb.wt[row] = weights[a];
+        if (FMT == kNvfp4) {
+            const Scales s = a == t ? early : scales(a);
+            tb.wt[row] *= s.t2;
+            // |g|, |u| < 2^(norm + shift) times the largest weight, 2688 t1, so |h| is below the square of that: 2^exp
+            // times at most 2^15
+            const int b = s.x.norm + s.x.shift + __builtin_amdgcn_frexp_expf(s.t1 * 2688.0f);
+            rows[row] = {s.t1, (int16_t)s.x.shift, (int16_t)(2 * b - 15)};
+        }
     }
     __syncthreads();
     return (int)uniform((uint32_t)total) >> 16;
 }
 
 // ------------------------------------------------------------------ the layer
-// Work is cut into tasks that the workgroups take from device-wide counters in order: a workgroup waits only for tasks
-// that running workgroups hold, so a call ends however few of its workgroups are resident at a time (another call's may
-// hold the rest of the chip, and wait as well).
+// Work is cut into tasks, and these into as many shares as there are workgroups: share i of G is tasks i, i + G, ... A
+// workgroup takes the next share from a device-wide counter, and another one when it is done. It waits only for tasks that
+// running workgroups hold, so a call ends however few of its workgroups are resident at a time (another call's may hold the
+// rest of the chip, and wait as well); where all are, each has one share. (Tasks taken one by one, two ahead of their use,
+// left the last workgroup 7 us behind the median one where each had four.)
 //
 //   choice   more than 8 tokens: 8 tokens a task, one per wave (up to 8 tokens every workgroup chooses for itself,
 //            which costs it less than waiting)
@@ -412,6 +513,18 @@ __device__ __forceinline__ void await(uint32_t* counter, uint32_t n) {
     __syncthreads();
 }
 
+// fc1 -> fc2. h is written through to memory (agent-scope stores), so that a workgroup has nothing to flush before it
+// counts its tasks as finished: a release fence writes the XCD's whole L2 back, 1 to 4 us. One thread of a workgroup
+// watches the count. (With a count per block of tokens, watched by every wave for the blocks it came to, 2000 waves
+// watching slowed fc1 down by a third.)
+__device__ __forceinline__ void store_through(uint16_t* p, uint32_t v) {
+    __hip_atomic_store(reinterpret_cast<uint32_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // fc1's operands of a wave in flight: D1 steps.
 template <int FMT>
 struct Stage1 {
@@ -424,23 +537,35 @@ struct Task1 {  // all scalars
 
 template <int FMT, int P>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
-    constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, D2 = Fmt<FMT>::D2, NF = Fmt<FMT>::kFrags;
+    constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, D2 = Fmt<FMT>::D2, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
     union Scratch {
         float part[2][kWaves][NB][16][17];  // fc1: each wave's sums
         float rows[kWaves][kMaxT][17];      // fc2: each wave's token rows
         struct {
-            int32_t ids[kMaxA];
-            float weights[kMaxA];
+            int32_t ids[kOwnChoice * kMaxK];
+            float weights[kOwnChoice * kMaxK];
             double val[kWaves][kMaxE];
         } c;                                // the choice
     };
     __shared__ Table tb;
     __shared__ Scratch sc;
-    __shared__ uint32_t next[2];
+    __shared__ uint32_t next;
+    __shared__ float bias[kMaxE];
+    __shared__ RowScale rows[FMT == kNvfp4 ? kMaxA : 1];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    uint32_t ticket = 0;  // thread 0's
-    if (threadIdx.x == 0) ticket = take(&p.count->fc1);
+    const int G = gridDim.x;
+    // Thread 0's shares of fc1 and fc2, asked for well before they are used: with the last task of the share before.
+    uint32_t share1 = 0, share2 = 0;
+    if (threadIdx.x == 0) share1 = take(&p.count->fc1);
+    auto tell = [&](uint32_t share) {  // all threads: what thread 0 took (a barrier on either side)
+        if (threadIdx.x == 0) next = share;
+        __syncthreads();
+        const uint32_t v = uniform(next);
+        __syncthreads();
+        return (int)v;
+    };
+    for (int e = threadIdx.x; e < p.E; e += kThreads) bias[e] = p.bias ? p.bias[e] : 0.0f;
 
     // ---- the choice
     auto choose_for = [&](int t0, int32_t* ids, float* weights) {  // tokens t0 .. t0 + 7, one per wave
@@ -450,7 +575,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
         if (t >= p.T) return;
         int id;
         float w;
-        choose<P>(p, sc.c.val[wave], lane, &id, &w);
+        choose<P>(p, sc.c.val[wave], bias, lane, &id, &w);
         if (lane < p.k) {
             ids[t * p.k + lane] = id;
             weights[t * p.k + lane] = w;
@@ -465,13 +590,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
                 p.ids[a] = sc.c.ids[a];
                 p.weights[a] = sc.c.weights[a];
             }
-        V = build(tb, p, sc.c.ids, sc.c.weights);
+        V = build<FMT>(tb, rows, p, sc.c.ids, sc.c.weights);
     } else {
         const uint32_t tasks = (uint32_t)(p.T + kWaves - 1) / kWaves;
         for (;;) {
-            if (threadIdx.x == 0) next[0] = take(&p.count->pick);
+            if (threadIdx.x == 0) next = take(&p.count->pick);
             __syncthreads();
-            const uint32_t c = uniform(next[0]);
+            const uint32_t c = uniform(next);
             if (c >= tasks) break;
             choose_for((int)c * kWaves, p.ids, p.weights);
             publish(&p.count->picked, 1);
@@ -481,22 +606,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
             __syncthreads();
         }
         await(&p.count->picked, tasks);
-        V = build(tb, p, p.ids, p.weights);
+        V = build<FMT>(tb, rows, p, p.ids, p.weights);
     }
 
     // ---- fc1
     const int JB = (p.f + 8 * NB - 1) / (8 * NB), N1 = V * JB;
-    const auto xr = rsrc(p.x, (uint32_t)p.T * (uint32_t)p.d * 2u);
+    const auto xr = rsrc(FMT == kNvfp4 ? p.xh : p.x, (uint32_t)p.T * (uint32_t)p.d * 2u);
     const uint32_t rb1 = Fmt<FMT>::row_bytes(p.d);
     const int steps1 = (int)(rb1 + 63) / 64, part1 = (steps1 + kWaves - 1) / kWaves;
     const int chunks = (part1 + D1 - 1) / D1, s_first = wave * part1, s_end = min(s_first + part1, steps1);
-    if (threadIdx.x == 0) {
-        next[0] = ticket;
-        next[1] = take(&p.count->fc1);
-    }
-    __syncthreads();
-    int cur = (int)uniform(next[0]), nxt = (int)uniform(next[1]);
-    __syncthreads();
     auto set = [&](int task) {
         const Block b = tb.blocks[task / JB];
         return Task1{(int)uniform(b.e), (int)uniform(b.n), (int)uniform(b.row0), task % JB * 8 * NB};
@@ -512,19 +630,37 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
         st.x[j] = load_x<FMT>(xr, xrow, p.d, o, ok && r < t.n);
     };
     auto token = [&](const Task1& t) { return (uint32_t)tb.tok[t.row0 + min(r, t.n - 1)]; };
+    // The epilogue's thread: two columns of a token, neighbours as the operand of fc2 holds them.
+    const int em = threadIdx.x / (4 * NB), eg = threadIdx.x / 4 % NB, ep = threadIdx.x & 3;
+    const int ej = FMT == kNvfp4 ? (ep & 1) * 4 + (ep >> 1) : 2 * ep, ej2 = ej + (FMT == kNvfp4 ? 2 : 1);
     uint32_t finished = 0;
-    if (cur < N1) {
+    int flip = 0;
+    bool asked = false;  // for a share of fc2
+    for (int i = tell(share1); i < G; i = tell(share1)) {
+        if (threadIdx.x == 0 && i >= N1) share1 = take(&p.count->fc1);
         Stage1<FMT> st;
-        Task1 t = set(cur);
+        Task1 t = set(min(i, N1 - 1));
         uint32_t xrow = token(t);
 #pragma unroll
-        for (int j = 0; j < D1; ++j) fetch(st, j, t, xrow, s_first + j);
-        int flip = 0;
-        while (cur < N1) {
-            if (threadIdx.x == 0) ticket = take(&p.count->fc1);
-            const bool more = nxt < N1;
-            const Task1 tn = set(more ? nxt : cur);
+        for (int j = 0; j < D1; ++j) fetch(st, j, t, xrow, i < N1 ? s_first + j : s_end);
+        for (int cur = i; cur < N1; cur += G) {
+            const bool more = cur + G < N1;
+            if (threadIdx.x == 0 && !more) {
+                share1 = take(&p.count->fc1);
+                if (!asked) share2 = take(&p.count->fc2);
+            }
+            asked |= !more;
+            const Task1 tn = set(more ? cur + G : cur);
             const uint32_t xnext = token(tn);
+            float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // int8: the epilogue's channel scales, ahead of the loads that follow
+            if (FMT == kInt8 && wave < NB) {
+                const float* s = static_cast<const float*>(p.s1) + (int64_t)t.e * 2 * p.f;
+                const int c = min(t.c0 + 8 * eg + ej, p.f - 2);
+                cs[0] = s[c];
+                cs[1] = s[c + 1];
+                cs[2] = s[p.f + c];
+                cs[3] = s[p.f + c + 1];
+            }
             f32x4 acc[NB];
 #pragma unroll
             for (int g = 0; g < NB; ++g) acc[g] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -538,7 +674,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
 #pragma unroll
                     for (int i = 0; i < NF; ++i)
 #pragma unroll
-                        for (int g = 0; g < NB; ++g) acc[g] = mfma(decode<FMT>(st.w[j][g], i), st.x[j].v[i], acc[g]);
+                        for (int g = 0; g < NB; ++g) acc[g] = mfma<FMT>(decode<FMT>(st.w[j][g], i), st.x[j].v[i], acc[g]);
                     fetch(st, j, tl, xl, sl + j);
                 }
             }
@@ -549,63 +685,78 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sc.part[flip][wave][g][r][4 * q + i] = acc[g][i];
             }
-            if (threadIdx.x == 0) next[flip] = ticket;
             lds_barrier();
-            if (wave < 2 * NB) {
-                const int cc = threadIdx.x % (8 * NB), i = threadIdx.x / (8 * NB), g8 = cc / 8, j = cc % 8;
-                const int col = t.c0 + cc;
-                if (i < t.n && col < p.f) {
-                    float g = sc.part[flip][0][g8][i][j], u = sc.part[flip][0][g8][i][8 + j];
+            if (wave < NB) {
+                const int col = t.c0 + 8 * eg + ej;
+                if (em < t.n && t.c0 + 8 * eg < p.f) {
+                    float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
 #pragma unroll
-                    for (int w = 1; w < kWaves; ++w) {
-                        g += sc.part[flip][w][g8][i][j];
-                        u += sc.part[flip][w][g8][i][8 + j];
+                    for (int w = 0; w < kWaves; ++w) {
+                        const float* s = sc.part[flip][w][eg][em];
+                        g[0] += s[ej];
+                        g[1] += s[ej2];
+                        u[0] += s[8 + ej];
+                        u[1] += s[8 + ej2];
                     }
-                    if (FMT == kInt8) {
-                        const float* s = static_cast<const float*>(p.s1) + (int64_t)t.e * 2 * p.f + col;
-                        g *= s[0];
-                        u *= s[p.f];
-                    } else if (FMT == kNvfp4) {
-                        g *= p.t1[t.e];
-                        u *= p.t1[t.e];
+                    float h[2];
+                    RowScale rs{};
+                    if (FMT == kNvfp4) rs = rows[t.row0 + em];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (FMT == kInt8) {
+                            g[j] *= cs[j];
+                            u[j] *= cs[2 + j];
+                        } else if (FMT == kNvfp4) {
+                            g[j] = __builtin_amdgcn_ldexpf(g[j] * rs.t1, rs.shift);
+                            u[j] = __builtin_amdgcn_ldexpf(u[j] * rs.t1, rs.shift);
+                        }
+                        h[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[j])) * u[j];
                     }
-                    const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-                    const uint32_t hi = bf16x2_rne(h, h) & 0xFFFFu;
-                    // (of an infinite h the first part is all)
-                    const float left = (hi & 0x7F80u) == 0x7F80u ? 0.0f : h - bf16_to_f32(hi);
-                    uint16_t* o = p.h + ((int64_t)(t.row0 + i) * p.f + col / 8 * 8) * 2 + col % 8;
-                    o[0] = (uint16_t)hi;
-                    o[8] = (uint16_t)bf16x2_rne(left, left);
+                    uint16_t* o = p.h + ((int64_t)(t.row0 + em) * p.f + (col & ~7)) * HP + 2 * ep;
+                    if (FMT == kNvfp4) {
+                        const half2v v = {(_Float16)__builtin_amdgcn_ldexpf(h[0], -rs.exp),
+                                          (_Float16)__builtin_amdgcn_ldexpf(h[1], -rs.exp)};
+                        store_through(o, __builtin_bit_cast(uint32_t, v));
+                    } else {
+                        const uint32_t hi = bf16x2_rne(h[0], h[1]);
+                        // (of an infinite h the first part is all)
+                        const float l0 = (hi & 0x7F80u) == 0x7F80u ? 0.0f : h[0] - __uint_as_float(hi << 16);
+                        const float l1 = (hi & 0x7F800000u) == 0x7F800000u ? 0.0f : h[1] - __uint_as_float(hi & 0xFFFF0000u);
+                        store_through(o, hi);
+                        store_through(o + 8, bf16x2_rne(l0, l1));
+                    }
                 }
             }
             ++finished;
-            cur = nxt;
-            nxt = (int)uniform(next[flip]);
             t = tn;
             xrow = xnext;
             flip ^= 1;  // (the next task's sums go to the other half while slow threads still read this one)
         }
     }
-    if (finished) publish(&p.count->done, finished);
-    else __syncthreads();
+    wait_vm<0>();  // this wave's h is in memory
+    __syncthreads();
+    if (threadIdx.x == 0 && finished)
+        __hip_atomic_fetch_add(&p.count->done, finished, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 
     // ---- fc2 + combine
-    const auto hr = rsrc(p.h, (uint32_t)(p.T * p.k) * (uint32_t)p.f * 4u);
+    const auto hr = rsrc(p.h, (uint32_t)(p.T * p.k) * (uint32_t)p.f * (2u * HP));
     const uint32_t rb2 = Fmt<FMT>::row_bytes(p.f);
     const int S = (int)(rb2 + 63) / 64, total = V * S, part2 = (total + kWaves - 1) / kWaves;
     const int first = min(wave * part2, total), end = min(first + part2, total);
     const int N2 = (p.d + 15) / 16;
     bool waited = false;
-    for (;;) {
-        if (threadIdx.x == 0) next[0] = take(&p.count->fc2);
-        __syncthreads();
-        const int task = (int)uniform(next[0]);
-        if (task >= N2) break;
+    if (threadIdx.x == 0 && !asked) share2 = take(&p.count->fc2);
+    for (int i = tell(share2); i < G; i = tell(share2)) {
+      if (i >= N2) {
+        if (threadIdx.x == 0) share2 = take(&p.count->fc2);
+        continue;
+      }
+      for (int task = i; task < N2; task += G) {
         const int n0 = task * 16;
         const bool w_ok = n0 + r < p.d;
-        for (int i = threadIdx.x; i < kWaves * kMaxT * 17; i += kThreads) (&sc.rows[0][0][0])[i] = 0.0f;
+        for (int z = threadIdx.x; z < kWaves * kMaxT * 17; z += kThreads) (&sc.rows[0][0][0])[z] = 0.0f;
         W16 w[D2];
-        u32x4 x[D2][NF][2];
+        u32x4 x[D2][NF][HP];
         int wv = first / S, ws = first - wv * S, xv = wv, xs = ws, cv = wv, cs = ws;  // next weights, h, products
         auto fetch_w = [&](int j, bool live) {
             const int e = __builtin_amdgcn_readfirstlane((int)tb.blocks[live ? wv : 0].e);
@@ -621,13 +772,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
             const Block b = tb.blocks[live ? xv : 0];
             const int n = __builtin_amdgcn_readfirstlane(b.n), row0 = __builtin_amdgcn_readfirstlane((int)b.row0);
             const uint32_t o = (uint32_t)xs * 64 + q * 16;
-            const uint32_t at = (uint32_t)(row0 + r) * (uint32_t)p.f * 4u + o / 16 * (NF * 32);
+            const uint32_t at = (uint32_t)(row0 + r) * (uint32_t)p.f * (2u * HP) + o / 16 * (NF * HP * 16);
 #pragma unroll
             for (int i = 0; i < NF; ++i)
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                for (int half = 0; half < HP; ++half)
                     x[j][i][half] = __builtin_amdgcn_raw_buffer_load_b128(
-                        hr, live && o < rb2 && r < n ? at + 32 * i + 16 * half : kNowhere, 0, 0);
+                        hr, live && o < rb2 && r < n ? at + 16 * (HP * i + half) : kNowhere, 0, 0);
             if (++xs == S) {
                 xs = 0;
                 ++xv;
@@ -635,11 +786,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
         };
 #pragma unroll
         for (int j = 0; j < D2; ++j) fetch_w(j, first + j < end);
-        if (waited) __syncthreads();
+        if (waited) __syncthreads();  // (sc.rows is clear)
         else await(&p.count->done, (uint32_t)N1);
         waited = true;
 #pragma unroll
         for (int j = 0; j < D2; ++j) fetch_x(j, first + j < end);
+        // (asked for only now, when every workgroup has had time to take its first share)
+        if (threadIdx.x == 0 && task + G >= N2) share2 = take(&p.count->fc2);
+        auto channel_scales = [&](int b) {  // int8: of this lane's columns in a block's expert, a block ahead of their use
+            f32x4 s = {1.0f, 1.0f, 1.0f, 1.0f};
+            if (FMT == kInt8 && first < end) {
+                const int e = (int)uniform((uint32_t)(int)tb.blocks[min(b, V - 1)].e);
+                s = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.s2) + (int64_t)e * p.d +
+                                                    min(n0 + 4 * q, p.d - 4));
+            }
+            return s;
+        };
+        f32x4 cscale = channel_scales(cv);
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int i0 = first; i0 < end; i0 += D2) {
 #pragma unroll
@@ -647,9 +810,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
                 if (i0 + j < end) {
 #pragma unroll
                     for (int i = 0; i < NF; ++i) {
-                        const bf16x8 v = decode<FMT>(w[j], i);
-                        acc = mfma(v, x[j][i][0], acc);
-                        acc = mfma(v, x[j][i][1], acc);
+                        const u32x4 v = decode<FMT>(w[j], i);
+#pragma unroll
+                        for (int half = 0; half < HP; ++half) acc = mfma<FMT>(v, x[j][i][half], acc);
                     }
                 }
                 const bool live = i0 + D2 + j < end;
@@ -660,18 +823,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
                     if (r < b.n) {
                         const float wt = tb.wt[b.row0 + r];
                         float* o = sc.rows[wave][tb.tok[b.row0 + r]] + 4 * q;
+                        if (FMT == kInt8) acc *= cscale;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float v = acc[i];
-                            if (FMT == kInt8) {
-                                const int c = min(n0 + 4 * q + i, p.d - 1);
-                                v *= static_cast<const float*>(p.s2)[(int64_t)b.e * p.d + c];
-                            } else if (FMT == kNvfp4) {
-                                v *= p.t2[b.e];
-                            }
+                            const float v = FMT == kNvfp4 ? __builtin_amdgcn_ldexpf(acc[i], rows[b.row0 + r].exp) : acc[i];
                             o[i] = __builtin_fmaf(wt, v, o[i]);
                         }
                     }
+                    cscale = channel_scales(cv + 1);
                     acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
                     cs = 0;
                     ++cv;
@@ -690,6 +849,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
             p.out[at] = (uint16_t)bf16x2_rne(v, v);
         }
         __syncthreads();
+      }
     }
 }
 
@@ -710,9 +870,12 @@ int router_parts(int64_t T, int64_t d, int64_t E) {
 }
 size_t carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t f, Args* p) {
     p->parts = router_parts(T, d, E);
+    p->max_blocks = (int)std::min<int64_t>(T * k, E + T * k / 16);
     p->count = c.take<Counters>(1);
     p->logits = c.take<double>((size_t)(p->parts * T * E));
     p->h = c.take<uint16_t>((size_t)(2 * T * k * f));
+    p->xh = c.take<uint16_t>((size_t)(T * d));
+    p->xs = c.take<TokenScale>((size_t)T);
     return c.need;
 }
 
@@ -720,15 +883,14 @@ template <int FMT, int P>
 void launch_layer(const Args& p, hipStream_t s) {
     constexpr int NB = Fmt<FMT>::NB;
     // as many workgroups as have a task, at most one per CU (their registers and LDS let no more be resident)
-    const int64_t blocks = std::min(p.T * p.k, p.E + p.T * p.k / 16);
-    const int64_t tasks = std::max<int64_t>(blocks * ((p.f + 8 * NB - 1) / (8 * NB)), (p.d + 15) / 16);
+    const int64_t tasks = std::max<int64_t>((int64_t)p.max_blocks * ((p.f + 8 * NB - 1) / (8 * NB)), (p.d + 15) / 16);
     const unsigned grid = (unsigned)std::min<int64_t>(tasks, device_cus());
     hipLaunchKernelGGL((k_decode_layer<FMT, P>), dim3(grid), dim3(kThreads), 0, s, p);
 }
 template <int FMT>
 int run(const Args& p, hipStream_t s) {
-    const dim3 grid((unsigned)(p.E + 15) / 16, (unsigned)(p.T + 15) / 16, (unsigned)p.parts);
-    hipLaunchKernelGGL(k_decode_router, grid, dim3(64 * kRouterWaves), 0, s, p);
+    const unsigned grid = (unsigned)((p.E + 15) / 16 * ((p.T + 15) / 16) * p.parts + (FMT == kNvfp4 ? p.T : 0));
+    hipLaunchKernelGGL(k_decode_router<FMT == kNvfp4>, dim3(grid), dim3(kRouterThreads), 0, s, p);
     if (p.E <= 64) launch_layer<FMT, 1>(p, s);
     else if (p.E <= 128) launch_layer<FMT, 2>(p, s);
     else if (p.E <= 256) launch_layer<FMT, 4>(p, s);
