@@ -50,6 +50,7 @@ constexpr int64_t kMaxBytes = 0xFFFFFE00ll;
 struct Counters {
     uint32_t pick, picked;  // tasks of the choice taken, finished
     uint32_t fc1, done;     // shares of fc1 taken, tasks of it finished
+    uint32_t tail;          // tasks taken of fc1's tail
     uint32_t fc2;           // shares of fc2 taken
 };
 // x of a token for NVFP4 weights is its fp16 values times 2^shift; the sum of these values' magnitudes is below 2^norm.
@@ -92,7 +93,7 @@ struct Fmt {
     static constexpr int kVals = FMT == kBf16 ? 8 : FMT == kInt8 ? 16 : 32;  // in 16 bytes
     static constexpr int kFrags = kVals / 8;
     static constexpr int NB = FMT == kBf16 ? 1 : 2;         // fc1: groups of 16 weight rows of a wave
-    static constexpr int D1 = FMT == kBf16 ? 8 : 4, D2 = 8;  // steps in flight in fc1, fc2
+    static constexpr int D1 = FMT == kBf16 ? 8 : 4, D2 = FMT == kNvfp4 ? 6 : 8;  // steps in flight in fc1, fc2
     static constexpr int kParts = FMT == kNvfp4 ? 1 : 2;    // 16-bit parts of h
     static __host__ __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)(K / kVals) * 16u; }
 };
@@ -539,7 +540,10 @@ template <int FMT, int P>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
     constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, D2 = Fmt<FMT>::D2, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
     union Scratch {
-        float part[2][kWaves][NB][16][17];  // fc1: each wave's sums
+        struct {
+            float part[2][kWaves][NB][16][17];  // fc1: each wave's sums
+            uint32_t told[2];                   // and a task
+        };
         float rows[kWaves][kMaxT][17];      // fc2: each wave's token rows
         struct {
             int32_t ids[kOwnChoice * kMaxK];
@@ -636,21 +640,31 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
     uint32_t finished = 0;
     int flip = 0;
     bool asked = false;  // for a share of fc2
+    // Shares of fc1 are of the tasks before `tail`, whole rounds; the rest is taken task by task, two ahead of its use.
+    const int tail = N1 >= 8 * G ? (N1 / G - 4) * G : N1;
     for (int i = tell(share1); i < G; i = tell(share1)) {
-        if (threadIdx.x == 0 && i >= N1) share1 = take(&p.count->fc1);
         Stage1<FMT> st;
-        Task1 t = set(min(i, N1 - 1));
+        int cur = i < tail ? i : N1, nxt = cur + G;
+        if (cur >= N1) {
+            if (threadIdx.x == 0) share1 = take(&p.count->fc1);
+            continue;
+        }
+        Task1 t = set(cur);
         uint32_t xrow = token(t);
 #pragma unroll
-        for (int j = 0; j < D1; ++j) fetch(st, j, t, xrow, i < N1 ? s_first + j : s_end);
-        for (int cur = i; cur < N1; cur += G) {
-            const bool more = cur + G < N1;
-            if (threadIdx.x == 0 && !more) {
-                share1 = take(&p.count->fc1);
-                if (!asked) share2 = take(&p.count->fc2);
+        for (int j = 0; j < D1; ++j) fetch(st, j, t, xrow, s_first + j);
+        for (; cur < N1;) {
+            const bool more = nxt < N1;
+            // the task after the next one: of the share, or of the tail (thread 0 asks; told at this task's barrier)
+            const bool ask = tail < N1 && nxt + G >= tail;
+            uint32_t got = 0;
+            if (threadIdx.x == 0) {
+                if (ask) got = take(&p.count->tail);
+                if (!more) share1 = take(&p.count->fc1);
+                if (!more && !asked) share2 = take(&p.count->fc2);
             }
             asked |= !more;
-            const Task1 tn = set(more ? cur + G : cur);
+            const Task1 tn = set(more ? nxt : cur);
             const uint32_t xnext = token(tn);
             float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // int8: the epilogue's channel scales, ahead of the loads that follow
             if (FMT == kInt8 && wave < NB) {
@@ -685,7 +699,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sc.part[flip][wave][g][r][4 * q + i] = acc[g][i];
             }
+            if (ask && threadIdx.x == 0) sc.told[flip] = got;
             lds_barrier();
+            const int after = ask ? tail + (int)uniform(sc.told[flip]) : nxt + G;
             if (wave < NB) {
                 const int col = t.c0 + 8 * eg + ej;
                 if (em < t.n && t.c0 + 8 * eg < p.f) {
@@ -728,6 +744,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
                 }
             }
             ++finished;
+            cur = nxt;
+            nxt = after;
             t = tn;
             xrow = xnext;
             flip ^= 1;  // (the next task's sums go to the other half while slow threads still read this one)
