@@ -44,14 +44,17 @@ constexpr int kMaxA = kMaxT * kMaxK;
 constexpr int kMaxV = kMaxE + kMaxA / 16;  // blocks of at most 16 tokens of one expert
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr uint32_t kNowhere = 0xFFFFFFE0u;
+constexpr int kAgentScope = 16;  // buffer loads: the sc1 bit, as an agent-scope atomic load has it
 constexpr int64_t kMaxBytes = 0xFFFFFE00ll;
 
 // Device-wide counters of one call, cleared by k_decode_router.
 struct Counters {
     uint32_t pick, picked;  // tasks of the choice taken, finished
-    uint32_t fc1, done;     // shares of fc1 taken, tasks of it finished
-    uint32_t tail;          // tasks taken of fc1's tail
+    uint32_t fc1, tail;     // shares of fc1 taken, tasks taken of its tail
     uint32_t fc2;           // shares of fc2 taken
+    uint32_t done;          // tasks of fc1 finished
+    uint32_t pad[26];
+    uint32_t block[64];     // the same of each block of tokens, where there are few
 };
 // x of a token for NVFP4 weights is its fp16 values times 2^shift; the sum of these values' magnitudes is below 2^norm.
 struct TokenScale {
@@ -93,7 +96,7 @@ struct Fmt {
     static constexpr int kVals = FMT == kBf16 ? 8 : FMT == kInt8 ? 16 : 32;  // in 16 bytes
     static constexpr int kFrags = kVals / 8;
     static constexpr int NB = FMT == kBf16 ? 1 : 2;         // fc1: groups of 16 weight rows of a wave
-    static constexpr int D1 = FMT == kBf16 ? 8 : 4, D2 = FMT == kNvfp4 ? 6 : 8;  // steps in flight in fc1, fc2
+    static constexpr int D1 = FMT == kBf16 ? 8 : 4;         // steps in flight in fc1
     static constexpr int kParts = FMT == kNvfp4 ? 1 : 2;    // 16-bit parts of h
     static __host__ __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)(K / kVals) * 16u; }
 };
@@ -246,7 +249,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_decode_router(Args p) {
     __shared__ double red[kRouterWaves][16][17];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = Counters{};
+    if (blockIdx.x == 0 && threadIdx.x < sizeof(Counters) / 4) reinterpret_cast<uint32_t*>(p.count)[threadIdx.x] = 0;
     int b = blockIdx.x;
     if (HALF) {
         if (b < p.T) return scale_token(p, b);
@@ -477,8 +480,7 @@ __device__ __forceinline__ int build(Table& tb, RowScale* rows, const Args& p, c
 // Work is cut into tasks, and these into as many shares as there are workgroups: share i of G is tasks i, i + G, ... A
 // workgroup takes the next share from a device-wide counter, and another one when it is done. It waits only for tasks that
 // running workgroups hold, so a call ends however few of its workgroups are resident at a time (another call's may hold the
-// rest of the chip, and wait as well); where all are, each has one share. (Tasks taken one by one, two ahead of their use,
-// left the last workgroup 7 us behind the median one where each had four.)
+// rest of the chip, and wait as well); where all are, each has one share.
 //
 //   choice   more than 8 tokens: 8 tokens a task, one per wave (up to 8 tokens every workgroup chooses for itself,
 //            which costs it less than waiting)
@@ -515,11 +517,22 @@ __device__ __forceinline__ void await(uint32_t* counter, uint32_t n) {
 }
 
 // fc1 -> fc2. h is written through to memory (agent-scope stores), so that a workgroup has nothing to flush before it
-// counts its tasks as finished: a release fence writes the XCD's whole L2 back, 1 to 4 us. One thread of a workgroup
-// watches the count. (With a count per block of tokens, watched by every wave for the blocks it came to, 2000 waves
-// watching slowed fc1 down by a third.)
+// counts a task as finished: a release fence writes the XCD's whole L2 back, 1 to 4 us.
+//
+// FEW (at most kFewRows rows of h): fc2 waits block by block, so that the first experts' W2 is read while the last
+// workgroups are still busy with fc1 (they end some 5 us after the median one), and reads h past the L2, so that no wave
+// has to invalidate anything (2000 invalidations took 14 us). A task counts as finished a task later: the waves wait until
+// no more of their memory operations are outstanding than the loads they have issued since, which costs nothing, and
+// thread 0 counts after the barrier that follows. (One token on NVFP4 weights 46.7 us waiting for all of fc1, 43.8 so;
+// three tokens of a small layer 26.3 and 23.1; one bf16 token the same; two bf16 tokens, 16 rows, 104 and 126.)
+// Else one thread of a workgroup waits for all of fc1 and invalidates, and h is read through the L2, which serves it to 32
+// CUs (64 int8 tokens: 627 us; past the L2, block by block, 800).
+constexpr int kFewRows = 8;
 __device__ __forceinline__ void store_through(uint16_t* p, uint32_t v) {
     __hip_atomic_store(reinterpret_cast<uint32_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void count_up(uint32_t* counter, uint32_t n) {
+    __hip_atomic_fetch_add(counter, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -533,12 +546,13 @@ struct Stage1 {
     X16<FMT> x[Fmt<FMT>::D1];
 };
 struct Task1 {  // all scalars
-    int e, n, row0, c0;
+    int block, e, n, row0, c0;
 };
 
-template <int FMT, int P>
+template <int FMT, int P, bool FEW>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
-    constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, D2 = Fmt<FMT>::D2, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
+    constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
+    constexpr int D2 = FMT == kNvfp4 && !FEW ? 6 : 8;  // steps in flight in fc2
     union Scratch {
         struct {
             float part[2][kWaves][NB][16][17];  // fc1: each wave's sums
@@ -620,8 +634,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
     const int steps1 = (int)(rb1 + 63) / 64, part1 = (steps1 + kWaves - 1) / kWaves;
     const int chunks = (part1 + D1 - 1) / D1, s_first = wave * part1, s_end = min(s_first + part1, steps1);
     auto set = [&](int task) {
-        const Block b = tb.blocks[task / JB];
-        return Task1{(int)uniform(b.e), (int)uniform(b.n), (int)uniform(b.row0), task % JB * 8 * NB};
+        const int i = task / JB;
+        const Block b = tb.blocks[i];
+        return Task1{i, (int)uniform(b.e), (int)uniform(b.n), (int)uniform(b.row0), task % JB * 8 * NB};
     };
     auto fetch = [&](Stage1<FMT>& st, int j, const Task1& t, uint32_t xrow, int s) {
         const Matrix<FMT> m(p.w1, p.s1, t.e, 2 * p.f, p.d);
@@ -637,11 +652,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
     // The epilogue's thread: two columns of a token, neighbours as the operand of fc2 holds them.
     const int em = threadIdx.x / (4 * NB), eg = threadIdx.x / 4 % NB, ep = threadIdx.x & 3;
     const int ej = FMT == kNvfp4 ? (ep & 1) * 4 + (ep >> 1) : 2 * ep, ej2 = ej + (FMT == kNvfp4 ? 2 : 1);
-    uint32_t finished = 0;
+    uint32_t finished = 0;  // tasks
+    int pending = -1;       // FEW: block of the finished task that is not counted yet
     int flip = 0;
     bool asked = false;  // for a share of fc2
-    // Shares of fc1 are of the tasks before `tail`, whole rounds; the rest is taken task by task, two ahead of its use.
-    const int tail = N1 >= 8 * G ? (N1 / G - 4) * G : N1;
+    // Where fc1 is long, shares are of the tasks before `tail`, whole rounds, and the rest is taken task by task, two ahead
+    // of its use (64 tokens on NVFP4 weights: the last workgroup ends 6 us after the median one instead of 34).
+    const int tail = N1 >= 24 * G ? (N1 / G - 4) * G : N1;
     for (int i = tell(share1); i < G; i = tell(share1)) {
         Stage1<FMT> st;
         int cur = i < tail ? i : N1, nxt = cur + G;
@@ -700,7 +717,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
                     for (int i = 0; i < 4; ++i) sc.part[flip][wave][g][r][4 * q + i] = acc[g][i];
             }
             if (ask && threadIdx.x == 0) sc.told[flip] = got;
+            if (FEW) wait_vm<D1 * (NB * (FMT == kNvfp4 ? 2 : 1) + NF)>();  // the loads of the next task's first steps
             lds_barrier();
+            if (FEW && threadIdx.x == 0 && pending >= 0) count_up(&p.count->block[pending], 1);
             const int after = ask ? tail + (int)uniform(sc.told[flip]) : nxt + G;
             if (wave < NB) {
                 const int col = t.c0 + 8 * eg + ej;
@@ -744,6 +763,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
                 }
             }
             ++finished;
+            pending = t.block;
             cur = nxt;
             nxt = after;
             t = tn;
@@ -753,8 +773,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
     }
     wait_vm<0>();  // this wave's h is in memory
     __syncthreads();
-    if (threadIdx.x == 0 && finished)
-        __hip_atomic_fetch_add(&p.count->done, finished, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0 && finished) {
+        if (FEW) count_up(&p.count->block[pending], 1);
+        else count_up(&p.count->done, finished);
+    }
 
     // ---- fc2 + combine
     const auto hr = rsrc(p.h, (uint32_t)(p.T * p.k) * (uint32_t)p.f * (2u * HP));
@@ -763,6 +785,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
     const int first = min(wave * part2, total), end = min(first + part2, total);
     const int N2 = (p.d + 15) / 16;
     bool waited = false;
+    int upto = FEW ? first / S : V;  // blocks of this wave's run before this one have their h
+    auto ready = [&](int b) {
+        while (b >= upto) {
+            const int at = min(b + lane, 63);
+            const bool there = __hip_atomic_load(&p.count->block[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)JB;
+            const uint64_t waits = ~__ballot(there);
+            const int n = waits ? __builtin_ctzll(waits) : 64;
+            upto = b + n;
+            if (n == 0) __builtin_amdgcn_s_sleep(16);
+        }
+        asm volatile("" ::: "memory");
+    };
     if (threadIdx.x == 0 && !asked) share2 = take(&p.count->fc2);
     for (int i = tell(share2); i < G; i = tell(share2)) {
       if (i >= N2) {
@@ -787,6 +821,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
             }
         };
         auto fetch_x = [&](int j, bool live) {
+            if (FEW && live) ready(xv);
             const Block b = tb.blocks[live ? xv : 0];
             const int n = __builtin_amdgcn_readfirstlane(b.n), row0 = __builtin_amdgcn_readfirstlane((int)b.row0);
             const uint32_t o = (uint32_t)xs * 64 + q * 16;
@@ -796,7 +831,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
 #pragma unroll
                 for (int half = 0; half < HP; ++half)
                     x[j][i][half] = __builtin_amdgcn_raw_buffer_load_b128(
-                        hr, live && o < rb2 && r < n ? at + 16 * (HP * i + half) : kNowhere, 0, 0);
+                        hr, live && o < rb2 && r < n ? at + 16 * (HP * i + half) : kNowhere, 0, FEW ? kAgentScope : 0);
             if (++xs == S) {
                 xs = 0;
                 ++xv;
@@ -804,7 +839,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
         };
 #pragma unroll
         for (int j = 0; j < D2; ++j) fetch_w(j, first + j < end);
-        if (waited) __syncthreads();  // (sc.rows is clear)
+        if (FEW || waited) __syncthreads();  // (sc.rows is clear)
         else await(&p.count->done, (uint32_t)N1);
         waited = true;
 #pragma unroll
@@ -897,24 +932,26 @@ size_t carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t f, Args*
     return c.need;
 }
 
-template <int FMT, int P>
+template <int FMT, int P, bool FEW>
 void launch_layer(const Args& p, hipStream_t s) {
     constexpr int NB = Fmt<FMT>::NB;
     // as many workgroups as have a task, at most one per CU (their registers and LDS let no more be resident)
     const int64_t tasks = std::max<int64_t>((int64_t)p.max_blocks * ((p.f + 8 * NB - 1) / (8 * NB)), (p.d + 15) / 16);
     const unsigned grid = (unsigned)std::min<int64_t>(tasks, device_cus());
-    hipLaunchKernelGGL((k_decode_layer<FMT, P>), dim3(grid), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_decode_layer<FMT, P, FEW>), dim3(grid), dim3(kThreads), 0, s, p);
+}
+template <int FMT, int P>
+void launch_rows(const Args& p, hipStream_t s) {
+    if (p.T <= kOwnChoice && p.T * p.k <= kFewRows) launch_layer<FMT, P, true>(p, s);
+    else launch_layer<FMT, P, false>(p, s);
 }
 template <int FMT>
 int run(const Args& p, hipStream_t s) {
     const unsigned grid = (unsigned)((p.E + 15) / 16 * ((p.T + 15) / 16) * p.parts + (FMT == kNvfp4 ? p.T : 0));
     hipLaunchKernelGGL(k_decode_router<FMT == kNvfp4>, dim3(grid), dim3(kRouterThreads), 0, s, p);
-    if (p.E <= 64) launch_layer<FMT, 1>(p, s);
-    else if (p.E <= 128) launch_layer<FMT, 2>(p, s);
-    else if (p.E <= 256) launch_layer<FMT, 4>(p, s);
-    else if (p.E <= 384) launch_layer<FMT, 6>(p, s);
-    else if (p.E <= 512) launch_layer<FMT, 8>(p, s);
-    else launch_layer<FMT, 16>(p, s);
+    if (p.E <= 128) launch_rows<FMT, 2>(p, s);
+    else if (p.E <= 384) launch_rows<FMT, 6>(p, s);
+    else launch_rows<FMT, 16>(p, s);
     return launch_status();
 }
 
