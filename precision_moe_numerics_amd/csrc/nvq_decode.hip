@@ -1,11 +1,20 @@
 // nvq_decode.hip -- a whole mixture-of-experts layer for a few tokens (up to
 // 64, single tokens being decoded): router, chosen experts and weighted combine
-// on bf16, int8 or NVFP4 weights, in two launches.
+// on bf16, int8 or NVFP4 weights.
 //
 //   k_decode_router   logits = x Wr^T
-//   k_decode_layer    ids, weights = top-k of the logits;
-//                     h = silu(g) * u of every (expert, token) pair;
-//                     out = residual + sum_s weight * (W2 h)
+//   k_decode_fc1      ids, weights = top-k of the logits (k_decode_choice where
+//                     tokens are more than eight);
+//                     h = silu(g) * u of every (expert, token) pair
+//   k_decode_fc2      out = residual + sum_s weight * (W2 h)
+//
+// All of it after the router in one kernel, whose workgroups took tasks from
+// device counters, handed h over through memory and had their first W2 in
+// flight while they waited, was built and measured too. For 8 of 384 experts,
+// d 4096, f 1024 (us, that kernel and these): one bf16 token 65 and 56, four
+// int8 tokens 113 and 102, one NVFP4 token 43 and 38, 64 of them 515 and 497.
+// Noticing that the last workgroup is done and reading h past the caches costs
+// more than a launch.
 //
 // Bound by reading the chosen experts' weights once. The activations are not
 // quantized: they are a few rows, and it would save nothing. A weight reaches
@@ -26,7 +35,6 @@
 #include "nvq_host.hpp"
 
 #include <algorithm>
-#include <type_traits>
 
 namespace nvq {
 namespace {
@@ -43,19 +51,9 @@ constexpr int kMaxK = 64;
 constexpr int kMaxA = kMaxT * kMaxK;
 constexpr int kMaxV = kMaxE + kMaxA / 16;  // blocks of at most 16 tokens of one expert
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr uint32_t kNowhere = 0xFFFFFFE0u;
-constexpr int kAgentScope = 16;  // buffer loads: the sc1 bit, as an agent-scope atomic load has it
-constexpr int64_t kMaxBytes = 0xFFFFFE00ll;
+constexpr int64_t kMaxBytes = 0xFFFFFE00ll;     // of a buffer
+constexpr uint32_t kNowhere = (uint32_t)kMaxBytes;  // an offset behind any buffer's end, also with 511 added: reads zeros
 
-// Device-wide counters of one call, cleared by k_decode_router.
-struct Counters {
-    uint32_t pick, picked;  // tasks of the choice taken, finished
-    uint32_t fc1, tail;     // shares of fc1 taken, tasks taken of its tail
-    uint32_t fc2;           // shares of fc2 taken
-    uint32_t done;          // tasks of fc1 finished
-    uint32_t pad[26];
-    uint32_t block[64];     // the same of each block of tokens, where there are few
-};
 // x of a token for NVFP4 weights is its fp16 values times 2^shift; the sum of these values' magnitudes is below 2^norm.
 struct TokenScale {
     int32_t shift, norm;
@@ -76,7 +74,8 @@ struct Args {
     uint16_t* h;              // [T k, f], rows in expert order; bf16: each eight values' high, then low parts
     uint16_t* xh;             // NVFP4: [T, d] fp16 (both in the order of half_slot)
     TokenScale* xs;
-    Counters* count;
+    uint32_t* tail;           // tasks taken of fc1's tail (k_decode_router clears it)
+    struct Plan* plan;        // fc1's table, for fc2
     int T, d, E, k, f, sigmoid, parts, max_blocks;
 };
 
@@ -179,10 +178,9 @@ struct Matrix {
 template <int FMT>
 __device__ __forceinline__ X16<FMT> load_x(__amdgpu_buffer_rsrc_t x, uint32_t row, int K, uint32_t o, bool ok) {
     X16<FMT> r;
+    const uint32_t at = ok ? row * (uint32_t)K * 2u + o / 16 * (2u * Fmt<FMT>::kVals) : kNowhere;
 #pragma unroll
-    for (int i = 0; i < Fmt<FMT>::kFrags; ++i)
-        r.v[i] = __builtin_amdgcn_raw_buffer_load_b128(
-            x, ok ? row * (uint32_t)K * 2u + (o / 16 * Fmt<FMT>::kVals + 8 * i) * 2u : kNowhere, 0, 0);
+    for (int i = 0; i < Fmt<FMT>::kFrags; ++i) r.v[i] = __builtin_amdgcn_raw_buffer_load_b128(x, at + 16 * i, 0, 0);
     return r;
 }
 
@@ -249,7 +247,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_decode_router(Args p) {
     __shared__ double red[kRouterWaves][16][17];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    if (blockIdx.x == 0 && threadIdx.x < sizeof(Counters) / 4) reinterpret_cast<uint32_t*>(p.count)[threadIdx.x] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.tail = 0;
     int b = blockIdx.x;
     if (HALF) {
         if (b < p.T) return scale_token(p, b);
@@ -384,30 +382,39 @@ __device__ __forceinline__ void choose(const Args& p, const double* val, const f
     *weight = (float)(v / sum);
 }
 
-// The chosen experts and their tokens, in LDS of every workgroup: blocks of at most 16 tokens of one expert, in
-// ascending expert order; row row0 + i of h, tok and wt is token i of the block.
+// The chosen experts and their tokens: blocks of at most 16 tokens of one expert, in ascending expert order; row
+// row0 + i of h and of rows is token i of the block.
 struct Block {
     int16_t e;
     int16_t row0;
     int32_t n;
 };
+struct Row {
+    float wt;       // routing weight; NVFP4: times w2's tensor scale
+    int16_t exp;    // NVFP4: h is its fp16 value times 2^exp
+    int16_t token;
+};
+struct Plan {
+    int32_t blocks_n;
+    int32_t pad[3];
+    Block blocks[kMaxV];
+    Row rows[kMaxA];
+};
 struct Table {
     uint64_t mask[kMaxE];  // tokens of each expert
     int32_t base[kMaxE];   // its first row
     Block blocks[kMaxV];
-    float wt[kMaxA];       // routing weight; NVFP4: times w2's tensor scale
-    uint8_t tok[kMaxA];
+    Row rows[kMaxA];
     int32_t scan[kWaves];
 };
-// NVFP4, per row: g and u are the sums times t1 times 2^shift; h is its fp16 value times 2^exp.
+// NVFP4, per row: g and u are the sums times t1 times 2^shift.
 struct RowScale {
     float t1;
-    int16_t shift, exp;
+    int32_t shift;
 };
-// From ids and weights (global, as another launch or `choose` of this workgroup left them). All threads take part;
-// returns the number of blocks.
+// From ids and weights (of another launch, or of this workgroup). All threads take part; returns the number of blocks.
 template <int FMT>
-__device__ __forceinline__ int build(Table& tb, RowScale* rows, const Args& p, const int32_t* ids, const float* weights) {
+__device__ __forceinline__ int build(Table& tb, RowScale* scale, const Args& p, const int32_t* ids, const float* weights) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int A = p.T * p.k;
     struct Scales {
@@ -461,448 +468,344 @@ __device__ __forceinline__ int build(Table& tb, RowScale* rows, const Args& p, c
     for (int a = t; a < A; a += kThreads) {
         const int e = ids[a], tk = a / p.k;
         const int row = tb.base[e] + __popcll(tb.mask[e] & ((1ull << tk) - 1));
-        tb.tok[row] = (uint8_t)tk;
-        tb.wt[row] = weights[a];
+        Row v = {weights[a], 0, (int16_t)tk};
         if (FMT == kNvfp4) {
             const Scales s = a == t ? early : scales(a);
-            tb.wt[row] *= s.t2;
             // |g|, |u| < 2^(norm + shift) times the largest weight, 2688 t1, so |h| is below the square of that: 2^exp
             // times at most 2^15
             const int b = s.x.norm + s.x.shift + __builtin_amdgcn_frexp_expf(s.t1 * 2688.0f);
-            rows[row] = {s.t1, (int16_t)s.x.shift, (int16_t)(2 * b - 15)};
+            v.wt *= s.t2;
+            v.exp = (int16_t)(2 * b - 15);
+            scale[row] = {s.t1, s.x.shift};
         }
+        tb.rows[row] = v;
     }
     __syncthreads();
     return (int)uniform((uint32_t)total) >> 16;
 }
 
-// ------------------------------------------------------------------ the layer
-// Work is cut into tasks, and these into as many shares as there are workgroups: share i of G is tasks i, i + G, ... A
-// workgroup takes the next share from a device-wide counter, and another one when it is done. It waits only for tasks that
-// running workgroups hold, so a call ends however few of its workgroups are resident at a time (another call's may hold the
-// rest of the chip, and wait as well); where all are, each has one share.
-//
-//   choice   more than 8 tokens: 8 tokens a task, one per wave (up to 8 tokens every workgroup chooses for itself,
-//            which costs it less than waiting)
-//   fc1      one block of tokens and 8 NB gate rows with their up rows; the waves share K
-//   fc2      16 columns of out; the waves share the (block, K step) pairs of all chosen experts in contiguous runs, and
-//            where a run leaves a block its wave adds weight * sum to its own token rows in LDS
-//
-// Which workgroup does a task does not show in its result, and every sum has a fixed order.
+// Tokens t0 .. t0 + 7, one per wave, by all threads.
 constexpr int kOwnChoice = kWaves;
-
-// By one thread. (The offset that the compiler cannot see through keeps it from first adding up over the wave, which
-// would wait for the result, and with it for every load in flight, on the spot.)
-__device__ __forceinline__ uint32_t take(uint32_t* counter) {
-    uint32_t zero = 0;
-    asm volatile("" : "+v"(zero));
-    counter += zero;
-    return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// All threads: everything this workgroup stored becomes visible to workgroups that see `counter` counted up by n.
-__device__ __forceinline__ void publish(uint32_t* counter, uint32_t n) {
+template <int P>
+__device__ __forceinline__ void choose_for(const Args& p, int t0, double (*val)[kMaxE], const float* bias, int32_t* ids,
+                                           float* weights) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), t = t0 + wave;
+    add_parts(p, t0, min(p.T - t0, kWaves), val);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-        __hip_atomic_fetch_add(counter, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (t >= p.T) return;
+    int id;
+    float w;
+    choose<P>(p, val[wave], bias, lane, &id, &w);
+    if (lane < p.k) {
+        ids[t * p.k + lane] = id;
+        weights[t * p.k + lane] = w;
     }
 }
-// All threads: waits until `counter` has reached n; what was published before it did is visible then.
-__device__ __forceinline__ void await(uint32_t* counter, uint32_t n) {
-    if (threadIdx.x == 0) {
-        while (__hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < n) __builtin_amdgcn_s_sleep(1);
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    }
-    __syncthreads();
+__device__ __forceinline__ void load_bias(const Args& p, float* bias) {
+    for (int e = threadIdx.x; e < p.E; e += kThreads) bias[e] = p.bias ? p.bias[e] : 0.0f;
+}
+template <int P>
+__global__ __launch_bounds__(kThreads) void k_decode_choice(Args p) {
+    __shared__ double val[kWaves][kMaxE];
+    __shared__ float bias[kMaxE];
+    load_bias(p, bias);
+    choose_for<P>(p, (int)blockIdx.x * kWaves, val, bias, p.ids, p.weights);
 }
 
-// fc1 -> fc2. h is written through to memory (agent-scope stores), so that a workgroup has nothing to flush before it
-// counts a task as finished: a release fence writes the XCD's whole L2 back, 1 to 4 us.
-//
-// FEW (at most kFewRows rows of h): fc2 waits block by block, so that the first experts' W2 is read while the last
-// workgroups are still busy with fc1 (they end some 5 us after the median one), and reads h past the L2, so that no wave
-// has to invalidate anything (2000 invalidations took 14 us). A task counts as finished a task later: the waves wait until
-// no more of their memory operations are outstanding than the loads they have issued since, which costs nothing, and
-// thread 0 counts after the barrier that follows. (One token on NVFP4 weights 46.7 us waiting for all of fc1, 43.8 so;
-// three tokens of a small layer 26.3 and 23.1; one bf16 token the same; two bf16 tokens, 16 rows, 104 and 126.)
-// Else one thread of a workgroup waits for all of fc1 and invalidates, and h is read through the L2, which serves it to 32
-// CUs (64 int8 tokens: 627 us; past the L2, block by block, 800).
-constexpr int kFewRows = 8;
-__device__ __forceinline__ void store_through(uint16_t* p, uint32_t v) {
-    __hip_atomic_store(reinterpret_cast<uint32_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void count_up(uint32_t* counter, uint32_t n) {
-    __hip_atomic_fetch_add(counter, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-// fc1's operands of a wave in flight: D1 steps.
+// ------------------------------------------------------------------ fc1 + SwiGLU
+// One persistent workgroup per CU. A task is one block of tokens and 8 NB gate rows with their up rows; the waves share K
+// and their sums meet in LDS, added in order. A wave's loads run ahead across the tasks' ends: D1 steps, 8 KiB of weights,
+// are in flight all the time, 64 KiB per CU, which the memory serves at 5.4 to 5.6 TB/s (twice as many were no faster).
 template <int FMT>
-struct Stage1 {
+struct Stage1 {  // operands of a wave in flight
     W16 w[Fmt<FMT>::D1][Fmt<FMT>::NB];
     X16<FMT> x[Fmt<FMT>::D1];
 };
 struct Task1 {  // all scalars
-    int block, e, n, row0, c0;
+    int e, n, row0, c0;
 };
 
-template <int FMT, int P, bool FEW>
-__global__ __launch_bounds__(kThreads, 2) void k_decode_layer(Args p) {
+// Next of the tail's tasks, by one thread. (The offset that the compiler cannot see through keeps it from first adding up
+// over the wave, which would wait for the result, and with it for every load in flight, on the spot.)
+__device__ __forceinline__ uint32_t take(uint32_t* counter) {
+    uint32_t zero = 0;
+    asm volatile("" : "+v"(zero));
+    return __hip_atomic_fetch_add(counter + zero, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <int FMT, int P>
+__global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
     constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
-    constexpr int D2 = FMT == kNvfp4 && !FEW ? 6 : 8;  // steps in flight in fc2
     union Scratch {
         struct {
-            float part[2][kWaves][NB][16][17];  // fc1: each wave's sums
-            uint32_t told[2];                   // and a task
+            float part[2][kWaves][NB][16][17];  // each wave's sums
+            uint32_t told[2];                   // a task
         };
-        float rows[kWaves][kMaxT][17];      // fc2: each wave's token rows
         struct {
             int32_t ids[kOwnChoice * kMaxK];
             float weights[kOwnChoice * kMaxK];
             double val[kWaves][kMaxE];
-        } c;                                // the choice
+        } c;                                    // the choice
     };
     __shared__ Table tb;
     __shared__ Scratch sc;
-    __shared__ uint32_t next;
     __shared__ float bias[kMaxE];
-    __shared__ RowScale rows[FMT == kNvfp4 ? kMaxA : 1];
+    __shared__ RowScale scale[FMT == kNvfp4 ? kMaxA : 1];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int G = gridDim.x;
-    // Thread 0's shares of fc1 and fc2, asked for well before they are used: with the last task of the share before.
-    uint32_t share1 = 0, share2 = 0;
-    if (threadIdx.x == 0) share1 = take(&p.count->fc1);
-    auto tell = [&](uint32_t share) {  // all threads: what thread 0 took (a barrier on either side)
-        if (threadIdx.x == 0) next = share;
-        __syncthreads();
-        const uint32_t v = uniform(next);
-        __syncthreads();
-        return (int)v;
-    };
-    for (int e = threadIdx.x; e < p.E; e += kThreads) bias[e] = p.bias ? p.bias[e] : 0.0f;
-
-    // ---- the choice
-    auto choose_for = [&](int t0, int32_t* ids, float* weights) {  // tokens t0 .. t0 + 7, one per wave
-        add_parts(p, t0, min(p.T - t0, kWaves), sc.c.val);
-        __syncthreads();
-        const int t = t0 + wave;
-        if (t >= p.T) return;
-        int id;
-        float w;
-        choose<P>(p, sc.c.val[wave], bias, lane, &id, &w);
-        if (lane < p.k) {
-            ids[t * p.k + lane] = id;
-            weights[t * p.k + lane] = w;
-        }
-    };
     int V;
     if (p.T <= kOwnChoice) {
-        choose_for(0, sc.c.ids, sc.c.weights);
+        load_bias(p, bias);
+        choose_for<P>(p, 0, sc.c.val, bias, sc.c.ids, sc.c.weights);
         __syncthreads();
-        if (blockIdx.x == 0)
-            for (int a = threadIdx.x; a < p.T * p.k; a += kThreads) {
-                p.ids[a] = sc.c.ids[a];
-                p.weights[a] = sc.c.weights[a];
-            }
-        V = build<FMT>(tb, rows, p, sc.c.ids, sc.c.weights);
+        V = build<FMT>(tb, scale, p, sc.c.ids, sc.c.weights);
     } else {
-        const uint32_t tasks = (uint32_t)(p.T + kWaves - 1) / kWaves;
-        for (;;) {
-            if (threadIdx.x == 0) next = take(&p.count->pick);
-            __syncthreads();
-            const uint32_t c = uniform(next);
-            if (c >= tasks) break;
-            choose_for((int)c * kWaves, p.ids, p.weights);
-            publish(&p.count->picked, 1);
-            // Nothing may come between thread 0's part of publish and its next take but this barrier: without it the
-            // compiler makes one block of the two, and a loop around the rest that lane 0 leaves for that block while
-            // the other lanes of its wave go round and wait for it there.
-            __syncthreads();
+        V = build<FMT>(tb, scale, p, p.ids, p.weights);
+    }
+    if ((int)blockIdx.x == G - 1) {  // (the one with the fewest tasks) for fc2 and the caller
+        const int A = p.T * p.k;
+        if (threadIdx.x == 0) p.plan->blocks_n = V;
+        for (int i = threadIdx.x; i < V; i += kThreads) p.plan->blocks[i] = tb.blocks[i];
+        for (int i = threadIdx.x; i < A; i += kThreads) {
+            p.plan->rows[i] = tb.rows[i];
+            if (p.T <= kOwnChoice) {
+                p.ids[i] = sc.c.ids[i];
+                p.weights[i] = sc.c.weights[i];
+            }
         }
-        await(&p.count->picked, tasks);
-        V = build<FMT>(tb, rows, p, p.ids, p.weights);
+        __syncthreads();
     }
 
-    // ---- fc1
     const int JB = (p.f + 8 * NB - 1) / (8 * NB), N1 = V * JB;
     const auto xr = rsrc(FMT == kNvfp4 ? p.xh : p.x, (uint32_t)p.T * (uint32_t)p.d * 2u);
-    const uint32_t rb1 = Fmt<FMT>::row_bytes(p.d);
-    const int steps1 = (int)(rb1 + 63) / 64, part1 = (steps1 + kWaves - 1) / kWaves;
-    const int chunks = (part1 + D1 - 1) / D1, s_first = wave * part1, s_end = min(s_first + part1, steps1);
+    const uint32_t rb = Fmt<FMT>::row_bytes(p.d);
+    const int steps = (int)(rb + 63) / 64, part = (steps + kWaves - 1) / kWaves;
+    const int chunks = (part + D1 - 1) / D1, s_first = wave * part, s_end = min(s_first + part, steps);
     auto set = [&](int task) {
-        const int i = task / JB;
-        const Block b = tb.blocks[i];
-        return Task1{i, (int)uniform(b.e), (int)uniform(b.n), (int)uniform(b.row0), task % JB * 8 * NB};
+        const Block b = tb.blocks[task / JB];
+        return Task1{(int)uniform(b.e), (int)uniform(b.n), (int)uniform(b.row0), task % JB * 8 * NB};
     };
     auto fetch = [&](Stage1<FMT>& st, int j, const Task1& t, uint32_t xrow, int s) {
         const Matrix<FMT> m(p.w1, p.s1, t.e, 2 * p.f, p.d);
         const uint32_t o = (uint32_t)s * 64 + q * 16;
-        const bool ok = s < s_end && o < rb1;
+        const bool ok = s < s_end && o < rb;
         const int col = t.c0 + (r & 7);
 #pragma unroll
-        for (int g = 0; g < NB; ++g)
-            st.w[j][g] = m.load((r < 8 ? 0 : p.f) + col + 8 * g, o, ok && col + 8 * g < p.f);
+        for (int g = 0; g < NB; ++g) st.w[j][g] = m.load((r < 8 ? 0 : p.f) + col + 8 * g, o, ok && col + 8 * g < p.f);
         st.x[j] = load_x<FMT>(xr, xrow, p.d, o, ok && r < t.n);
     };
-    auto token = [&](const Task1& t) { return (uint32_t)tb.tok[t.row0 + min(r, t.n - 1)]; };
+    auto token = [&](const Task1& t) { return (uint32_t)tb.rows[t.row0 + min(r, t.n - 1)].token; };
     // The epilogue's thread: two columns of a token, neighbours as the operand of fc2 holds them.
     const int em = threadIdx.x / (4 * NB), eg = threadIdx.x / 4 % NB, ep = threadIdx.x & 3;
     const int ej = FMT == kNvfp4 ? (ep & 1) * 4 + (ep >> 1) : 2 * ep, ej2 = ej + (FMT == kNvfp4 ? 2 : 1);
-    uint32_t finished = 0;  // tasks
-    int pending = -1;       // FEW: block of the finished task that is not counted yet
-    int flip = 0;
-    bool asked = false;  // for a share of fc2
-    // Where fc1 is long, shares are of the tasks before `tail`, whole rounds, and the rest is taken task by task, two ahead
-    // of its use (64 tokens on NVFP4 weights: the last workgroup ends 6 us after the median one instead of 34).
+    // A workgroup's tasks are blockIdx.x, + G, ...; where there are many, only those before `tail`, whole rounds, and the
+    // rest is taken from a counter, two tasks ahead of its use (64 tokens on NVFP4 weights: the last workgroup then ends
+    // 6 us after the median one instead of 34). Which workgroup does a task does not show in its result.
     const int tail = N1 >= 24 * G ? (N1 / G - 4) * G : N1;
-    for (int i = tell(share1); i < G; i = tell(share1)) {
-        Stage1<FMT> st;
-        int cur = i < tail ? i : N1, nxt = cur + G;
-        if (cur >= N1) {
-            if (threadIdx.x == 0) share1 = take(&p.count->fc1);
-            continue;
+    int cur = blockIdx.x, nxt = cur + G, flip = 0;
+    if (cur >= N1) return;
+    Stage1<FMT> st;
+    Task1 t = set(cur);
+    uint32_t xrow = token(t);
+#pragma unroll
+    for (int j = 0; j < D1; ++j) fetch(st, j, t, xrow, s_first + j);
+    while (cur < N1) {
+        const bool more = nxt < N1;
+        // the task after the next one (a taken one is told at this task's barrier)
+        const bool ask = tail < N1 && nxt + G >= tail;
+        uint32_t got = 0;
+        if (ask && threadIdx.x == 0) got = take(p.tail);
+        const Task1 tn = set(more ? nxt : cur);
+        const uint32_t xnext = token(tn);
+        float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // int8: the epilogue's channel scales, ahead of the loads that follow
+        if (FMT == kInt8 && wave < NB) {
+            const float* s = static_cast<const float*>(p.s1) + (int64_t)t.e * 2 * p.f;
+            const int c = min(t.c0 + 8 * eg + ej, p.f - 2);
+            cs[0] = s[c];
+            cs[1] = s[c + 1];
+            cs[2] = s[p.f + c];
+            cs[3] = s[p.f + c + 1];
         }
-        Task1 t = set(cur);
-        uint32_t xrow = token(t);
+        f32x4 acc[NB];
 #pragma unroll
-        for (int j = 0; j < D1; ++j) fetch(st, j, t, xrow, s_first + j);
-        for (; cur < N1;) {
-            const bool more = nxt < N1;
-            // the task after the next one: of the share, or of the tail (thread 0 asks; told at this task's barrier)
-            const bool ask = tail < N1 && nxt + G >= tail;
-            uint32_t got = 0;
-            if (threadIdx.x == 0) {
-                if (ask) got = take(&p.count->tail);
-                if (!more) share1 = take(&p.count->fc1);
-                if (!more && !asked) share2 = take(&p.count->fc2);
+        for (int g = 0; g < NB; ++g) acc[g] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int c = 0; c < chunks; ++c) {
+            const bool last = c + 1 == chunks;
+            const Task1 tl = last ? tn : t;
+            const uint32_t xl = last ? xnext : xrow;
+            const int sl = !last ? s_first + (c + 1) * D1 : more ? s_first : s_end;
+#pragma unroll
+            for (int j = 0; j < D1; ++j) {
+#pragma unroll
+                for (int i = 0; i < NF; ++i)
+#pragma unroll
+                    for (int g = 0; g < NB; ++g) acc[g] = mfma<FMT>(decode<FMT>(st.w[j][g], i), st.x[j].v[i], acc[g]);
+                fetch(st, j, tl, xl, sl + j);
             }
-            asked |= !more;
-            const Task1 tn = set(more ? nxt : cur);
-            const uint32_t xnext = token(tn);
-            float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // int8: the epilogue's channel scales, ahead of the loads that follow
-            if (FMT == kInt8 && wave < NB) {
-                const float* s = static_cast<const float*>(p.s1) + (int64_t)t.e * 2 * p.f;
-                const int c = min(t.c0 + 8 * eg + ej, p.f - 2);
-                cs[0] = s[c];
-                cs[1] = s[c + 1];
-                cs[2] = s[p.f + c];
-                cs[3] = s[p.f + c + 1];
-            }
-            f32x4 acc[NB];
+        }
+        // lane: rows 4 q + i of the group (gate 0 .. 7, up 8 .. 15), token r
+        if (r < t.n) {
 #pragma unroll
-            for (int g = 0; g < NB; ++g) acc[g] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-            for (int c = 0; c < chunks; ++c) {
-                const bool last = c + 1 == chunks;
-                const Task1 tl = last ? tn : t;
-                const uint32_t xl = last ? xnext : xrow;
-                const int sl = !last ? s_first + (c + 1) * D1 : more ? s_first : s_end;
+            for (int g = 0; g < NB; ++g)
 #pragma unroll
-                for (int j = 0; j < D1; ++j) {
+                for (int i = 0; i < 4; ++i) sc.part[flip][wave][g][r][4 * q + i] = acc[g][i];
+        }
+        if (ask && threadIdx.x == 0) sc.told[flip] = got;
+        lds_barrier();
+        const int after = ask ? tail + (int)uniform(sc.told[flip]) : nxt + G;
+        if (wave < NB) {
+            const int col = t.c0 + 8 * eg + ej;
+            if (em < t.n && t.c0 + 8 * eg < p.f) {
+                float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < NF; ++i)
+                for (int w = 0; w < kWaves; ++w) {
+                    const float* s = sc.part[flip][w][eg][em];
+                    g[0] += s[ej];
+                    g[1] += s[ej2];
+                    u[0] += s[8 + ej];
+                    u[1] += s[8 + ej2];
+                }
+                float h[2];
+                RowScale rs{};
+                if (FMT == kNvfp4) rs = scale[t.row0 + em];
 #pragma unroll
-                        for (int g = 0; g < NB; ++g) acc[g] = mfma<FMT>(decode<FMT>(st.w[j][g], i), st.x[j].v[i], acc[g]);
-                    fetch(st, j, tl, xl, sl + j);
+                for (int j = 0; j < 2; ++j) {
+                    if (FMT == kInt8) {
+                        g[j] *= cs[j];
+                        u[j] *= cs[2 + j];
+                    } else if (FMT == kNvfp4) {
+                        g[j] = __builtin_amdgcn_ldexpf(g[j] * rs.t1, rs.shift);
+                        u[j] = __builtin_amdgcn_ldexpf(u[j] * rs.t1, rs.shift);
+                    }
+                    h[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[j])) * u[j];
+                }
+                uint16_t* o = p.h + ((int64_t)(t.row0 + em) * p.f + (col & ~7)) * HP + 2 * ep;
+                if (FMT == kNvfp4) {
+                    const int exp = tb.rows[t.row0 + em].exp;
+                    const half2v v = {(_Float16)__builtin_amdgcn_ldexpf(h[0], -exp),
+                                      (_Float16)__builtin_amdgcn_ldexpf(h[1], -exp)};
+                    *reinterpret_cast<uint32_t*>(o) = __builtin_bit_cast(uint32_t, v);
+                } else {
+                    const uint32_t hi = bf16x2_rne(h[0], h[1]);
+                    // (of an infinite h the first part is all)
+                    const float l0 = (hi & 0x7F80u) == 0x7F80u ? 0.0f : h[0] - __uint_as_float(hi << 16);
+                    const float l1 = (hi & 0x7F800000u) == 0x7F800000u ? 0.0f : h[1] - __uint_as_float(hi & 0xFFFF0000u);
+                    *reinterpret_cast<uint32_t*>(o) = hi;
+                    *reinterpret_cast<uint32_t*>(o + 8) = bf16x2_rne(l0, l1);
                 }
             }
-            // lane: rows 4 q + i of the group (gate 0 .. 7, up 8 .. 15), token r
-            if (r < t.n) {
-#pragma unroll
-                for (int g = 0; g < NB; ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sc.part[flip][wave][g][r][4 * q + i] = acc[g][i];
-            }
-            if (ask && threadIdx.x == 0) sc.told[flip] = got;
-            if (FEW) wait_vm<D1 * (NB * (FMT == kNvfp4 ? 2 : 1) + NF)>();  // the loads of the next task's first steps
-            lds_barrier();
-            if (FEW && threadIdx.x == 0 && pending >= 0) count_up(&p.count->block[pending], 1);
-            const int after = ask ? tail + (int)uniform(sc.told[flip]) : nxt + G;
-            if (wave < NB) {
-                const int col = t.c0 + 8 * eg + ej;
-                if (em < t.n && t.c0 + 8 * eg < p.f) {
-                    float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int w = 0; w < kWaves; ++w) {
-                        const float* s = sc.part[flip][w][eg][em];
-                        g[0] += s[ej];
-                        g[1] += s[ej2];
-                        u[0] += s[8 + ej];
-                        u[1] += s[8 + ej2];
-                    }
-                    float h[2];
-                    RowScale rs{};
-                    if (FMT == kNvfp4) rs = rows[t.row0 + em];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (FMT == kInt8) {
-                            g[j] *= cs[j];
-                            u[j] *= cs[2 + j];
-                        } else if (FMT == kNvfp4) {
-                            g[j] = __builtin_amdgcn_ldexpf(g[j] * rs.t1, rs.shift);
-                            u[j] = __builtin_amdgcn_ldexpf(u[j] * rs.t1, rs.shift);
-                        }
-                        h[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[j])) * u[j];
-                    }
-                    uint16_t* o = p.h + ((int64_t)(t.row0 + em) * p.f + (col & ~7)) * HP + 2 * ep;
-                    if (FMT == kNvfp4) {
-                        const half2v v = {(_Float16)__builtin_amdgcn_ldexpf(h[0], -rs.exp),
-                                          (_Float16)__builtin_amdgcn_ldexpf(h[1], -rs.exp)};
-                        store_through(o, __builtin_bit_cast(uint32_t, v));
-                    } else {
-                        const uint32_t hi = bf16x2_rne(h[0], h[1]);
-                        // (of an infinite h the first part is all)
-                        const float l0 = (hi & 0x7F80u) == 0x7F80u ? 0.0f : h[0] - __uint_as_float(hi << 16);
-                        const float l1 = (hi & 0x7F800000u) == 0x7F800000u ? 0.0f : h[1] - __uint_as_float(hi & 0xFFFF0000u);
-                        store_through(o, hi);
-                        store_through(o + 8, bf16x2_rne(l0, l1));
-                    }
-                }
-            }
-            ++finished;
-            pending = t.block;
-            cur = nxt;
-            nxt = after;
-            t = tn;
-            xrow = xnext;
-            flip ^= 1;  // (the next task's sums go to the other half while slow threads still read this one)
         }
+        cur = nxt;
+        nxt = after;
+        t = tn;
+        xrow = xnext;
+        flip ^= 1;  // (the next task's sums go to the other half while slow threads still read this one)
     }
-    wait_vm<0>();  // this wave's h is in memory
-    __syncthreads();
-    if (threadIdx.x == 0 && finished) {
-        if (FEW) count_up(&p.count->block[pending], 1);
-        else count_up(&p.count->done, finished);
-    }
+}
 
-    // ---- fc2 + combine
-    const auto hr = rsrc(p.h, (uint32_t)(p.T * p.k) * (uint32_t)p.f * (2u * HP));
-    const uint32_t rb2 = Fmt<FMT>::row_bytes(p.f);
-    const int S = (int)(rb2 + 63) / 64, total = V * S, part2 = (total + kWaves - 1) / kWaves;
-    const int first = min(wave * part2, total), end = min(first + part2, total);
-    const int N2 = (p.d + 15) / 16;
-    bool waited = false;
-    int upto = FEW ? first / S : V;  // blocks of this wave's run before this one have their h
-    auto ready = [&](int b) {
-        while (b >= upto) {
-            const int at = min(b + lane, 63);
-            const bool there = __hip_atomic_load(&p.count->block[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)JB;
-            const uint64_t waits = ~__ballot(there);
-            const int n = waits ? __builtin_ctzll(waits) : 64;
-            upto = b + n;
-            if (n == 0) __builtin_amdgcn_s_sleep(16);
-        }
-        asm volatile("" ::: "memory");
+// ------------------------------------------------------------------ fc2 + combine
+// A workgroup owns 16 columns of out. Its waves share the (block, K step) pairs of all chosen experts in equal contiguous
+// runs, D2 steps in flight; where a run leaves a block, the wave adds weight * sum to its own token rows in LDS. The waves'
+// rows are added in order at the end. Nothing but the operands is loaded inside the loop, so that no wait empties the
+// pipeline (int8 with the channel scales loaded there: four tokens 118 us instead of 102, 64 713 instead of 602). D2 of 6,
+// 10 or (bf16) 12, 16 is within 2 % of 8, the deeper ones on the slow side.
+template <int FMT>
+__global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
+    constexpr int D2 = 8, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
+    __shared__ Block blocks[kMaxV];
+    __shared__ Row rows[kMaxA];
+    __shared__ float sums[kWaves][kMaxT][17];
+    __shared__ f32x4 channel[FMT == kInt8 ? kMaxV : 1][4];  // s2 of the 16 columns, per block
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int A = p.T * p.k, V = (int)uniform((uint32_t)p.plan->blocks_n);
+    for (int i = threadIdx.x; i < p.max_blocks; i += kThreads) blocks[i] = p.plan->blocks[i];
+    for (int i = threadIdx.x; i < A; i += kThreads) rows[i] = p.plan->rows[i];
+    const auto hr = rsrc(p.h, (uint32_t)A * (uint32_t)p.f * (2u * HP));
+    const uint32_t rb = Fmt<FMT>::row_bytes(p.f);
+    const int S = (int)(rb + 63) / 64, total = V * S, part = (total + kWaves - 1) / kWaves;
+    const int first = min(wave * part, total), end = min(first + part, total);
+    const int n0 = blockIdx.x * 16;
+    const bool w_ok = n0 + r < p.d;
+    for (int z = threadIdx.x; z < kWaves * kMaxT * 17; z += kThreads) (&sums[0][0][0])[z] = 0.0f;
+    __syncthreads();
+    W16 w[D2];
+    u32x4 x[D2][NF][HP];
+    int cv = first / S, cs = first - cv * S;  // the next step's block and step in it, of the products
+    int lv = cv, ls = cs;                     // and of the loads
+    Matrix<FMT> m(p.w2, p.s2, 0, p.d, p.f);
+    uint32_t at = 0;                          // of this lane's row of h in block lv
+    bool x_ok = false;
+    auto enter = [&](int v) {
+        const Block b = blocks[min(v, V - 1)];
+        m = Matrix<FMT>(p.w2, p.s2, (int)uniform((uint32_t)(int)b.e), p.d, p.f);
+        at = ((uint32_t)(int)uniform((uint32_t)(int)b.row0) + r) * (uint32_t)p.f * (2u * HP);
+        x_ok = r < (int)uniform((uint32_t)b.n);
     };
-    if (threadIdx.x == 0 && !asked) share2 = take(&p.count->fc2);
-    for (int i = tell(share2); i < G; i = tell(share2)) {
-      if (i >= N2) {
-        if (threadIdx.x == 0) share2 = take(&p.count->fc2);
-        continue;
-      }
-      for (int task = i; task < N2; task += G) {
-        const int n0 = task * 16;
-        const bool w_ok = n0 + r < p.d;
-        for (int z = threadIdx.x; z < kWaves * kMaxT * 17; z += kThreads) (&sc.rows[0][0][0])[z] = 0.0f;
-        W16 w[D2];
-        u32x4 x[D2][NF][HP];
-        int wv = first / S, ws = first - wv * S, xv = wv, xs = ws, cv = wv, cs = ws;  // next weights, h, products
-        auto fetch_w = [&](int j, bool live) {
-            const int e = __builtin_amdgcn_readfirstlane((int)tb.blocks[live ? wv : 0].e);
-            const Matrix<FMT> m(p.w2, p.s2, e, p.d, p.f);
-            const uint32_t o = (uint32_t)ws * 64 + q * 16;
-            w[j] = m.load((uint32_t)(n0 + r), o, live && o < rb2 && w_ok);
-            if (++ws == S) {
-                ws = 0;
-                ++wv;
-            }
-        };
-        auto fetch_x = [&](int j, bool live) {
-            if (FEW && live) ready(xv);
-            const Block b = tb.blocks[live ? xv : 0];
-            const int n = __builtin_amdgcn_readfirstlane(b.n), row0 = __builtin_amdgcn_readfirstlane((int)b.row0);
-            const uint32_t o = (uint32_t)xs * 64 + q * 16;
-            const uint32_t at = (uint32_t)(row0 + r) * (uint32_t)p.f * (2u * HP) + o / 16 * (NF * HP * 16);
+    auto fetch = [&](int j, bool live) {
+        const uint32_t o = (uint32_t)ls * 64 + q * 16;
+        const bool ok = live & (o < rb);
+        w[j] = m.load((uint32_t)(n0 + r), o, ok & w_ok);
+        const uint32_t from = ok & x_ok ? at + o / 16 * (NF * HP * 16) : kNowhere;
 #pragma unroll
-            for (int i = 0; i < NF; ++i)
+        for (int i = 0; i < NF; ++i)
 #pragma unroll
-                for (int half = 0; half < HP; ++half)
-                    x[j][i][half] = __builtin_amdgcn_raw_buffer_load_b128(
-                        hr, live && o < rb2 && r < n ? at + 16 * (HP * i + half) : kNowhere, 0, FEW ? kAgentScope : 0);
-            if (++xs == S) {
-                xs = 0;
-                ++xv;
-            }
-        };
+            for (int half = 0; half < HP; ++half)
+                x[j][i][half] = __builtin_amdgcn_raw_buffer_load_b128(hr, from + 16 * (HP * i + half), 0, 0);
+        if (++ls == S) {
+            ls = 0;
+            enter(++lv);
+        }
+    };
+    enter(lv);
 #pragma unroll
-        for (int j = 0; j < D2; ++j) fetch_w(j, first + j < end);
-        if (FEW || waited) __syncthreads();  // (sc.rows is clear)
-        else await(&p.count->done, (uint32_t)N1);
-        waited = true;
+    for (int j = 0; j < D2; ++j) fetch(j, first + j < end);
+    if (FMT == kInt8) {  // through LDS: a wait for a load of its own would wait for all that run ahead
+        for (int i = threadIdx.x; i < 4 * V; i += kThreads)
+            channel[i >> 2][i & 3] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.s2) +
+                                                                     (int64_t)blocks[i >> 2].e * p.d + min(n0 + 4 * (i & 3), p.d - 4));
+        lds_barrier();
+    }
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i0 = first; i0 < end; i0 += D2) {
 #pragma unroll
-        for (int j = 0; j < D2; ++j) fetch_x(j, first + j < end);
-        // (asked for only now, when every workgroup has had time to take its first share)
-        if (threadIdx.x == 0 && task + G >= N2) share2 = take(&p.count->fc2);
-        auto channel_scales = [&](int b) {  // int8: of this lane's columns in a block's expert, a block ahead of their use
-            f32x4 s = {1.0f, 1.0f, 1.0f, 1.0f};
-            if (FMT == kInt8 && first < end) {
-                const int e = (int)uniform((uint32_t)(int)tb.blocks[min(b, V - 1)].e);
-                s = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.s2) + (int64_t)e * p.d +
-                                                    min(n0 + 4 * q, p.d - 4));
-            }
-            return s;
-        };
-        f32x4 cscale = channel_scales(cv);
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int i0 = first; i0 < end; i0 += D2) {
+        for (int j = 0; j < D2; ++j) {
+            if (i0 + j < end) {
 #pragma unroll
-            for (int j = 0; j < D2; ++j) {
-                if (i0 + j < end) {
+                for (int i = 0; i < NF; ++i) {
+                    const u32x4 v = decode<FMT>(w[j], i);
 #pragma unroll
-                    for (int i = 0; i < NF; ++i) {
-                        const u32x4 v = decode<FMT>(w[j], i);
-#pragma unroll
-                        for (int half = 0; half < HP; ++half) acc = mfma<FMT>(v, x[j][i][half], acc);
-                    }
-                }
-                const bool live = i0 + D2 + j < end;
-                fetch_w(j, live);
-                fetch_x(j, live);
-                if (i0 + j < end && (++cs == S || i0 + j + 1 == end)) {
-                    const Block b = tb.blocks[cv];
-                    if (r < b.n) {
-                        const float wt = tb.wt[b.row0 + r];
-                        float* o = sc.rows[wave][tb.tok[b.row0 + r]] + 4 * q;
-                        if (FMT == kInt8) acc *= cscale;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float v = FMT == kNvfp4 ? __builtin_amdgcn_ldexpf(acc[i], rows[b.row0 + r].exp) : acc[i];
-                            o[i] = __builtin_fmaf(wt, v, o[i]);
-                        }
-                    }
-                    cscale = channel_scales(cv + 1);
-                    acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-                    cs = 0;
-                    ++cv;
+                    for (int half = 0; half < HP; ++half) acc = mfma<FMT>(v, x[j][i][half], acc);
                 }
             }
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < p.T * 16; i += kThreads) {
-            const int t = i >> 4, c = i & 15;
-            if (n0 + c >= p.d) continue;
-            float v = sc.rows[0][t][c];
+            fetch(j, i0 + D2 + j < end);
+            if (i0 + j < end && (++cs == S || i0 + j + 1 == end)) {
+                const Block b = blocks[cv];
+                if (r < b.n) {
+                    const Row row = rows[b.row0 + r];
+                    float* o = sums[wave][row.token] + 4 * q;
+                    if (FMT == kInt8) acc *= channel[cv][q];
 #pragma unroll
-            for (int w2 = 1; w2 < kWaves; ++w2) v += sc.rows[w2][t][c];
-            const int64_t at = (int64_t)t * p.d + n0 + c;
-            if (p.residual) v += bf16_to_f32(p.residual[at]);
-            p.out[at] = (uint16_t)bf16x2_rne(v, v);
+                    for (int i = 0; i < 4; ++i)
+                        o[i] = __builtin_fmaf(row.wt, FMT == kNvfp4 ? __builtin_amdgcn_ldexpf(acc[i], row.exp) : acc[i], o[i]);
+                }
+                acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+                cs = 0;
+                ++cv;
+            }
         }
-        __syncthreads();
-      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.T * 16; i += kThreads) {
+        const int t = i >> 4, c = i & 15;
+        if (n0 + c >= p.d) continue;
+        float v = sums[0][t][c];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) v += sums[k][t][c];
+        const int64_t at = (int64_t)t * p.d + n0 + c;
+        if (p.residual) v += bf16_to_f32(p.residual[at]);
+        p.out[at] = (uint16_t)bf16x2_rne(v, v);
     }
 }
 
@@ -924,7 +827,8 @@ int router_parts(int64_t T, int64_t d, int64_t E) {
 size_t carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t f, Args* p) {
     p->parts = router_parts(T, d, E);
     p->max_blocks = (int)std::min<int64_t>(T * k, E + T * k / 16);
-    p->count = c.take<Counters>(1);
+    p->tail = c.take<uint32_t>(1);
+    p->plan = c.take<Plan>(1);
     p->logits = c.take<double>((size_t)(p->parts * T * E));
     p->h = c.take<uint16_t>((size_t)(2 * T * k * f));
     p->xh = c.take<uint16_t>((size_t)(T * d));
@@ -932,26 +836,23 @@ size_t carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t f, Args*
     return c.need;
 }
 
-template <int FMT, int P, bool FEW>
-void launch_layer(const Args& p, hipStream_t s) {
-    constexpr int NB = Fmt<FMT>::NB;
-    // as many workgroups as have a task, at most one per CU (their registers and LDS let no more be resident)
-    const int64_t tasks = std::max<int64_t>((int64_t)p.max_blocks * ((p.f + 8 * NB - 1) / (8 * NB)), (p.d + 15) / 16);
-    const unsigned grid = (unsigned)std::min<int64_t>(tasks, device_cus());
-    hipLaunchKernelGGL((k_decode_layer<FMT, P, FEW>), dim3(grid), dim3(kThreads), 0, s, p);
-}
 template <int FMT, int P>
-void launch_rows(const Args& p, hipStream_t s) {
-    if (p.T <= kOwnChoice && p.T * p.k <= kFewRows) launch_layer<FMT, P, true>(p, s);
-    else launch_layer<FMT, P, false>(p, s);
+void launch_fc1(const Args& p, hipStream_t s) {
+    constexpr int NB = Fmt<FMT>::NB;
+    if (p.T > kOwnChoice)
+        hipLaunchKernelGGL(k_decode_choice<P>, dim3((unsigned)(p.T + kWaves - 1) / kWaves), dim3(kThreads), 0, s, p);
+    const int64_t tasks = (int64_t)p.max_blocks * ((p.f + 8 * NB - 1) / (8 * NB));
+    const unsigned grid = (unsigned)std::min<int64_t>(tasks, device_cus());
+    hipLaunchKernelGGL((k_decode_fc1<FMT, P>), dim3(grid), dim3(kThreads), 0, s, p);
 }
 template <int FMT>
 int run(const Args& p, hipStream_t s) {
     const unsigned grid = (unsigned)((p.E + 15) / 16 * ((p.T + 15) / 16) * p.parts + (FMT == kNvfp4 ? p.T : 0));
     hipLaunchKernelGGL(k_decode_router<FMT == kNvfp4>, dim3(grid), dim3(kRouterThreads), 0, s, p);
-    if (p.E <= 128) launch_rows<FMT, 2>(p, s);
-    else if (p.E <= 384) launch_rows<FMT, 6>(p, s);
-    else launch_rows<FMT, 16>(p, s);
+    if (p.E <= 128) launch_fc1<FMT, 2>(p, s);
+    else if (p.E <= 384) launch_fc1<FMT, 6>(p, s);
+    else launch_fc1<FMT, 16>(p, s);
+    hipLaunchKernelGGL(k_decode_fc2<FMT>, dim3((unsigned)(p.d + 15) / 16), dim3(kThreads), 0, s, p);
     return launch_status();
 }
 
