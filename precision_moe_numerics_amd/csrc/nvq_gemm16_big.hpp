@@ -327,6 +327,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
     __shared__ int32_t rows_lds[kBigWaves][64];
     __shared__ __attribute__((aligned(16))) int32_t ring[kBigWaves][4][4];
     __shared__ __attribute__((aligned(16))) uint8_t row_buf[MODE == kWgrad ? kBigWaves : 1][kRowBuf];
+    __shared__ __attribute__((aligned(16))) std::conditional_t<I8, Side<128>, int> side[I8 ? kBigWaves : 1];
     using Load = BigLoad<MODE, EPI>;
     constexpr int kNew = 2 * (kSlots - 3);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -520,7 +521,7 @@ __global__ __launch_bounds__(64 * kBigWaves, 2) void k_gemm16_big(Args p) {
                 if (p.out_f32) epilogue_wgrad<true>(p, acc, o, row_buf[wave], full, lane);
                 else epilogue_wgrad<false>(p, acc, o, row_buf[wave], full, lane);
             } else {
-                epilogue<EPI>(p, acc, o, lane);
+                epilogue<EPI>(p, acc, o, side[I8 ? wave : 0], lane);
             }
         }
     };
