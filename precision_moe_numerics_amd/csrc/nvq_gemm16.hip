@@ -62,19 +62,27 @@ __global__ __launch_bounds__(kTabThreads) void k_tile_table(const int32_t* __res
     }
 }
 
-template <int MODE, int EPI, bool AHEAD, bool I8>
+template <int MODE, int EPI, bool AHEAD, bool I8, int TM = 128>
 void run(Args p, int64_t m_tiles_cap, hipStream_t s) {
     constexpr int TNO = EPI == kEpiGlu ? 64 : 128;
     p.n_tiles = (p.N + TNO - 1) / TNO;
     p.total = (int)(m_tiles_cap * p.n_tiles);
     const unsigned grid = ((unsigned)p.total + 7u) & ~7u;  // xcd_id: whole rounds of the 8 XCDs
-    hipLaunchKernelGGL((k_gemm16<MODE, EPI, 128, 128, 2, 2, AHEAD, I8>), dim3(grid), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_gemm16<MODE, EPI, TM, 128, 2, 2, AHEAD, I8>), dim3(grid), dim3(256), 0, s, p);
 }
 // Reading a stage ahead pays where a CU has one workgroup, whose reads nothing else covers (512 x 1024 x 4096 47 us
 // without, 37 with; 2048^3 27.6, 25.3); with two it costs (16384 x 384 x 4096 65, 69; the weight gradient of 4091 x 2048
 // x 4096 74, 78), but for the transposed reads of dgrad (8192 rows, 8 experts of 2048 x 4096 163, 153).
+//
+// int8, 64 rows: with no more than a tile per CU half the rows per workgroup are faster, the K steps being bound by what one
+// workgroup does in a row, reading LDS and multiplying (128 or 512 rows x 4096 x 4096 21.8 us with 128, 16.5 with 64; 1000
+// x 504 x 1008 9.4 and 7.0); past that they do not matter (1003 x 2056 x 4112 25.5 and 25.8). Four stages of LDS instead
+// of two measured slower (512 x 1024 x 4096 28.9).
 template <int MODE, int EPI, bool I8 = false>
-void run_ahead(const Args& p, int64_t m_tiles_cap, bool one, hipStream_t s) {
+void run_ahead(const Args& p, int64_t m_tiles_cap, bool one, int tm, hipStream_t s) {
+    if constexpr (I8) {
+        if (tm == 64) return run<MODE, EPI, true, I8, 64>(p, m_tiles_cap, s);
+    }
     if (one) run<MODE, EPI, true, I8>(p, m_tiles_cap, s);
     else run<MODE, EPI, false, I8>(p, m_tiles_cap, s);
 }
@@ -134,16 +142,18 @@ void run_skinny_rows(const Args& p, int64_t active, hipStream_t s) {
 
 using namespace g16;
 
-constexpr int kMinTileM = 128;
+constexpr int kMinTileM = 128, kMinTileM8 = 64;
 
 static int64_t tile_cap(int64_t rows, int64_t E, int tm) { return (rows + tm - 1) / tm + E; }
 
-size_t gemm16_ws_bytes(int64_t rows, int64_t E) {
+static size_t ws_bytes(int64_t rows, int64_t E, int tm) {
     Carver c(nullptr);
     c.take<int32_t>(1);
-    c.take<Tile>((size_t)tile_cap(std::max<int64_t>(rows, 0), std::max<int64_t>(E, 1), kMinTileM));
+    c.take<Tile>((size_t)tile_cap(std::max<int64_t>(rows, 0), std::max<int64_t>(E, 1), tm));
     return c.need;
 }
+size_t gemm16_ws_bytes(int64_t rows, int64_t E) { return ws_bytes(rows, E, kMinTileM); }
+size_t gemm8_ws_bytes(int64_t rows, int64_t E) { return ws_bytes(rows, E, kMinTileM8); }
 
 bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int64_t N, int64_t K) {
     const int64_t i31 = (int64_t)1 << 31;
@@ -191,7 +201,7 @@ static void launch(int mode, int epi, Args p, void* ws, hipStream_t s) {
             run_big<kWgrad, kEpiOut>(p, mb, s);
         } else {
             p.m_tiles = (p.M + 127) / 128;
-            run_ahead<kWgrad, kEpiOut>(p, ms, ms * n_small <= cus, s);
+            run_ahead<kWgrad, kEpiOut>(p, ms, ms * n_small <= cus, 128, s);
         }
         return;
     }
@@ -219,7 +229,7 @@ static void launch(int mode, int epi, Args p, void* ws, hipStream_t s) {
         return std::max((double)active, (double)p.rows / tm + 0.5 * active);
     };
     const bool big = big_tiles(m_tiles(256) * n_big, m_tiles(128) * n_small, cus);
-    const int tm = big ? 256 : 128;
+    const int tm = big ? 256 : I8 && m_tiles(64) * n_small <= cus ? 64 : 128;
     int64_t mt;
     if (p.seg) {
         Carver cv(ws);
@@ -242,9 +252,9 @@ static void launch(int mode, int epi, Args p, void* ws, hipStream_t s) {
     }
     const bool one = m_tiles(128) * n_small <= cus;  // tile per CU
     if (!I8 && mode == kDgrad) run<kDgrad, kEpiOut, true, false>(p, mt, s);
-    else if (epi == kEpiGlu) run_ahead<kFwd, kEpiGlu, I8>(p, mt, one, s);
-    else if (epi == kEpiAct) run_ahead<kFwd, kEpiAct, I8>(p, mt, one, s);
-    else run_ahead<kFwd, kEpiOut, I8>(p, mt, one, s);
+    else if (epi == kEpiGlu) run_ahead<kFwd, kEpiGlu, I8>(p, mt, one, tm, s);
+    else if (epi == kEpiAct) run_ahead<kFwd, kEpiAct, I8>(p, mt, one, tm, s);
+    else run_ahead<kFwd, kEpiOut, I8>(p, mt, one, tm, s);
 }
 
 void launch_gemm16(int mode, int epi, Args p, void* ws, hipStream_t s) { launch<false>(mode, epi, p, ws, s); }

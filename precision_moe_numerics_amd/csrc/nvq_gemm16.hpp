@@ -432,15 +432,15 @@ struct Side {
 };
 template <int EPI, int MF, int NF, int ROWS>
 __device__ __forceinline__ void load_side(const Args& p, const Pos& o, Side<ROWS>& sd, int lane) {
-    static_assert(NF == 4 && MF % 4 == 0 && 16 * MF <= ROWS, "a column per lane, whole waves of rows");
+    static_assert(NF == 4 && 16 * MF <= ROWS, "a column per lane");
     const int N = p.N, j = lane >> 4;
     int n = (EPI == kEpiGlu ? o.col(j >> 2) + 16 * (j >> 1 & 1) : o.col(j >> 1) + 16 * (j & 1)) + (lane & 15);
     n = min(n, N - 1) + (EPI == kEpiGlu && (j & 1) ? N : 0);
     const float scale = p.b_scale[(int64_t)o.e * (EPI == kEpiGlu ? 2 : 1) * N + n], bias = p.bias ? p.bias[n] : 0.0f;
-    float row[MF / 4];
-    int32_t dst[MF / 4];
+    float row[ROWS / 64];
+    int32_t dst[ROWS / 64];
 #pragma unroll
-    for (int u = 0; u < MF / 4; ++u) {
+    for (int u = 0; u < ROWS / 64; ++u) {
         const int m = min(o.row(4 * u + j) + (lane & 15), o.row_end - 1);
         row[u] = row_scale(p, m);
         dst[u] = EPI == kEpiOut && p.scatter ? p.scatter[m] : m;
@@ -448,7 +448,7 @@ __device__ __forceinline__ void load_side(const Args& p, const Pos& o, Side<ROWS
     sd.scale[lane] = scale;
     sd.bias[lane] = bias;
 #pragma unroll
-    for (int u = 0; u < MF / 4; ++u) {
+    for (int u = 0; u < ROWS / 64; ++u) {
         sd.row[64 * u + lane] = row[u];
         sd.dst[64 * u + lane] = dst[u];
     }
@@ -572,7 +572,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
     constexpr int kStage = (TM + TN) * 128;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kStage];
     __shared__ __attribute__((aligned(16))) uint8_t rows_lds[MODE == kWgrad ? WM * WN : 1][kRowBuf];
-    __shared__ __attribute__((aligned(16))) std::conditional_t<I8, Side<16 * MF>, int> side[I8 ? NW : 1];
+    __shared__ __attribute__((aligned(16))) std::conditional_t<I8, Side<64>, int> side[I8 ? NW : 1];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63;
     const int wm = wave / WN, wn = wave % WN;
@@ -797,12 +797,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(Args p) {
 }  // namespace g16
 
 // Launches the product described by `p` (operands, sizes, epilogue; tiles and
-// tile counts are filled in here). `ws` holds gemm16_ws_bytes for segmented
+// tile counts are filled in here). `ws` holds gemm16_ws_bytes (int8: gemm8_ws_bytes) for segmented
 // FWD and DGRAD. mode is g16::kFwd, kDgrad or kWgrad.
 void launch_gemm16(int mode, int epi, g16::Args p, void* ws, hipStream_t s);
 // The same in int8 (FWD): p.a and p.b hold int8, p.a_scale and p.b_scale their scales; lda, ldb and K count pairs.
 void launch_gemm8(int epi, g16::Args p, void* ws, hipStream_t s);
 size_t gemm16_ws_bytes(int64_t rows, int64_t E);
+size_t gemm8_ws_bytes(int64_t rows, int64_t E);
 // Whether every tile count and lane offset of the product fits (see the limits in nvq.h).
 bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int64_t N, int64_t K);
 

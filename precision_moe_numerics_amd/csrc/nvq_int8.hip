@@ -225,7 +225,7 @@ size_t fwd_carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t d_ff
     nvq_moe_buffers z{};
     const nvq_moe_buffers& in = b ? *b : z;
     o->rws = c.take<uint32_t>(route_ws_words(A, E));
-    o->gws = c.take<uint8_t>(gemm16_ws_bytes(A, E));
+    o->gws = c.take<uint8_t>(gemm8_ws_bytes(A, E));
     o->offsets = in.offsets ? in.offsets : c.take<int32_t>((size_t)E + 1);
     o->s2a = in.sorted2assign ? in.sorted2assign : c.take<int32_t>((size_t)A);
     o->h = in.h ? in.h : c.take<uint16_t>((size_t)(A * d_ff));
@@ -297,7 +297,7 @@ int moe_fc1_swiglu_int8(const int8_t* xq, const float* x_scales, int64_t T, int6
     if (!aligned16(xq) || !aligned16(x_scales) || !aligned16(w1) || !aligned16(w1_scales) || !aligned16(h) ||
         !aligned256(ws))
         return NVQ_ERR_ALIGN;
-    if (ws_bytes < gemm16_ws_bytes(T * k, E)) return NVQ_ERR_WORKSPACE;
+    if (ws_bytes < gemm8_ws_bytes(T * k, E)) return NVQ_ERR_WORKSPACE;
     launch_gemm8(kEpiGlu, fc1_args(xq, x_scales, T, d, offsets, sorted2assign, k, E, d_ff, w1, w1_scales, h), ws,
                  as_stream(stream));
     return launch_status();
@@ -311,13 +311,13 @@ int moe_fc2_int8(const int8_t* hq, const float* h_scales, int64_t A, int64_t d_f
     if (!aligned16(hq) || !aligned16(h_scales) || !aligned16(w2) || !aligned16(w2_scales) || !aligned16(y) ||
         !aligned256(ws))
         return NVQ_ERR_ALIGN;
-    if (ws_bytes < gemm16_ws_bytes(A, E)) return NVQ_ERR_WORKSPACE;
+    if (ws_bytes < gemm8_ws_bytes(A, E)) return NVQ_ERR_WORKSPACE;
     launch_gemm8(kEpiOut, fc2_args(hq, h_scales, A, d_ff, offsets, sorted2assign, E, d, w2, w2_scales, y), ws,
                  as_stream(stream));
     return launch_status();
 }
 
-size_t moe_gemm_int8_workspace_size(int64_t A, int64_t E) { return gemm16_ws_bytes(A, E); }
+size_t moe_gemm_int8_workspace_size(int64_t A, int64_t E) { return gemm8_ws_bytes(A, E); }
 
 size_t moe_expert_fwd_int8_workspace_size(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff) {
     if (T < 0 || d < 0 || k < 1 || E < 1 || d_ff < 0) return 0;
