@@ -12,7 +12,7 @@
 // device counters, handed h over through memory and had their first W2 in
 // flight while they waited, was built and measured too. For 8 of 384 experts,
 // d 4096, f 1024 (us, that kernel and these): one bf16 token 65 and 56, four
-// int8 tokens 113 and 102, one NVFP4 token 43 and 38, 64 of them 515 and 497.
+// int8 tokens 113 and 102, one NVFP4 token 43 and 38, 64 of them 515 and 497 (before WIDE).
 // Noticing that the last workgroup is done and reading h past the caches costs
 // more than a launch.
 //
@@ -42,6 +42,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 enum { kBf16 = 0, kInt8 = 1, kNvfp4 = 2 };
 
@@ -102,7 +103,7 @@ struct Fmt {
 
 struct W16 {
     u32x4 w;
-    uint32_t sc;   // NVFP4: the two scale bytes
+    uint32_t sc;   // NVFP4: the two scale bytes, in the lower or (decode's HI) upper half
 };
 template <int FMT>
 struct X16 {
@@ -128,7 +129,7 @@ __device__ __forceinline__ u32x4 decode_fp4(uint32_t w, half2v scale) {
 }
 
 // Fragment i (8 values) of 16 bytes of weights, in bf16 or (NVFP4) fp16.
-template <int FMT>
+template <int FMT, bool HI = false>
 __device__ __forceinline__ u32x4 decode(const W16& w, int i) {
     if constexpr (FMT == kBf16) {
         return w.w;
@@ -142,7 +143,7 @@ __device__ __forceinline__ u32x4 decode(const W16& w, int i) {
         }
         return o;
     } else {
-        const half2v s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.sc, 1.0f, false);
+        const half2v s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.sc, 1.0f, HI);
         return decode_fp4(w.w[i], half2v{s[i >> 1], s[i >> 1]});
     }
 }
@@ -166,15 +167,33 @@ struct Matrix {
         w = rsrc(static_cast<const uint8_t*>(base) + (int64_t)e * bytes, bytes);
         if (FMT == kNvfp4) s = rsrc(static_cast<const uint8_t*>(scales) + (int64_t)e * (bytes / 8), bytes / 8);
     }
-    // 16 bytes at byte `o` of row `row` (nothing is read where !ok)
+    // 16 bytes at byte `o` of row `row` (nothing is read where !ok) and, unless WIDE, NVFP4's scales
+    template <bool WIDE>
     __device__ __forceinline__ W16 load(uint32_t row, uint32_t o, bool ok) const {
         W16 r;
         const uint32_t at = ok ? row * rb + o : kNowhere;
         r.w = __builtin_amdgcn_raw_buffer_load_b128(w, at, 0, 2);  // read once: past the caches
-        r.sc = FMT == kNvfp4 ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(s, ok ? at / 8 : kNowhere, 0, 0) : 0;
+        r.sc = FMT == kNvfp4 && !WIDE ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(s, ok ? at / 8 : kNowhere, 0, 0) : 0;
         return r;
     }
+    // The eight scale bytes of a row's step (whole steps only).
+    __device__ __forceinline__ u32x2 scales(uint32_t row, int step, bool ok) const {
+        return __builtin_amdgcn_raw_buffer_load_b64(s, ok ? row * (rb / 8) + step * 8 : kNowhere, 0, 0);
+    }
 };
+// NVFP4, WIDE: four steps' scales as one load, lane l taking the eight bytes of step l / 16, of which lane 16 j + r wants
+// bytes 2 j, 2 j + 1 of each: a 4 x 4 transposition between the lanes of a row. sc[0]: steps 0, 1; sc[1]: 2, 3. Two bytes
+// per lane and step, as `load` takes them, are a memory instruction for each weight instruction: the 384-expert layer's 64
+// tokens take 497 us with those, 377 so, eight 143 and 113, one 38 and 34.
+__device__ __forceinline__ void spread(u32x2 v, int lane, uint32_t (&sc)[2]) {
+    const uint32_t half = lane & 16 ? 0x07060302u : 0x05040100u;
+    const auto ab = __builtin_amdgcn_permlane32_swap(v[0], v[1], false, false);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto eo = __builtin_amdgcn_permlane16_swap(ab[i], ab[i], false, false);
+        sc[i] = __builtin_amdgcn_perm(eo[1], eo[0], half);
+    }
+}
 template <int FMT>
 __device__ __forceinline__ X16<FMT> load_x(__amdgpu_buffer_rsrc_t x, uint32_t row, int K, uint32_t o, bool ok) {
     X16<FMT> r;
@@ -518,6 +537,7 @@ __global__ __launch_bounds__(kThreads) void k_decode_choice(Args p) {
 // are in flight all the time, 64 KiB per CU, which the memory serves at 5.4 to 5.6 TB/s (twice as many were no faster).
 template <int FMT>
 struct Stage1 {  // operands of a wave in flight
+    u32x2 raw[Fmt<FMT>::NB];  // WIDE: scales of the steps
     W16 w[Fmt<FMT>::D1][Fmt<FMT>::NB];
     X16<FMT> x[Fmt<FMT>::D1];
 };
@@ -533,8 +553,9 @@ __device__ __forceinline__ uint32_t take(uint32_t* counter) {
     return __hip_atomic_fetch_add(counter + zero, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <int FMT, int P>
+template <int FMT, int P, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
+    static_assert(!WIDE || (FMT == kNvfp4 && Fmt<FMT>::D1 == 4), "four steps' scales");
     constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
     union Scratch {
         struct {
@@ -592,7 +613,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
         const bool ok = s < s_end && o < rb;
         const int col = t.c0 + (r & 7);
 #pragma unroll
-        for (int g = 0; g < NB; ++g) st.w[j][g] = m.load((r < 8 ? 0 : p.f) + col + 8 * g, o, ok && col + 8 * g < p.f);
+        for (int g = 0; g < NB; ++g) {
+            const uint32_t row = (r < 8 ? 0 : p.f) + col + 8 * g;
+            if (WIDE && j == 0) st.raw[g] = m.scales(row, s + q, s + q < s_end && col + 8 * g < p.f);
+            st.w[j][g] = m.template load<WIDE>(row, o, ok && col + 8 * g < p.f);
+        }
         st.x[j] = load_x<FMT>(xr, xrow, p.d, o, ok && r < t.n);
     };
     auto token = [&](const Task1& t) { return (uint32_t)tb.rows[t.row0 + min(r, t.n - 1)].token; };
@@ -635,13 +660,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
             const Task1 tl = last ? tn : t;
             const uint32_t xl = last ? xnext : xrow;
             const int sl = !last ? s_first + (c + 1) * D1 : more ? s_first : s_end;
+            uint32_t sc2[NB][2];
+            if (WIDE) {
+#pragma unroll
+                for (int g = 0; g < NB; ++g) spread(st.raw[g], lane, sc2[g]);
+            }
 #pragma unroll
             for (int j = 0; j < D1; ++j) {
 #pragma unroll
                 for (int i = 0; i < NF; ++i)
 #pragma unroll
-                    for (int g = 0; g < NB; ++g) acc[g] = mfma<FMT>(decode<FMT>(st.w[j][g], i), st.x[j].v[i], acc[g]);
+                    for (int g = 0; g < NB; ++g) {
+                        W16 w = st.w[j][g];
+                        if (WIDE) w.sc = sc2[g][j >> 1 & 1];
+                        acc[g] = mfma<FMT>(WIDE && (j & 1) ? decode<FMT, true>(w, i) : decode<FMT>(w, i), st.x[j].v[i], acc[g]);
+                    }
                 fetch(st, j, tl, xl, sl + j);
+                __builtin_amdgcn_sched_barrier(0);  // (steps run into each other take 80 registers more and are slower)
             }
         }
         // lane: rows 4 q + i of the group (gate 0 .. 7, up 8 .. 15), token r
@@ -710,7 +745,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
 // rows are added in order at the end. Nothing but the operands is loaded inside the loop, so that no wait empties the
 // pipeline (int8 with the channel scales loaded there: four tokens 118 us instead of 102, 64 713 instead of 602). D2 of 6,
 // 10 or (bf16) 12, 16 is within 2 % of 8, the deeper ones on the slow side.
-template <int FMT>
+template <int FMT, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
     constexpr int D2 = 8, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
     __shared__ Block blocks[kMaxV];
@@ -724,7 +759,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
     for (int i = threadIdx.x; i < A; i += kThreads) rows[i] = p.plan->rows[i];
     const auto hr = rsrc(p.h, (uint32_t)A * (uint32_t)p.f * (2u * HP));
     const uint32_t rb = Fmt<FMT>::row_bytes(p.f);
-    const int S = (int)(rb + 63) / 64, total = V * S, part = (total + kWaves - 1) / kWaves;
+    const int S = (int)(rb + 63) / 64, total = V * S;
+    constexpr int kUnit = WIDE ? 4 : 1;  // steps whose scales are one load; a block is whole units of them
+    const int part = (total + kWaves * kUnit - 1) / (kWaves * kUnit) * kUnit;
     const int first = min(wave * part, total), end = min(first + part, total);
     const int n0 = blockIdx.x * 16;
     const bool w_ok = n0 + r < p.d;
@@ -732,6 +769,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
     __syncthreads();
     W16 w[D2];
     u32x4 x[D2][NF][HP];
+    u32x2 raw[D2 / 4];
     int cv = first / S, cs = first - cv * S;  // the next step's block and step in it, of the products
     int lv = cv, ls = cs;                     // and of the loads
     Matrix<FMT> m(p.w2, p.s2, 0, p.d, p.f);
@@ -746,7 +784,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
     auto fetch = [&](int j, bool live) {
         const uint32_t o = (uint32_t)ls * 64 + q * 16;
         const bool ok = live & (o < rb);
-        w[j] = m.load((uint32_t)(n0 + r), o, ok & w_ok);
+        if (WIDE && (j & 3) == 0) raw[j >> 2] = m.scales((uint32_t)(n0 + r), ls + q, live & w_ok);
+        w[j] = m.template load<WIDE>((uint32_t)(n0 + r), o, ok & w_ok);
         const uint32_t from = ok & x_ok ? at + o / 16 * (NF * HP * 16) : kNowhere;
 #pragma unroll
         for (int i = 0; i < NF; ++i)
@@ -768,18 +807,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
         lds_barrier();
     }
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t sc2[2];
     for (int i0 = first; i0 < end; i0 += D2) {
 #pragma unroll
         for (int j = 0; j < D2; ++j) {
+            if (WIDE && (j & 3) == 0) spread(raw[j >> 2], lane, sc2);
             if (i0 + j < end) {
+                W16 wj = w[j];
+                if (WIDE) wj.sc = sc2[j >> 1 & 1];
 #pragma unroll
                 for (int i = 0; i < NF; ++i) {
-                    const u32x4 v = decode<FMT>(w[j], i);
+                    const u32x4 v = WIDE && (j & 1) ? decode<FMT, true>(wj, i) : decode<FMT>(wj, i);
 #pragma unroll
                     for (int half = 0; half < HP; ++half) acc = mfma<FMT>(v, x[j][i][half], acc);
                 }
             }
             fetch(j, i0 + D2 + j < end);
+            __builtin_amdgcn_sched_barrier(0);  // (four int8 tokens 102.5 us without, 100 with)
             if (i0 + j < end && (++cs == S || i0 + j + 1 == end)) {
                 const Block b = blocks[cv];
                 if (r < b.n) {
@@ -842,8 +886,25 @@ void launch_fc1(const Args& p, hipStream_t s) {
     if (p.T > kOwnChoice)
         hipLaunchKernelGGL(k_decode_choice<P>, dim3((unsigned)(p.T + kWaves - 1) / kWaves), dim3(kThreads), 0, s, p);
     const int64_t tasks = (int64_t)p.max_blocks * ((p.f + 8 * NB - 1) / (8 * NB));
-    const unsigned grid = (unsigned)std::min<int64_t>(tasks, device_cus());
-    hipLaunchKernelGGL((k_decode_fc1<FMT, P>), dim3(grid), dim3(kThreads), 0, s, p);
+    const dim3 grid((unsigned)std::min<int64_t>(tasks, device_cus()));
+    if constexpr (FMT == kNvfp4) {
+        if (p.d % 128 == 0) {  // whole steps
+            hipLaunchKernelGGL((k_decode_fc1<FMT, P, true>), grid, dim3(kThreads), 0, s, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_decode_fc1<FMT, P, false>), grid, dim3(kThreads), 0, s, p);
+}
+template <int FMT>
+void launch_fc2(const Args& p, hipStream_t s) {
+    const dim3 grid((unsigned)(p.d + 15) / 16);
+    if constexpr (FMT == kNvfp4) {
+        if (p.f % 512 == 0) {  // blocks of whole groups of four steps
+            hipLaunchKernelGGL((k_decode_fc2<FMT, true>), grid, dim3(kThreads), 0, s, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_decode_fc2<FMT, false>), grid, dim3(kThreads), 0, s, p);
 }
 template <int FMT>
 int run(const Args& p, hipStream_t s) {
@@ -852,7 +913,7 @@ int run(const Args& p, hipStream_t s) {
     if (p.E <= 128) launch_fc1<FMT, 2>(p, s);
     else if (p.E <= 384) launch_fc1<FMT, 6>(p, s);
     else launch_fc1<FMT, 16>(p, s);
-    hipLaunchKernelGGL(k_decode_fc2<FMT>, dim3((unsigned)(p.d + 15) / 16), dim3(kThreads), 0, s, p);
+    launch_fc2<FMT>(p, s);
     return launch_status();
 }
 
