@@ -238,3 +238,69 @@ def test_agrees_with_the_layer_in_parts(fmt):
     assert torch.equal(ids, i2) and torch.allclose(wts, w2_, rtol=1e-5)
     ref = nvq.moe_combine_bf16(y, wts).double()
     assert (out.double() - ref).norm() <= tol * ref.norm()
+
+
+# Steps are 64 bytes of a weight row: several a wave in fc1 (d 8192), a last part of a wave (d 1152), whole groups of four of
+# them in one product only (d 160 and f 512, d 128 and f 640), blocks of 12 and 16 that the waves share unevenly.
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,d,E,k,f", [(3, 8192, 3, 2, 64), (2, 1152, 5, 3, 1536), (10, 160, 6, 2, 512), (9, 128, 6, 4, 640),
+                                       (1, 384, 3, 1, 2048), (20, 256, 7, 3, 1024)])
+def test_steps_of_long_and_uneven_rows(fmt, T, d, E, k, f):
+    verify(fmt, *case(fmt, T, d, E, k, f, sigmoid=True))
+
+
+# More tasks than 24 per workgroup: the last ones are taken from a counter.
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_tasks(fmt):
+    verify(fmt, *case(fmt, 64, 64, 100, 3, 2048))
+    verify(fmt, *case(fmt, 5, 32, 100, 64, 2048, sigmoid=True))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_most_experts_and_choices(fmt):
+    verify(fmt, *case(fmt, 64, 32, 1024, 64, 32, bias=False))
+    verify(fmt, *case(fmt, 64, 32, 64, 64, 32, sigmoid=True))
+
+
+@pytest.mark.parametrize("d,f", [(128, 512), (384, 1024)])
+def test_non_finite_nvfp4_scales_reach_only_their_rows(d, f):
+    """A scale that is not finite, in the middle of a row and next to other rows' and experts'."""
+    a, w1, w2 = case("nvfp4", 12, d, 6, 2, f)
+    clean, ids, wts = run_case("nvfp4", a, w1, w2)
+    w1, w2 = tuple(t.clone() for t in w1), tuple(t.clone() for t in w2)
+    w2[1][2, 9, f // 32], w2[1][4, d - 1, f // 16 - 1] = 0x7F, 0x7F
+    out, ids2, wts2 = run_case("nvfp4", a, w1, w2)
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    bad[(ids == 2).any(1), 9] = True
+    bad[(ids == 4).any(1), d - 1] = True
+    assert bad.any() and torch.equal(ids, ids2) and torch.equal(out[~bad], clean[~bad]) and torch.isnan(out[bad]).all()
+    w1[1][2, f - 1, d // 16 - 1] = 0x7F  # a gate row: all of what expert 2's tokens get
+    out, _, _ = run_case("nvfp4", a, w1, w2)
+    hit = (ids == 2).any(1)
+    assert hit.any() and torch.isnan(out[hit]).all() and torch.equal(out[~hit & ~bad.any(1)], clean[~hit & ~bad.any(1)])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_one_workspace_for_two_captured_graphs(fmt):
+    """Two graphs of other sizes that share a workspace, replayed in turn, with eager calls in it between them."""
+    sizes = [(3, 256, 16, 4, 128), (20, 128, 8, 2, 512)]
+    cases = [case(fmt, *s, seed=20 * i) for i, s in enumerate(sizes)]
+    expect = [run_case(fmt, *c) for c in cases]
+    need = max(nvq.lib().moe_layer_decode_workspace_size(T, d, k, E, f) for T, d, E, k, f in sizes)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for (a, w1, w2), e in zip(cases, expect):
+        o = dict(out=torch.empty_like(e[0]), ids=torch.empty_like(e[1]), weights=torch.empty_like(e[2]), ws=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run_case(fmt, dict(a, **o), w1, w2)
+        graphs.append(g)
+        outs.append(o)
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        for n in ("out", "ids", "weights"):
+            outs[i][n].fill_(77)
+        graphs[i].replay()
+        eager = run_case(fmt, dict(cases[1 - i][0], ws=ws), *cases[1 - i][1:])
+        torch.cuda.synchronize()
+        assert all(torch.equal(outs[i][n], e) for n, e in zip(("out", "ids", "weights"), expect[i]))
+        assert all(torch.equal(p, e) for p, e in zip(eager, expect[1 - i]))
