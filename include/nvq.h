@@ -27,8 +27,9 @@
  *     static buffer); every call is safe to make from several host threads.
  *   - Asynchrony: all work is enqueued on `stream` (a hipStream_t; NULL is the
  *     default stream). No call synchronizes with the host.
- *   - Determinism: identical inputs give identical output bytes (no atomics;
- *     maxima are folded from partial maxima written with plain stores).
+ *   - Determinism: identical inputs give identical output bytes (no atomics
+ *     on values; maxima are folded from partial maxima written with plain
+ *     stores).
  *   - Errors: every call returns an NVQ_* status. Argument errors are
  *     detected on the host before anything is launched. Preconditions that
  *     would need a device read (finite inputs, 0 <= topk_ids < E) are not
@@ -636,19 +637,21 @@ int moe_fc2_int8(const int8_t* hq, const float* h_scales, int64_t A, int64_t d_f
 /*   topk_ids, weights: as moe_router_softmax_topk (NVQ_ROUTER_SOFTMAX) or    */
 /*     moe_router_sigmoid_topk (NVQ_ROUTER_SIGMOID) choose from the logits,   */
 /*     which are not rounded in between; bias [E] fp32 (nullable: 0)          */
-/*   h = silu(W1g x) * (W1u x) for every chosen expert (kept to 2^-17)        */
+/*   h = silu(W1g x) * (W1u x) for every chosen expert (kept to 2^-16; with   */
+/*     NVFP4 weights to 2^-11)                                                */
 /*   out[t] = residual[t] + sum_s weights[t][s] * (W2 h), rounded once        */
 /* Only the weights are quantized; what one token gets does not depend on the */
-/* others but for the order of its fp32 sums. w_router bf16 [E, d], residual (nullable)  */
-/* and out [T, d] bf16, topk_ids [T, k] int32 and weights [T, k] fp32 are    */
-/* outputs. Expert weights as for moe_expert_fwd_bf16, _int8 and _nvfp4; what */
-/* an expert's weights hold reaches only the tokens that chose it. Limits     */
-/* (else NVQ_ERR_DIM): 0 <= T <= 64, 1 <= k <= min(E, 64), E <= 1024, d and   */
-/* d_ff multiples of 8 (bf16), 16 (int8) or 32 (NVFP4) up to 2^22, one        */
-/* expert's matrix, w_router and T*k*d_ff fp32 values below 4 GiB - 512. All */
-/* pointers 16-byte aligned, ws 256-byte. Outputs must not overlap inputs or  */
-/* the workspace (residual == out is allowed). Non-finite logits: ids are     */
-/* distinct and in range, but otherwise undefined.                           */
+/* others but for the order of its fp32 sums, which is fixed for given        */
+/* inputs. w_router bf16 [E, d], residual (nullable) and out [T, d] bf16;     */
+/* topk_ids [T, k] int32 and weights [T, k] fp32 are outputs. Expert weights  */
+/* as for moe_expert_fwd_bf16, _int8 and _nvfp4; what an expert's weights     */
+/* hold reaches only the tokens that chose it. Limits (else NVQ_ERR_DIM): 0   */
+/* <= T <= 64, 1 <= k <= min(E, 64), E <= 1024, d and d_ff multiples of 8     */
+/* (bf16), 16 (int8) or 32 (NVFP4) up to 2^22, one expert's matrix, w_router  */
+/* and T*k*d_ff fp32 values below 4 GiB - 512. All pointers 16-byte aligned,  */
+/* ws 256-byte. Outputs must not overlap inputs or the workspace (residual == */
+/* out is allowed). Non-finite logits: ids are distinct and in range, but     */
+/* otherwise undefined.                                                       */
 /* ------------------------------------------------------------------------ */
 enum { NVQ_ROUTER_SOFTMAX = 0, NVQ_ROUTER_SIGMOID = 1 };
 size_t moe_layer_decode_workspace_size(int64_t T, int64_t d, int k, int64_t E, int64_t d_ff);

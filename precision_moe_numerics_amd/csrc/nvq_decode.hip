@@ -23,12 +23,12 @@
 // the channel's or tensor's fp32 scale is applied to the fp32 sum.
 //
 // The other operand. bf16 and int8 weights: x as it is, and h as two bf16 parts,
-// its rounding and the rounding of what that left (2^-17 of it in all; one part
-// would be 2^-9, as much as out's own rounding), which costs only products and
+// its rounding and the rounding of what that left (2^-16 of it in all; one part
+// would be 2^-8, as much as out's own rounding), which costs only products and
 // these are far from the limit. NVFP4 weights: x in fp16 times a power of two
 // per token that takes its largest value to [2^14, 2^15), which holds its 8 bits
 // down to 2^-29 of that and is off by at most 2^-40 of it below; and h rounded to
-// fp16 once (2^-12 of it), times a power of two that no h of the token and expert
+// fp16 once (2^-11 of it), times a power of two that no h of the token and expert
 // can exceed, from the 1-norm of x and the expert's largest possible weight.
 #include "nvq_argmax.hpp"
 #include "nvq_device.hpp"

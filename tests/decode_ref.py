@@ -4,12 +4,14 @@ Bounds, U = 2^-23 per fp32 operation of a sum (2^-24 rounded, twice that where t
   logits   every 32 products are summed to fp32, then in fp64: U * sum |x w|
   weights  a softmax or a ratio of sigmoids of logits off by dl: 2.1 dl relative, and the rounding to fp32
   g, u     K U sum |x w|, and one product with a scale
-  h        bf16_ref.act_bound, and the rounding to bf16
+  h        bf16_ref.act_bound, and its rounding: two bf16 parts, 2^-16 of it; NVFP4 fp16, 2^-11 of it and half the smallest
+           subnormal, 2^-25, times 2^exp, where 2^(exp + 15) is the square of three factors' product rounded up to powers
+           of two (each at most twice): the sum of |x|, 2688 and w1's tensor scale
   out      f U sum |w2 h|, a product with a scale, weights and the at most k + 16 partial sums that are added
 """
 import torch
 
-from bf16_ref import SWIGLU, U8, U23, act_bound, act_ref, d64
+from bf16_ref import SWIGLU, U23, act_bound, act_ref, d64
 
 E2M1 = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
 
@@ -58,8 +60,8 @@ def check_choice(ids, weights, key, lg, dl, k, sigmoid):
     return ids, w, dw
 
 
-def layer(x, ids, w, dw, w1, w2, residual):
-    """(out, bound of its fp32 value) for 64-bit weights w1 [E, 2f, d], w2 [E, d, f]."""
+def layer(x, ids, w, dw, w1, w2, residual, t1=None):
+    """(out, bound of its fp32 value) for 64-bit weights w1 [E, 2f, d], w2 [E, d, f]. t1: NVFP4's tensor scales of w1."""
     T, k = ids.shape
     f, d = w2.shape[2], w2.shape[1]
     out = torch.zeros((T, d), dtype=torch.float64)
@@ -72,7 +74,11 @@ def layer(x, ids, w, dw, w1, w2, residual):
             dz = (d + 2) * U23 * (xt.abs() @ w1[e].abs().T)
             h = act_ref(z, SWIGLU, f)[0]
             dh = act_bound(z, dz, SWIGLU, f)
-            dh = dh + U8 * (h.abs() + dh) + 2.0 ** -133
+            if t1 is None:
+                dh = dh + 2.0 ** -16 * (h.abs() + dh) + 2.0 ** -133
+            else:
+                top = float(xt.abs().sum()) * 2688.0 * float(t1[e])
+                dh = dh + 2.0 ** -11 * (h.abs() + dh) + 2.0 ** -40 * (4.0 * top) ** 2
             y, a = (h @ w2[e].T)[0], ((h.abs() + dh) @ w2[e].abs().T)[0]
             dy = (dh @ w2[e].abs().T)[0] + (f + 2) * U23 * a
             out[t] += w[t, s] * y

@@ -64,7 +64,8 @@ def verify(fmt, a, w1, w2):
     sigmoid = a["router"] == nvq.ROUTER_SIGMOID
     key, lg, dl = route(a["x"], a["w_router"], a["bias"], a["k"], sigmoid)
     idc, w, dw = check_choice(ids, wts, key, lg, dl, a["k"], sigmoid)
-    ref, err = layer(a["x"], idc, w, dw, values(w1, fmt), values(w2, fmt), a["residual"])
+    ref, err = layer(a["x"], idc, w, dw, values(w1, fmt), values(w2, fmt), a["residual"],
+                     w1[2] if fmt == "nvfp4" else None)
     check(out, ref, out_bound(ref, err, False), "out")
     again = run_case(fmt, a, w1, w2)
     assert all(torch.equal(p, q) for p, q in zip((out, ids, wts), again))
