@@ -1007,20 +1007,25 @@ def moe_expert_fwd_int8(x, topk_ids, w1q, w2q, export=False, y=None, ws=None):
 
 
 # ------------------------------------------------------------------ the whole layer for a few tokens
+def _result(t, dtype, name, shape, device):
+    """(output, its address): the caller's, checked, or a new one."""
+    if t is not None:
+        return t, _arg(t, dtype, name, shape, device)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    return t, t.data_ptr()
+
+
 def _layer_decode(name, x, w_router, k, E, d_ff, w, bias, router, residual, out, ids, weights, ws):
     bf, f32 = torch.bfloat16, torch.float32
     dev, (T, d) = _main(x, bf, "x", 2)
-    if out is None:
-        out = torch.empty((T, d), dtype=bf, device=dev)
-    if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if weights is None:
-        weights = torch.empty((T, k), dtype=f32, device=dev)
     addresses = [_arg(t, dtype, n, shape, dev) for t, dtype, n, shape in w]
+    w_router, bias = _arg(w_router, bf, "w_router", (E, d), dev), _arg(bias, f32, "bias", (E,), dev)
+    residual = _arg(residual, bf, "residual", (T, d), dev)
+    out, op = _result(out, bf, "out", (T, d), dev)
+    ids, ip = _result(ids, torch.int32, "ids", (T, k), dev)
+    weights, wp = _result(weights, f32, "weights", (T, k), dev)
     s, sp, sn = _scratch(lib().moe_layer_decode_workspace_size(T, d, k, E, d_ff), dev, ws)
-    _launch(name, dev, x.data_ptr(), T, d, _arg(w_router, bf, "w_router", (E, d), dev), _arg(bias, f32, "bias", (E,), dev),
-            router, k, E, d_ff, *addresses, _arg(residual, bf, "residual", (T, d), dev), _arg(out, bf, "out", (T, d), dev),
-            _arg(ids, torch.int32, "ids", (T, k), dev), _arg(weights, f32, "weights", (T, k), dev), sp, sn)
+    _launch(name, dev, x.data_ptr(), T, d, w_router, bias, router, k, E, d_ff, *addresses, residual, op, ip, wp, sp, sn)
     return out, ids, weights
 
 

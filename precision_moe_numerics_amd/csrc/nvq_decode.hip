@@ -747,7 +747,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
 // 10 or (bf16) 12, 16 is within 2 % of 8, the deeper ones on the slow side.
 template <int FMT, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
-    constexpr int D2 = 8, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
+    constexpr int D2 = 8, kOuts = kMaxT * 16 / kThreads, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
     __shared__ Block blocks[kMaxV];
     __shared__ Row rows[kMaxA];
     __shared__ float sums[kWaves][kMaxT][17];
@@ -765,7 +765,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
     const int first = min(wave * part, total), end = min(first + part, total);
     const int n0 = blockIdx.x * 16;
     const bool w_ok = n0 + r < p.d;
-    for (int z = threadIdx.x; z < kWaves * kMaxT * 17; z += kThreads) (&sums[0][0][0])[z] = 0.0f;
+#pragma unroll 1
+    for (int z = lane; z < p.T * 17; z += 64) (&sums[wave][0][0])[z] = 0.0f;
+    uint16_t old[kOuts] = {};  // the residual of this thread's outputs, ahead of all other loads
+#pragma unroll
+    for (int u = 0; u < kOuts; ++u) {
+        const int i = threadIdx.x + u * kThreads, c = i & 15;
+        if (p.residual && i < p.T * 16 && n0 + c < p.d) old[u] = p.residual[(int64_t)(i >> 4) * p.d + n0 + c];
+    }
     __syncthreads();
     W16 w[D2];
     u32x4 x[D2][NF][HP];
@@ -841,15 +848,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.T * 16; i += kThreads) {
-        const int t = i >> 4, c = i & 15;
-        if (n0 + c >= p.d) continue;
+#pragma unroll
+    for (int u = 0; u < kOuts; ++u) {
+        const int i = threadIdx.x + u * kThreads, t = i >> 4, c = i & 15;
+        if (i >= p.T * 16 || n0 + c >= p.d) continue;
         float v = sums[0][t][c];
 #pragma unroll
         for (int k = 1; k < kWaves; ++k) v += sums[k][t][c];
-        const int64_t at = (int64_t)t * p.d + n0 + c;
-        if (p.residual) v += bf16_to_f32(p.residual[at]);
-        p.out[at] = (uint16_t)bf16x2_rne(v, v);
+        if (p.residual) v += bf16_to_f32(old[u]);
+        p.out[(int64_t)t * p.d + n0 + c] = (uint16_t)bf16x2_rne(v, v);
     }
 }
 
