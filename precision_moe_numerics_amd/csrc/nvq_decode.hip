@@ -793,7 +793,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
         const bool ok = live & (o < rb);
         if (WIDE && (j & 3) == 0) raw[j >> 2] = m.scales((uint32_t)(n0 + r), ls + q, live & w_ok);
         w[j] = m.template load<WIDE>((uint32_t)(n0 + r), o, ok & w_ok);
-        const uint32_t from = ok & x_ok ? at + o / 16 * (NF * HP * 16) : kNowhere;
+        const uint32_t from = (ok & x_ok) ? at + o / 16 * (NF * HP * 16) : kNowhere;
 #pragma unroll
         for (int i = 0; i < NF; ++i)
 #pragma unroll

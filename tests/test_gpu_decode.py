@@ -305,3 +305,21 @@ def test_one_workspace_for_two_captured_graphs(fmt):
         torch.cuda.synchronize()
         assert all(torch.equal(outs[i][n], e) for n, e in zip(("out", "ids", "weights"), expect[i]))
         assert all(torch.equal(p, e) for p, e in zip(eager, expect[1 - i]))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("s", [2.0 ** 40, 2.0 ** -40])
+def test_large_and_small_activations(fmt, s):
+    """x times a power of two, the router's weights divided by it, so that the choice is an ordinary one."""
+    a, w1, w2 = case(fmt, 6, 256, 8, 2, 512)
+    verify(fmt, dict(a, x=a["x"] * s, w_router=a["w_router"] / s, residual=None), w1, w2)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_tokens_of_zeros_and_of_far_apart_values(fmt):
+    a, w1, w2 = case(fmt, 5, 256, 8, 2, 512, sigmoid=True)
+    x = a["x"].clone()
+    x[1] = 0.0
+    x[3, 1:] *= 2.0 ** -30
+    x[4, ::2] *= 2.0 ** -20
+    verify(fmt, dict(a, x=x), w1, w2)

@@ -323,3 +323,15 @@ def test_graph_replays_match_eager():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, expect[sel]) and torch.equal(out, dense[sel])
+
+
+@pytest.mark.parametrize("shape", [(1024, 2064), (1025, 16), (1025, 1040), (1026, 2048), (1027, 2064), (1, 16400), (1030, 16400)])
+def test_quantize_on_both_sides_of_long_and_many_rows(shape):
+    test_quantize(shape)
+
+
+@pytest.mark.parametrize("lens", [[1, 65, 127, 0, 200, 333, 64], [1000]], ids=lambda v: "x".join(map(str, v)))
+@pytest.mark.parametrize("d,f", [(512, 2048), (2048, 256), (272, 2064)])
+def test_fc1_and_fc2_of_few_tiles(lens, d, f):
+    """Segments of some hundred rows and few columns: tiles of 64 rows, with every kind of last tile."""
+    test_fc1_and_fc2(lens, d, f)
