@@ -630,8 +630,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
     const int em = threadIdx.x / (4 * NB), eg = threadIdx.x / 4 % NB, ep = threadIdx.x & 3;
     const int ej = FMT == kNvfp4 ? (ep & 1) * 4 + (ep >> 1) : 2 * ep, ej2 = ej + (FMT == kNvfp4 ? 2 : 1);
     // A workgroup's tasks are blockIdx.x, + G, ...; where there are many, only those before `tail`, whole rounds, and the
-    // rest is taken from a counter, two tasks ahead of its use (64 tokens on NVFP4 weights: the last workgroup then ends
-    // 6 us after the median one instead of 34). Which workgroup does a task does not show in its result.
+    // rest is taken from a counter, two tasks ahead of its use (64 tokens of 384 experts without
+    // and with, before WIDE: NVFP4 504 and 497 us, int8 607 and 599, bf16 1013 and 995; the last workgroup ends 6 us after
+    // the median one instead of 34). Which workgroup does a task does not show in its result.
     const int tail = N1 >= 24 * G ? (N1 / G - 4) * G : N1;
     int cur = blockIdx.x, nxt = cur + G, flip = 0;
     if (cur >= N1) return;
