@@ -637,8 +637,7 @@ int moe_fc2_int8(const int8_t* hq, const float* h_scales, int64_t A, int64_t d_f
 /*   topk_ids, weights: as moe_router_softmax_topk (NVQ_ROUTER_SOFTMAX) or    */
 /*     moe_router_sigmoid_topk (NVQ_ROUTER_SIGMOID) choose from the logits,   */
 /*     which are not rounded in between; bias [E] fp32 (nullable: 0)          */
-/*   h = silu(W1g x) * (W1u x) for every chosen expert (kept to 2^-16; with   */
-/*     NVFP4 weights to 2^-11)                                                */
+/*   h = silu(W1g x) * (W1u x) for every chosen expert (kept to 2^-16)        */
 /*   out[t] = residual[t] + sum_s weights[t][s] * (W2 h), rounded once        */
 /* Only the weights are quantized; what one token gets does not depend on the */
 /* others but for the order of its fp32 sums, which is fixed for given        */

@@ -18,18 +18,16 @@
 //
 // Bound by reading the chosen experts' weights once. The activations are not
 // quantized: they are a few rows, and it would save nothing. A weight reaches
-// the matrix pipe as a 16-bit value that holds it exactly (int8 codes have 8
-// significant bits: bf16; e2m1 * e4m3 has 6 and lies in [2^-10, 2688]: fp16);
-// the channel's or tensor's fp32 scale is applied to the fp32 sum.
+// the matrix pipe as the bf16 value that holds it exactly (int8 codes have 8
+// significant bits, e2m1 * e4m3 has 6); the channel's or tensor's fp32 scale is
+// applied to the fp32 sum.
 //
-// The other operand. bf16 and int8 weights: x as it is, and h as two bf16 parts,
-// its rounding and the rounding of what that left (2^-16 of it in all; one part
-// would be 2^-8, as much as out's own rounding), which costs only products and
-// these are far from the limit. NVFP4 weights: x in fp16 times a power of two
-// per token that takes its largest value to [2^14, 2^15), which holds its 8 bits
-// down to 2^-29 of that and is off by at most 2^-40 of it below; and h rounded to
-// fp16 once (2^-11 of it), times a power of two that no h of the token and expert
-// can exceed, from the 1-norm of x and the expert's largest possible weight.
+// The other operand is x as it is, and h as two bf16 parts, its rounding and the
+// rounding of what that left (2^-16 of it in all; one part would be 2^-8, as much
+// as out's own rounding). bf16's exponents hold whatever fp32's do, so nothing has
+// to be known of h's size beforehand: fp16 needs a power of two per row, and the
+// only one at hand before h is computed, from the 1-norm of x and the largest
+// weight that the tensor scale allows, can lie any number of bits above h.
 #include "nvq_argmax.hpp"
 #include "nvq_device.hpp"
 #include "nvq_host.hpp"
@@ -51,14 +49,10 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxK = 64;
 constexpr int kMaxA = kMaxT * kMaxK;
 constexpr int kMaxV = kMaxE + kMaxA / 16;  // blocks of at most 16 tokens of one expert
+constexpr int kMaxV8 = kMaxE + kMaxA / 8;  // of at most eight
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int64_t kMaxBytes = 0xFFFFFE00ll;     // of a buffer
 constexpr uint32_t kNowhere = (uint32_t)kMaxBytes;  // an offset behind any buffer's end, also with 511 added: reads zeros
-
-// x of a token for NVFP4 weights is its fp16 values times 2^shift; the sum of these values' magnitudes is below 2^norm.
-struct TokenScale {
-    int32_t shift, norm;
-};
 
 struct Args {
     const uint16_t* x;
@@ -72,12 +66,11 @@ struct Args {
     int32_t* ids;
     float* weights;
     double* logits;           // [parts, T, E]: sums over parts of K
-    uint16_t* h;              // [T k, f], rows in expert order; bf16: each eight values' high, then low parts
-    uint16_t* xh;             // NVFP4: [T, d] fp16 (both in the order of half_slot)
-    TokenScale* xs;
+    uint16_t* h;              // [T k, f], rows in expert order: each eight values' high, then low parts
+    uint16_t* xp;             // NVFP4: x (both in the order of decoded codes)
     uint32_t* tail;           // tasks taken of fc1's tail (k_decode_router clears it)
     struct Plan* plan;        // fc1's table, for fc2
-    int T, d, E, k, f, sigmoid, parts, max_blocks;
+    int T, d, E, k, f, sigmoid, parts, max_blocks;  // max_blocks: of fc2
 };
 
 // A value that all lanes of a wave hold, as a scalar: branches on it are the wave's, not a lane's. Every loop here that
@@ -97,7 +90,7 @@ struct Fmt {
     static constexpr int kFrags = kVals / 8;
     static constexpr int NB = FMT == kBf16 ? 1 : 2;         // fc1: groups of 16 weight rows of a wave
     static constexpr int D1 = FMT == kBf16 ? 8 : 4;         // steps in flight in fc1
-    static constexpr int kParts = FMT == kNvfp4 ? 1 : 2;    // 16-bit parts of h
+    static constexpr int kRows = FMT == kNvfp4 ? 8 : 16;    // tokens of a block in fc2
     static __host__ __device__ __forceinline__ uint32_t row_bytes(int K) { return (uint32_t)(K / kVals) * 16u; }
 };
 
@@ -110,27 +103,48 @@ struct X16 {
     u32x4 v[Fmt<FMT>::kFrags];
 };
 
-// Slot of value j of eight in the fp16 operands: the pairs in which NVFP4 codes are decoded, (0 2) (4 6) (1 3) (5 7).
-__host__ __device__ constexpr int half_slot(int j) { return (j & 1) * 4 + (j >> 1); }
-
-// Eight E2M1 codes times an E4M3 scale in fp16, exact, in the order of half_slot. The upper byte of an E2M1 value's fp16
-// holds all of it: a byte permute looks up four magnitudes at a time, a bit select adds the signs, four more permutes
-// spread the bytes over halves. 16 full-rate operations for 8 values; four conversions and products (the converter runs
-// at a quarter of the rate) would take as long as 20, fp32 conversions as 28.
-__device__ __forceinline__ u32x4 decode_fp4(uint32_t w, half2v scale) {
-    constexpr uint32_t kLo = 0x3E3C3800u, kHi = 0x46444240u;  // 0 .5 1 1.5, 2 3 4 6
-    const uint32_t even = __builtin_amdgcn_perm(kHi, kLo, w & 0x07070707u);
-    const uint32_t odd = __builtin_amdgcn_perm(kHi, kLo, (w >> 4) & 0x07070707u);
-    const uint32_t e = (even & 0x7F7F7F7Fu) | ((w << 4) & 0x80808080u), o = (odd & 0x7F7F7F7Fu) | (w & 0x80808080u);
-    auto put = [&](uint32_t bytes, uint32_t sel) {
-        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0u, bytes, sel)) * scale);
-    };
-    return (u32x4){put(e, 0x010C000Cu), put(e, 0x030C020Cu), put(o, 0x010C000Cu), put(o, 0x030C020Cu)};
+// NVFP4's codes are decoded in the pairs (0 2) (4 6) (1 3) (5 7) of eight, and the other operands are held in that order.
+//
+// The eight magnitudes of E2M1 times the E4M3 scale `byte`, as bf16 (6 significant bits at most: exact; all NaN for a NaN):
+// the lower bytes of codes 0 .. 3 and 4 .. 7, then the upper ones.
+__device__ __forceinline__ u32x4 fp4_products(uint32_t byte) {
+    const float s = __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
+    constexpr float kMag[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
+    u32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint32_t b = __float_as_uint(kMag[c] * s);
+        o[c >> 2] |= (b >> 16 & 0xFFu) << 8 * (c & 3);
+        o[2 + (c >> 2)] |= (b >> 24) << 8 * (c & 3);
+    }
+    return o;
+}
+// fp4_products of every scale byte, in LDS, by all threads.
+__device__ __forceinline__ void fill_products(u32x4 (&table)[256]) {
+    if (threadIdx.x < 256) table[threadIdx.x] = fp4_products(threadIdx.x);
 }
 
-// Fragment i (8 values) of 16 bytes of weights, in bf16 or (NVFP4) fp16.
-template <int FMT, bool HI = false>
-__device__ __forceinline__ u32x4 decode(const W16& w, int i) {
+// fc2, WIDE (d_ff a multiple of kWideF): place of a row's group u of eight h. A lane takes four neighbouring groups of a step's
+// 16, one with each load; the groups that the lanes of one load take are neighbours here, whole lines of both parts (64
+// tokens of 384 experts 397 us without, 394 with; of 8, all chosen, 154 and 146).
+constexpr int kWideF = 512;  // blocks of whole groups of four steps
+__device__ __forceinline__ int wide_group(int u) { return (u & ~15) | (u & 3) << 2 | (u >> 2 & 3); }
+
+// Eight E2M1 codes times the scale of products `t`. Byte permutes look up lower and upper bytes four
+// codes at a time, the codes' signs flip the upper ones, four more permutes join them: 14 full-rate operations for 8 values, and
+// one LDS read for 16 of them. (Multiplying by the scale would be done in fp32, 28 operations.)
+__device__ __forceinline__ u32x4 decode_fp4(uint32_t w, u32x4 t) {
+    const uint32_t even = w & 0x07070707u, odd = (w >> 4) & 0x07070707u;
+    const uint32_t el = __builtin_amdgcn_perm(t[1], t[0], even), ol = __builtin_amdgcn_perm(t[1], t[0], odd);
+    const uint32_t eh = __builtin_amdgcn_perm(t[3], t[2], even) ^ ((w << 4) & 0x80808080u);
+    const uint32_t oh = __builtin_amdgcn_perm(t[3], t[2], odd) ^ (w & 0x80808080u);
+    return (u32x4){__builtin_amdgcn_perm(eh, el, 0x05010400u), __builtin_amdgcn_perm(eh, el, 0x07030602u),
+                   __builtin_amdgcn_perm(oh, ol, 0x05010400u), __builtin_amdgcn_perm(oh, ol, 0x07030602u)};
+}
+
+// Fragment i (8 values) of 16 bytes of weights, in bf16. `table`: NVFP4's fill_products.
+template <int FMT, bool HI = false, typename Table>
+__device__ __forceinline__ u32x4 decode(const W16& w, int i, const Table& table) {
     if constexpr (FMT == kBf16) {
         return w.w;
     } else if constexpr (FMT == kInt8) {
@@ -143,17 +157,11 @@ __device__ __forceinline__ u32x4 decode(const W16& w, int i) {
         }
         return o;
     } else {
-        const half2v s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.sc, 1.0f, HI);
-        return decode_fp4(w.w[i], half2v{s[i >> 1], s[i >> 1]});
+        return decode_fp4(w.w[i], table[w.sc >> (16 * HI + 8 * (i >> 1)) & 0xFFu]);
     }
 }
-template <int FMT>
 __device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 acc) {
-    if constexpr (FMT == kNvfp4)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, x), acc, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0,
-                                                       0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
 }
 
 // The matrices of one expert: `rows` rows of K values.
@@ -217,59 +225,28 @@ __device__ __forceinline__ void lds_barrier() {
 // the launch took 6.6 us.
 constexpr int kRouterWaves = 4, kRouterThreads = 64 * kRouterWaves;
 
-// x of token t in fp16 for NVFP4 weights (one workgroup).
-__device__ __forceinline__ void scale_token(const Args& p, int t) {
-    __shared__ uint32_t tops[kRouterWaves];
-    __shared__ float sums[kRouterWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, units = p.d / 8;
+// x of token t in the order of decoded codes for NVFP4 weights (one workgroup).
+__device__ __forceinline__ void order_token(const Args& p, int t) {
     const u32x4* src = reinterpret_cast<const u32x4*>(p.x + (int64_t)t * p.d);
-    u32x4* dst = reinterpret_cast<u32x4*>(p.xh + (int64_t)t * p.d);
-    uint32_t m = 0;
+    u32x4* dst = reinterpret_cast<u32x4*>(p.xp + (int64_t)t * p.d);
 #pragma unroll 2
-    for (int u = threadIdx.x; u < units; u += kRouterThreads) {
+    for (int u = threadIdx.x; u < p.d / 8; u += kRouterThreads) {
         const u32x4 v = src[u];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
-    }
-    m = wave_max_u32(m);
-    if (lane == 0) tops[wave] = m;
-    __syncthreads();
-    m = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-    // a row without a largest finite value keeps its size: what it holds becomes infinities and NaN
-    const int shift = m && m < 0x7F80u ? __builtin_amdgcn_frexp_expf(bf16_to_f32(m)) - 15 : 0;
-    float sum = 0.0f;
-#pragma unroll 2
-    for (int u = threadIdx.x; u < units; u += kRouterThreads) {
-        const u32x4 v = src[u];
-        half8 o;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = v[j >> 1];
-            const float f = __builtin_amdgcn_ldexpf(__uint_as_float((j & 1) ? b & 0xFFFF0000u : b << 16), -shift);
-            sum += fabsf(f);
-            o[half_slot(j)] = (_Float16)f;
-        }
-        dst[u] = __builtin_bit_cast(u32x4, o);
-    }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    if (lane == 0) sums[wave] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-        p.xs[t] = {shift, __builtin_amdgcn_frexp_expf(sum)};
+        auto even = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); };
+        auto odd = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };
+        dst[u] = (u32x4){even(v[0], v[1]), even(v[2], v[3]), odd(v[0], v[1]), odd(v[2], v[3])};
     }
 }
 
-template <bool HALF>
+template <bool ORDER>
 __global__ __launch_bounds__(kRouterThreads) void k_decode_router(Args p) {
     __shared__ double red[kRouterWaves][16][17];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.tail = 0;
     int b = blockIdx.x;
-    if (HALF) {
-        if (b < p.T) return scale_token(p, b);
+    if (ORDER) {
+        if (b < p.T) return order_token(p, b);
         b -= p.T;
     }
     const int eb = (p.E + 15) / 16, tb = (p.T + 15) / 16;
@@ -290,7 +267,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_decode_router(Args p) {
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const f32x4 a = mfma<kBf16>(w[j], x[j], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+            const f32x4 a = mfma(w[j], x[j], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] += (double)a[i];
         }
@@ -401,8 +378,8 @@ __device__ __forceinline__ void choose(const Args& p, const double* val, const f
     *weight = (float)(v / sum);
 }
 
-// The chosen experts and their tokens: blocks of at most 16 tokens of one expert, in ascending expert order; row
-// row0 + i of h and of rows is token i of the block.
+// The chosen experts and their tokens: blocks of at most 16 tokens of one expert (NVFP4's fc2: eight), in ascending expert
+// order; row row0 + i of h and of rows is token i of the block.
 struct Block {
     int16_t e;
     int16_t row0;
@@ -410,13 +387,12 @@ struct Block {
 };
 struct Row {
     float wt;       // routing weight; NVFP4: times w2's tensor scale
-    int16_t exp;    // NVFP4: h is its fp16 value times 2^exp
-    int16_t token;
+    int32_t token;
 };
-struct Plan {
+struct Plan {       // fc2's
     int32_t blocks_n;
     int32_t pad[3];
-    Block blocks[kMaxV];
+    Block blocks[kMaxV8];
     Row rows[kMaxA];
 };
 struct Table {
@@ -424,23 +400,20 @@ struct Table {
     int32_t base[kMaxE];   // its first row
     Block blocks[kMaxV];
     Row rows[kMaxA];
-    int32_t scan[kWaves];
+    uint32_t scan[kWaves];
 };
-// NVFP4, per row: g and u are the sums times t1 times 2^shift.
-struct RowScale {
-    float t1;
-    int32_t shift;
-};
-// From ids and weights (of another launch, or of this workgroup). All threads take part; returns the number of blocks.
+// From ids and weights (of another launch, or of this workgroup). All threads take part; returns the number of blocks. t1:
+// NVFP4's w1 tensor scale per row. `plan`: where not null, fc2's blocks go there.
 template <int FMT>
-__device__ __forceinline__ int build(Table& tb, RowScale* scale, const Args& p, const int32_t* ids, const float* weights) {
+__device__ __forceinline__ int build(Table& tb, float* t1, Plan* plan, const Args& p, const int32_t* ids,
+                                     const float* weights) {
+    constexpr int kRows = Fmt<FMT>::kRows;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int A = p.T * p.k;
     struct Scales {
         float t1, t2;
-        TokenScale x;
     };
-    auto scales = [&](int a) { return Scales{p.t1[ids[a]], p.t2[ids[a]], p.xs[a / p.k]}; };
+    auto scales = [&](int a) { return Scales{p.t1[ids[a]], p.t2[ids[a]]}; };
     Scales early = {};  // of row t, on their way while the table is made
     if (FMT == kNvfp4 && t < A) early = scales(t);
     for (int e = t; e < p.E; e += kThreads) tb.mask[e] = 0;
@@ -448,59 +421,63 @@ __device__ __forceinline__ int build(Table& tb, RowScale* scale, const Args& p, 
     for (int a = t; a < A; a += kThreads)
         atomicOr(reinterpret_cast<unsigned long long*>(&tb.mask[ids[a]]), 1ull << (a / p.k));
     __syncthreads();
-    // prefix sums over the experts (two neighbouring ones per thread) of rows (low half) and blocks (high half)
-    int n[2], sum = 0;
+    // prefix sums over the experts (two neighbouring ones per thread) of blocks (the lowest 11 bits: at most kMaxV), of what
+    // blocks of eight are more (9 bits: at most kMaxA / 9) and of rows (12 bits, modulo kMaxA: an expert with rows starts below)
+    static_assert(kMaxV < 1 << 11 && kMaxA / 9 < 1 << 9 && kMaxA == 1 << 12, "packed sums");
+    auto counts = [](uint32_t n) { return (n + 15) / 16 | (n + 7) / 16 << 11 | n << 20; };
+    uint32_t n[2], sum = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int e = 2 * t + j;
         n[j] = e < p.E ? __popcll(tb.mask[e]) : 0;
-        sum += n[j] | ((n[j] + 15) / 16) << 16;
+        sum += counts(n[j]);
     }
-    int incl = sum;
+    uint32_t incl = sum;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int v = __shfl_up(incl, off, 64);
+        const uint32_t v = (uint32_t)__shfl_up((int)incl, off, 64);
         incl += lane >= off ? v : 0;
     }
     if (lane == 63) tb.scan[wave] = incl;
     __syncthreads();
-    int before = 0, total = 0;
+    uint32_t before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        const int v = tb.scan[w];
+        const uint32_t v = tb.scan[w];
         before += w < wave ? v : 0;
         total += v;
     }
-    int at = before + incl - sum;
+    uint32_t at = before + incl - sum;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int e = 2 * t + j;
         if (e < p.E) {
-            const int row = at & 0xFFFF, b = at >> 16;
+            const int row = at >> 20, b = at & 0x7FF, more = at >> 11 & 0x1FF, m = (int)n[j];
+            auto put = [&](Block* to, int rows) {
+                for (int i = 0; i * rows < m; ++i) to[i] = {(int16_t)e, (int16_t)(row + rows * i), min(rows, m - rows * i)};
+            };
             tb.base[e] = row;
-            for (int i = 0; i * 16 < n[j]; ++i)
-                tb.blocks[b + i] = {(int16_t)e, (int16_t)(row + 16 * i), min(16, n[j] - 16 * i)};
+            put(tb.blocks + b, 16);
+            if (plan) put(plan->blocks + b + (kRows == 8 ? more : 0), kRows);
         }
-        at += n[j] | ((n[j] + 15) / 16) << 16;
+        at += counts(n[j]);
     }
+    const uint32_t blocks = total & 0x7FF, more = total >> 11 & 0x1FF;
+    if (plan && t == 0) plan->blocks_n = blocks + (kRows == 8 ? more : 0);
     __syncthreads();
     for (int a = t; a < A; a += kThreads) {
         const int e = ids[a], tk = a / p.k;
         const int row = tb.base[e] + __popcll(tb.mask[e] & ((1ull << tk) - 1));
-        Row v = {weights[a], 0, (int16_t)tk};
+        Row v = {weights[a], tk};
         if (FMT == kNvfp4) {
             const Scales s = a == t ? early : scales(a);
-            // |g|, |u| < 2^(norm + shift) times the largest weight, 2688 t1, so |h| is below the square of that: 2^exp
-            // times at most 2^15
-            const int b = s.x.norm + s.x.shift + __builtin_amdgcn_frexp_expf(s.t1 * 2688.0f);
             v.wt *= s.t2;
-            v.exp = (int16_t)(2 * b - 15);
-            scale[row] = {s.t1, s.x.shift};
+            t1[row] = s.t1;
         }
         tb.rows[row] = v;
     }
     __syncthreads();
-    return (int)uniform((uint32_t)total) >> 16;
+    return (int)uniform(blocks);
 }
 
 // Up to this many tokens every workgroup of fc1 chooses for itself: a launch of its own costs as much as adding eight tokens'
@@ -561,7 +538,7 @@ __device__ __forceinline__ uint32_t take(uint32_t* counter) {
 template <int FMT, int P, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
     static_assert(!WIDE || (FMT == kNvfp4 && Fmt<FMT>::D1 == 4), "four steps' scales");
-    constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
+    constexpr int NB = Fmt<FMT>::NB, D1 = Fmt<FMT>::D1, NF = Fmt<FMT>::kFrags;
     union Scratch {
         struct {
             float part[2][kWaves][NB][16][17];  // each wave's sums
@@ -576,25 +553,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
     __shared__ Table tb;
     __shared__ Scratch sc;
     __shared__ float bias[kMaxE];
-    __shared__ RowScale scale[FMT == kNvfp4 ? kMaxA : 1];
+    __shared__ float t1[FMT == kNvfp4 ? kMaxA : 1];
+    __shared__ u32x4 products[FMT == kNvfp4 ? 256 : 1];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int G = gridDim.x;
+    if constexpr (FMT == kNvfp4) fill_products(products);
+    Plan* plan = (int)blockIdx.x == G - 1 ? p.plan : nullptr;  // (by the workgroup with the fewest tasks)
     int V;
     if (p.T <= kOwnChoice) {
         load_bias(p, bias);
         choose_for<P, kOwnChoice>(p, 0, sc.c.val, bias, sc.c.ids, sc.c.weights);
         __syncthreads();
-        V = build<FMT>(tb, scale, p, sc.c.ids, sc.c.weights);
+        V = build<FMT>(tb, t1, plan, p, sc.c.ids, sc.c.weights);
     } else {
-        V = build<FMT>(tb, scale, p, p.ids, p.weights);
+        V = build<FMT>(tb, t1, plan, p, p.ids, p.weights);
     }
-    if ((int)blockIdx.x == G - 1) {  // (the one with the fewest tasks) for fc2 and the caller
+    if (plan) {  // the rest of it, and what the caller gets
         const int A = p.T * p.k;
-        if (threadIdx.x == 0) p.plan->blocks_n = V;
-        for (int i = threadIdx.x; i < V; i += kThreads) p.plan->blocks[i] = tb.blocks[i];
         for (int i = threadIdx.x; i < A; i += kThreads) {
-            p.plan->rows[i] = tb.rows[i];
+            plan->rows[i] = tb.rows[i];
             if (p.T <= kOwnChoice) {
                 p.ids[i] = sc.c.ids[i];
                 p.weights[i] = sc.c.weights[i];
@@ -604,7 +582,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
     }
 
     const int JB = (p.f + 8 * NB - 1) / (8 * NB), N1 = V * JB;
-    const auto xr = rsrc(FMT == kNvfp4 ? p.xh : p.x, (uint32_t)p.T * (uint32_t)p.d * 2u);
+    const auto xr = rsrc(FMT == kNvfp4 ? p.xp : p.x, (uint32_t)p.T * (uint32_t)p.d * 2u);
     const uint32_t rb = Fmt<FMT>::row_bytes(p.d);
     const int steps = (int)(rb + 63) / 64, part = (steps + kWaves - 1) / kWaves;
     const int chunks = (part + D1 - 1) / D1, s_first = wave * part, s_end = min(s_first + part, steps);
@@ -679,7 +657,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
                     for (int g = 0; g < NB; ++g) {
                         W16 w = st.w[j][g];
                         if (WIDE) w.sc = sc2[g][j >> 1 & 1];
-                        acc[g] = mfma<FMT>(WIDE && (j & 1) ? decode<FMT, true>(w, i) : decode<FMT>(w, i), st.x[j].v[i], acc[g]);
+                        acc[g] = mfma(WIDE && (j & 1) ? decode<FMT, true>(w, i, products) : decode<FMT>(w, i, products),
+                                      st.x[j].v[i], acc[g]);
                     }
                 fetch(st, j, tl, xl, sl + j);
                 __builtin_amdgcn_sched_barrier(0);  // (steps run into each other take 80 registers more and are slower)
@@ -708,33 +687,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
                     u[1] += s[8 + ej2];
                 }
                 float h[2];
-                RowScale rs{};
-                if (FMT == kNvfp4) rs = scale[t.row0 + em];
+                const float ts = FMT == kNvfp4 ? t1[t.row0 + em] : 1.0f;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if (FMT == kInt8) {
                         g[j] *= cs[j];
                         u[j] *= cs[2 + j];
                     } else if (FMT == kNvfp4) {
-                        g[j] = __builtin_amdgcn_ldexpf(g[j] * rs.t1, rs.shift);
-                        u[j] = __builtin_amdgcn_ldexpf(u[j] * rs.t1, rs.shift);
+                        g[j] *= ts;
+                        u[j] *= ts;
                     }
                     h[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[j])) * u[j];
                 }
-                uint16_t* o = p.h + ((int64_t)(t.row0 + em) * p.f + (col & ~7)) * HP + 2 * ep;
-                if (FMT == kNvfp4) {
-                    const int exp = tb.rows[t.row0 + em].exp;
-                    const half2v v = {(_Float16)__builtin_amdgcn_ldexpf(h[0], -exp),
-                                      (_Float16)__builtin_amdgcn_ldexpf(h[1], -exp)};
-                    *reinterpret_cast<uint32_t*>(o) = __builtin_bit_cast(uint32_t, v);
-                } else {
-                    const uint32_t hi = bf16x2_rne(h[0], h[1]);
-                    // (of an infinite h the first part is all)
-                    const float l0 = (hi & 0x7F80u) == 0x7F80u ? 0.0f : h[0] - __uint_as_float(hi << 16);
-                    const float l1 = (hi & 0x7F800000u) == 0x7F800000u ? 0.0f : h[1] - __uint_as_float(hi & 0xFFFF0000u);
-                    *reinterpret_cast<uint32_t*>(o) = hi;
-                    *reinterpret_cast<uint32_t*>(o + 8) = bf16x2_rne(l0, l1);
-                }
+                const int at = FMT == kNvfp4 && p.f % kWideF == 0 ? wide_group(col >> 3) : col >> 3;
+                uint16_t* o = p.h + (int64_t)(t.row0 + em) * p.f * 2 + at * 16 + 2 * ep;
+                const uint32_t hi = bf16x2_rne(h[0], h[1]);
+                // (of an infinite h the first part is all)
+                const float l0 = (hi & 0x7F80u) == 0x7F80u ? 0.0f : h[0] - __uint_as_float(hi << 16);
+                const float l1 = (hi & 0x7F800000u) == 0x7F800000u ? 0.0f : h[1] - __uint_as_float(hi & 0xFFFF0000u);
+                *reinterpret_cast<uint32_t*>(o) = hi;
+                *reinterpret_cast<uint32_t*>(o + 8) = bf16x2_rne(l0, l1);
             }
         }
         cur = nxt;
@@ -751,19 +723,30 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
 // rows are added in order at the end. Nothing but the operands is loaded inside the loop, so that no wait empties the
 // pipeline (int8 with the channel scales loaded there: four tokens 118 us instead of 102, 64 713 instead of 602). D2 of 6,
 // 10 or (bf16) 12, 16 is within 2 % of 8, the deeper ones on the slow side.
+//
+// The two parts of h are two products with one weight fragment. NVFP4's 16 bytes are four fragments, and both parts of them
+// would be 256 registers for D2 steps: there a block is at most eight tokens, columns 0 .. 7 of one product their upper and
+// 8 .. 15 their lower parts, and the two sums are added at the block's end. Blocks of 16 with both products and four steps in
+// flight: 64 tokens of 384 experts 442 us, 394 so; eight 129 and 115; only where most blocks are full are they a little
+// faster (64 tokens, all of 8 experts 137 and 146). What the lower part costs is its way through the L2: that last case
+// takes 113 us with one part, and its fc2 half as long without any h.
 template <int FMT, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
-    constexpr int D2 = 8, kOuts = kMaxT * 16 / kThreads, NF = Fmt<FMT>::kFrags, HP = Fmt<FMT>::kParts;
-    __shared__ Block blocks[kMaxV];
+    constexpr bool SPLIT = Fmt<FMT>::kRows == 8;
+    constexpr int D2 = 8, kOuts = kMaxT * 16 / kThreads, NF = Fmt<FMT>::kFrags, HP = SPLIT ? 1 : 2;
+    __shared__ Block blocks[SPLIT ? kMaxV8 : kMaxV];
     __shared__ Row rows[kMaxA];
     __shared__ float sums[kWaves][kMaxT][17];
     __shared__ f32x4 channel[FMT == kInt8 ? kMaxV : 1][4];  // s2 of the 16 columns, per block
+    __shared__ u32x4 products[FMT == kNvfp4 ? 256 : 1];
     const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int hrow = SPLIT ? r & 7 : r, low = SPLIT ? r >> 3 : 0;  // row of the block, and part, in this lane's column
+    if constexpr (FMT == kNvfp4) fill_products(products);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int A = p.T * p.k, V = (int)uniform((uint32_t)p.plan->blocks_n);
     for (int i = threadIdx.x; i < p.max_blocks; i += kThreads) blocks[i] = p.plan->blocks[i];
     for (int i = threadIdx.x; i < A; i += kThreads) rows[i] = p.plan->rows[i];
-    const auto hr = rsrc(p.h, (uint32_t)A * (uint32_t)p.f * (2u * HP));
+    const auto hr = rsrc(p.h, (uint32_t)A * (uint32_t)p.f * 4u);
     const uint32_t rb = Fmt<FMT>::row_bytes(p.f);
     const int S = (int)(rb + 63) / 64, total = V * S;
     constexpr int kUnit = WIDE ? 4 : 1;  // steps whose scales are one load; a block is whole units of them
@@ -791,20 +774,20 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
     auto enter = [&](int v) {
         const Block b = blocks[min(v, V - 1)];
         m = Matrix<FMT>(p.w2, p.s2, (int)uniform((uint32_t)(int)b.e), p.d, p.f);
-        at = ((uint32_t)(int)uniform((uint32_t)(int)b.row0) + r) * (uint32_t)p.f * (2u * HP);
-        x_ok = r < (int)uniform((uint32_t)b.n);
+        at = ((uint32_t)(int)uniform((uint32_t)(int)b.row0) + hrow) * (uint32_t)p.f * 4u + 16 * low;
+        x_ok = hrow < (int)uniform((uint32_t)b.n);
     };
     auto fetch = [&](int j, bool live) {
         const uint32_t o = (uint32_t)ls * 64 + q * 16;
         const bool ok = live & (o < rb);
         if (WIDE && (j & 3) == 0) raw[j >> 2] = m.scales((uint32_t)(n0 + r), ls + q, live & w_ok);
         w[j] = m.template load<WIDE>((uint32_t)(n0 + r), o, ok & w_ok);
-        const uint32_t from = (ok & x_ok) ? at + o / 16 * (NF * HP * 16) : kNowhere;
+        const uint32_t from = (ok & x_ok) ? at + (WIDE ? (uint32_t)ls * 512u + q * 32 : o / 16 * (NF * 32)) : kNowhere;
 #pragma unroll
         for (int i = 0; i < NF; ++i)
 #pragma unroll
             for (int half = 0; half < HP; ++half)
-                x[j][i][half] = __builtin_amdgcn_raw_buffer_load_b128(hr, from + 16 * (HP * i + half), 0, 0);
+                x[j][i][half] = __builtin_amdgcn_raw_buffer_load_b128(hr, from + (WIDE ? 128 : 32) * i + 16 * half, 0, 0);
         if (++ls == S) {
             ls = 0;
             enter(++lv);
@@ -830,22 +813,27 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc2(Args p) {
                 if (WIDE) wj.sc = sc2[j >> 1 & 1];
 #pragma unroll
                 for (int i = 0; i < NF; ++i) {
-                    const u32x4 v = WIDE && (j & 1) ? decode<FMT, true>(wj, i) : decode<FMT>(wj, i);
+                    const u32x4 v = WIDE && (j & 1) ? decode<FMT, true>(wj, i, products) : decode<FMT>(wj, i, products);
 #pragma unroll
-                    for (int half = 0; half < HP; ++half) acc = mfma<FMT>(v, x[j][i][half], acc);
+                    for (int half = 0; half < HP; ++half) acc = mfma(v, x[j][i][half], acc);
                 }
             }
             fetch(j, i0 + D2 + j < end);
             __builtin_amdgcn_sched_barrier(0);  // (four int8 tokens 102.5 us without, 100 with)
             if (i0 + j < end && (++cs == S || i0 + j + 1 == end)) {
                 const Block b = blocks[cv];
+                if (SPLIT) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // of lane r + 8
+                        acc[i] += __uint_as_float(dpp_u32<0x128>(__float_as_uint(acc[i])));
+                }
                 if (r < b.n) {
                     const Row row = rows[b.row0 + r];
                     float* o = sums[wave][row.token] + 4 * q;
                     if (FMT == kInt8) acc *= channel[cv][q];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        o[i] = __builtin_fmaf(row.wt, FMT == kNvfp4 ? __builtin_amdgcn_ldexpf(acc[i], row.exp) : acc[i], o[i]);
+                        o[i] = __builtin_fmaf(row.wt, acc[i], o[i]);
                 }
                 acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
                 cs = 0;
@@ -881,15 +869,15 @@ int router_parts(int64_t T, int64_t d, int64_t E) {
     const int64_t blocks = std::max<int64_t>(1, (E + 15) / 16 * ((T + 15) / 16));
     return (int)std::max<int64_t>(1, std::min({(200 + blocks - 1) / blocks, d / (32 * 4 * kRouterWaves), (int64_t)kMaxParts}));
 }
-size_t carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t f, Args* p) {
+// `rows`: tokens of a block in fc2.
+size_t carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t f, int rows, Args* p) {
     p->parts = router_parts(T, d, E);
-    p->max_blocks = (int)std::min<int64_t>(T * k, E + T * k / 16);
+    p->max_blocks = (int)std::min<int64_t>(T * k, E + T * k / rows);
     p->tail = c.take<uint32_t>(1);
     p->plan = c.take<Plan>(1);
     p->logits = c.take<double>((size_t)(p->parts * T * E));
     p->h = c.take<uint16_t>((size_t)(2 * T * k * f));
-    p->xh = c.take<uint16_t>((size_t)(T * d));
-    p->xs = c.take<TokenScale>((size_t)T);
+    p->xp = c.take<uint16_t>((size_t)(T * d));
     return c.need;
 }
 
@@ -898,7 +886,7 @@ void launch_fc1(const Args& p, hipStream_t s) {
     constexpr int NB = Fmt<FMT>::NB;
     if (p.T > kOwnChoice)
         hipLaunchKernelGGL(k_decode_choice<P>, dim3((unsigned)p.T), dim3(kThreads), 0, s, p);
-    const int64_t tasks = (int64_t)p.max_blocks * ((p.f + 8 * NB - 1) / (8 * NB));
+    const int64_t blocks = std::min<int64_t>(p.T * p.k, p.E + p.T * p.k / 16), tasks = blocks * ((p.f + 8 * NB - 1) / (8 * NB));
     const dim3 grid((unsigned)std::min<int64_t>(tasks, device_cus()));
     if constexpr (FMT == kNvfp4) {
         if (p.d % 128 == 0) {  // whole steps
@@ -912,7 +900,7 @@ template <int FMT>
 void launch_fc2(const Args& p, hipStream_t s) {
     const dim3 grid((unsigned)(p.d + 15) / 16);
     if constexpr (FMT == kNvfp4) {
-        if (p.f % 512 == 0) {  // blocks of whole groups of four steps
+        if (p.f % kWideF == 0) {
             hipLaunchKernelGGL((k_decode_fc2<FMT, true>), grid, dim3(kThreads), 0, s, p);
             return;
         }
@@ -946,10 +934,10 @@ int layer(const uint16_t* x, int64_t T, int64_t d, const uint16_t* w_router, con
         return NVQ_ERR_ALIGN;
     Args p{};
     Carver need(nullptr);
-    if (ws_bytes < carve(need, T, d, k, E, f, &p)) return NVQ_ERR_WORKSPACE;
+    if (ws_bytes < carve(need, T, d, k, E, f, Fmt<FMT>::kRows, &p)) return NVQ_ERR_WORKSPACE;
     if (T == 0) return NVQ_OK;
     Carver cv(ws);
-    carve(cv, T, d, k, E, f, &p);
+    carve(cv, T, d, k, E, f, Fmt<FMT>::kRows, &p);
     p.x = x; p.wr = w_router; p.bias = bias;
     p.w1 = w1; p.s1 = s1; p.t1 = t1;
     p.w2 = w2; p.s2 = s2; p.t2 = t2;
@@ -970,7 +958,7 @@ size_t moe_layer_decode_workspace_size(int64_t T, int64_t d, int k, int64_t E, i
     if (T < 0 || T > kMaxT || d < 0 || d > (1 << 22) || k < 1 || k > kMaxK || E < 1 || E > kMaxE || d_ff < 0 || d_ff > (1 << 22)) return 0;
     Carver c(nullptr);
     Args p{};
-    return carve(c, T, d, k, E, d_ff, &p);
+    return carve(c, T, d, k, E, d_ff, 8, &p);
 }
 
 int moe_layer_decode_bf16(const uint16_t* x, int64_t T, int64_t d, const uint16_t* w_router, const float* bias, int router,
