@@ -39,6 +39,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -219,10 +220,11 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // ------------------------------------------------------------------ router logits
-// One workgroup: 16 experts, 16 tokens, a part of K, shared by its four waves. The sum of 32 products that one
-// instruction adds is rounded to fp32, 2^-24 of it; from there on the sums are fp64, so that of two close logits the
-// larger one is chosen. K is cut so that a token's logits are some 200 workgroups: with one per 16 experts (24 of 384)
-// the launch took 6.6 us.
+// One workgroup: 16 experts, 16 tokens, a part of K, shared by its four waves. Products and sums are fp64, so that of two
+// close logits the larger one is chosen: the bf16 instruction's sum of 32 products is off by up to 2^-21 of their magnitudes
+// (1 and 31 products of 2^-28 give 1), which chooses wrongly where x has a few large values. Its launch takes 3.7 us for one
+// token of 384 experts and 7.7 for 64, this one 4.5 and 11.3. K is cut so that a token's logits are some 200 workgroups: with
+// one per 16 experts (24 of 384) the bf16 launch took 6.6 us.
 constexpr int kRouterWaves = 4, kRouterThreads = 64 * kRouterWaves;
 
 // x of token t in the order of decoded codes for NVFP4 weights (one workgroup).
@@ -255,7 +257,10 @@ __global__ __launch_bounds__(kRouterThreads) void k_decode_router(Args p) {
     const auto wr = rsrc(p.wr, (uint32_t)p.E * rb), xr = rsrc(p.x, (uint32_t)p.T * rb);
     const int steps = (p.d + 31) / 32, waves = p.parts * kRouterWaves, part = (steps + waves - 1) / waves;
     const int first = (z * kRouterWaves + wave) * part, s1 = min(first + part, steps);
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+    auto value = [](u32x4 u, int v) {
+        return (double)__uint_as_float(v & 1 ? u[v >> 1] & 0xFFFF0000u : u[v >> 1] << 16);
+    };
     for (int s0 = first; s0 < s1; s0 += 4) {
         u32x4 w[4], x[4];
 #pragma unroll
@@ -266,14 +271,14 @@ __global__ __launch_bounds__(kRouterThreads) void k_decode_router(Args p) {
             x[j] = __builtin_amdgcn_raw_buffer_load_b128(xr, ok && t0 + r < p.T ? (t0 + r) * rb + o : kNowhere, 0, 0);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f32x4 a = mfma(w[j], x[j], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] += (double)a[i];
-        }
+            for (int v = 0; v < 8; ++v)  // lane: value v of its eight of K
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(value(w[j], v), value(x[j], v), acc, 0, 0, 0);
     }
+    // lane: experts q + 4 i of token r
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][r][4 * q + i] = acc[i];
+    for (int i = 0; i < 4; ++i) red[wave][r][q + 4 * i] = acc[i];
     __syncthreads();
     const int e = threadIdx.x & 15, t = threadIdx.x >> 4;
     double v = red[0][t][e];
