@@ -181,7 +181,9 @@ bool gemm16_dims_ok(int mode, bool glu, int64_t rows, int64_t E, int64_t M, int6
 //   384 of 2048 x 4096, R =  341   5311, 4134   3569, 3020        1 of 2048 x 4096, R = 4096    70, 120    68, 118
 //    64 of 1024 x 1024, R =  256    100,   76     57,   57        1 of 4096 x 4096, R = 4096   149, 133   141, 131
 //   384 of 4096 x 1024, R =  341, accumulating   3867, 3618   2785, 2821
-// The rule takes the faster side of each, or one within 1.5 %; outputs twice as wide change none of them.
+// The rule takes the faster side of each, or one within 1.5 %; outputs twice as wide change none of them. int8, small against
+// big: 2048 x 4096 x 4096 41, 52; 4096^3 82, 60; 3000 x 7000 x 1008 44, 42; 6000 x 6000 x 608 44, 44; fc1 of 384 experts at
+// 4096 tokens 616, 712, at 8192 1001, 787; fc2 398, 407 and 618, 500: the faster side of each too.
 static bool big_tiles(double big, double small, int cus) {
     const double t_small = small <= cus ? 7.0 : 11.0 * std::max(1.0, small / (2.0 * cus));
     return 13.0 * std::max(1.0, std::ceil(big / cus)) < t_small;
@@ -209,7 +211,10 @@ static void launch(int mode, int epi, Args p, void* ws, hipStream_t s) {
     // Few tiles leave the 128 x 128 kernel with the latency of its K steps, 0.55 us each however few its workgroups; the
     // skinny kernel's time is that of its traffic: x once per 16 rows of weights, at about 8 TB/s from the caches, and the
     // weights once per block of rows, at about 5. (One token, 384 experts, fc1: 30 us against 47; two tokens: 60 against
-    // 50; 32 rows x 4096 x 4096: 15 against 37; 512 x 1024 x 4096: 43 against 37.)
+    // 50; 32 rows x 4096 x 4096: 15 against 37; 512 x 1024 x 4096: 43 against 37.) int8, skinny against tiles: 64 rows x 4096
+    // x 4096 14.6, 19.9; 128 23.8, 19.3; 256 x 1024 x 4096 12.8, 19.1; 512 22.4, 19.3; 384 experts, fc1 of one token 17.4,
+    // 22.6, of two 29.4, 26.9, of four 55, 49: the faster side of each; fc2 of one token 12.3, 14.0, of two 20.1, 22.0, of
+    // four 37, 32: the slower one for one and two.
     const int64_t active = p.seg ? std::min<int64_t>(p.E, p.rows) : 1;
     if (mode == kFwd) {
         const int64_t blocks = epi == kEpiGlu ? p.N / 8 : (p.N + 15) / 16;
