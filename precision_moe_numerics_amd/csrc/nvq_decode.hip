@@ -222,9 +222,10 @@ __device__ __forceinline__ void lds_barrier() {
 // ------------------------------------------------------------------ router logits
 // One workgroup: 16 experts, 16 tokens, a part of K, shared by its four waves. Products and sums are fp64, so that of two
 // close logits the larger one is chosen: the bf16 instruction's sum of 32 products is off by up to 2^-21 of their magnitudes
-// (1 and 31 products of 2^-28 give 1), which chooses wrongly where x has a few large values. Its launch takes 3.7 us for one
-// token of 384 experts and 7.7 for 64, this one 4.5 and 11.3. K is cut so that a token's logits are some 200 workgroups: with
-// one per 16 experts (24 of 384) the bf16 launch took 6.6 us.
+// (1 and 31 products of 2^-28 give 1), which chooses wrongly where x has a few large values. Its launch took 3.7 us for one
+// token of 384 experts and 7.7 for 64, this one takes 4.5 and 7.5. K is cut so that a token's logits are some 800 workgroups,
+// or eight parts: the fp64 products are the most of its time, and 64 tokens in three parts, 288 workgroups on 256 CUs, take
+// 11.4 us, in five 8.7.
 constexpr int kRouterWaves = 4, kRouterThreads = 64 * kRouterWaves;
 
 // x of token t in the order of decoded codes for NVFP4 weights (one workgroup).
@@ -869,10 +870,10 @@ bool dims_ok(int64_t T, int64_t d, int64_t E, int k, int64_t f) {
     return 2 * f * (int64_t)Fmt<FMT>::row_bytes((int)d) <= kMaxBytes && d * (int64_t)Fmt<FMT>::row_bytes((int)f) <= kMaxBytes &&
            E * d * 2 <= kMaxBytes && T * k * f * 4 <= kMaxBytes;
 }
-// Parts of K of the router's product: some 200 workgroups in all, of at least four steps a wave.
+// Parts of K of the router's product: some 800 workgroups in all, of at least four steps a wave.
 int router_parts(int64_t T, int64_t d, int64_t E) {
     const int64_t blocks = std::max<int64_t>(1, (E + 15) / 16 * ((T + 15) / 16));
-    return (int)std::max<int64_t>(1, std::min({(200 + blocks - 1) / blocks, d / (32 * 4 * kRouterWaves), (int64_t)kMaxParts}));
+    return (int)std::max<int64_t>(1, std::min({(800 + blocks - 1) / blocks, d / (32 * 4 * kRouterWaves), (int64_t)kMaxParts}));
 }
 // `rows`: tokens of a block in fc2.
 size_t carve(Carver& c, int64_t T, int64_t d, int k, int64_t E, int64_t f, int rows, Args* p) {
