@@ -8,7 +8,7 @@ import precision_moe_numerics_amd as nvq
 from bf16_ref import check, out_bound
 from decode_ref import check_choice, layer, route, values
 from gpu_util import require_gpu
-from test_gpu_decode import case, rnd, run_case
+from test_gpu_decode import SIZES, case, rnd, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,15 @@ def test_every_finite_scale_byte_of_both_signs(T, d, f):
     for w in (w1, w2):
         w[1][w[1] >= 127] += 1  # 0x7F is NaN; the last byte is then 0xFE
     verify(a, w1, w2)
+
+
+@pytest.mark.parametrize("T,d,E,k,f", SIZES)
+def test_every_size_within_the_other_formats_bound(T, d, E, k, f):
+    verify(*case("nvfp4", T, d, E, k, f, sigmoid=k % 2 == 1, bias=True, residual=T % 2 == 0))
+
+
+@pytest.mark.parametrize("T", [8, 9, 15, 16, 17, 24, 25, 31, 64])
+@pytest.mark.parametrize("f", [96, 512])
+def test_blocks_of_eight_tokens(T, f):
+    """One expert of every token beside others of a few: blocks of eight that are full, one short, one over."""
+    verify(*case("nvfp4", T, 128, 12, 3, f, hot=50.0, residual=False))
