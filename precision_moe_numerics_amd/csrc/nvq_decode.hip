@@ -16,11 +16,11 @@
 // Noticing that the last workgroup is done and reading h past the caches costs
 // more than a launch.
 //
-// Bound by reading the chosen experts' weights once. The activations are not
-// quantized: they are a few rows, and it would save nothing. A weight reaches
-// the matrix pipe as the bf16 value that holds it exactly (int8 codes have 8
-// significant bits, e2m1 * e4m3 has 6); the channel's or tensor's fp32 scale is
-// applied to the fp32 sum.
+// Bound by reading the chosen experts' weights, once per 16 tokens of an expert
+// (NVFP4's fc2: eight). The activations are not quantized: they are a few rows,
+// and it would save nothing. A weight reaches the matrix pipe as the bf16 value
+// that holds it exactly (int8 codes have 8 significant bits, e2m1 * e4m3 has 6);
+// the channel's or tensor's fp32 scale is applied to the fp32 sum.
 //
 // The other operand is x as it is, and h as two bf16 parts, its rounding and the
 // rounding of what that left (2^-16 of it in all; one part would be 2^-8, as much
@@ -193,7 +193,7 @@ struct Matrix {
 // NVFP4, WIDE: four steps' scales as one load, lane l taking the eight bytes of step l / 16, of which lane 16 j + r wants
 // bytes 2 j, 2 j + 1 of each: a 4 x 4 transposition between the lanes of a row. sc[0]: steps 0, 1; sc[1]: 2, 3. Two bytes
 // per lane and step, as `load` takes them, are a memory instruction for each weight instruction: the 384-expert layer's 64
-// tokens take 497 us with those, 377 so, eight 143 and 113, one 38 and 34.
+// tokens took 497 us with those, 377 so, eight 143 and 113, one 38 and 34 (with h in one part).
 __device__ __forceinline__ void spread(u32x2 v, int lane, uint32_t (&sc)[2]) {
     const uint32_t half = lane & 16 ? 0x07060302u : 0x05040100u;
     const auto ab = __builtin_amdgcn_permlane32_swap(v[0], v[1], false, false);
@@ -522,7 +522,9 @@ __global__ __launch_bounds__(kThreads) void k_decode_choice(Args p) {
 // ------------------------------------------------------------------ fc1 + SwiGLU
 // One persistent workgroup per CU. A task is one block of tokens and 8 NB gate rows with their up rows; the waves share K
 // and their sums meet in LDS, added in order. A wave's loads run ahead across the tasks' ends: D1 steps, 8 KiB of weights,
-// are in flight all the time, 64 KiB per CU, which the memory serves at 5.4 to 5.6 TB/s (twice as many were no faster).
+// are in flight all the time, 64 KiB per CU (twice as many were no faster): 64 tokens read the w1 of the 210 of 384 experts
+// that they hit at 4.8 TB/s (bf16, 731 us), 4.7 (int8, 375) and 4.0 (NVFP4, 246: a wave has four loads of x for two of
+// weights), one bf16 token that of its eight at 4.1.
 template <int FMT>
 struct Stage1 {  // operands of a wave in flight
     u32x2 raw[Fmt<FMT>::NB];  // WIDE: scales of the steps
@@ -724,7 +726,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
 }
 
 // ------------------------------------------------------------------ fc2 + combine
-// A workgroup owns 16 columns of out. Its waves share the (block, K step) pairs of all chosen experts in equal contiguous
+// A workgroup owns 16 columns of out: d = 4096 is one per CU, fewer columns leave CUs without work (64 tokens of 384 experts
+// read w2 at 4.3, 3.3 and 3.0 TB/s in bf16, int8 and NVFP4 with d = 4096, at 2.6, 1.9 and 1.7 with 2048). Its waves share the (block, K step) pairs of all chosen experts in equal contiguous
 // runs, D2 steps in flight; where a run leaves a block, the wave adds weight * sum to its own token rows in LDS. The waves'
 // rows are added in order at the end. Nothing but the operands is loaded inside the loop, so that no wait empties the
 // pipeline (int8 with the channel scales loaded there: four tokens 118 us instead of 102, 64 713 instead of 602). D2 of 6,
