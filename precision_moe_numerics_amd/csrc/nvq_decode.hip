@@ -726,12 +726,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_decode_fc1(Args p) {
 }
 
 // ------------------------------------------------------------------ fc2 + combine
-// A workgroup owns 16 columns of out: d = 4096 is one per CU, fewer columns leave CUs without work (64 tokens of 384 experts
-// read w2 at 4.3, 3.3 and 3.0 TB/s in bf16, int8 and NVFP4 with d = 4096, at 2.6, 1.9 and 1.7 with 2048). Its waves share the (block, K step) pairs of all chosen experts in equal contiguous
-// runs, D2 steps in flight; where a run leaves a block, the wave adds weight * sum to its own token rows in LDS. The waves'
-// rows are added in order at the end. Nothing but the operands is loaded inside the loop, so that no wait empties the
-// pipeline (int8 with the channel scales loaded there: four tokens 118 us instead of 102, 64 713 instead of 602). D2 of 6,
-// 10 or (bf16) 12, 16 is within 2 % of 8, the deeper ones on the slow side.
+// A workgroup owns 16 columns of out: d = 4096 is one per CU, fewer columns leave CUs without work (64 tokens of 384
+// experts read w2 at 4.3, 3.3 and 3.0 TB/s in bf16, int8 and NVFP4 with d = 4096, at 2.6, 1.9 and 1.7 with 2048). Its waves
+// share the (block, K step) pairs of all chosen experts in equal contiguous runs, D2 steps in flight; where a run leaves a
+// block, the wave adds weight * sum to its own token rows in LDS. The waves' rows are added in order at the end. Nothing
+// but the operands is loaded inside the loop, so that no wait empties the pipeline (int8 with the channel scales loaded
+// there: four tokens 118 us instead of 102, 64 713 instead of 602). D2 of 6, 10 or (bf16) 12, 16 is within 2 % of 8, the
+// deeper ones on the slow side.
 //
 // The two parts of h are two products with one weight fragment. NVFP4's 16 bytes are four fragments, and both parts of them
 // would be 256 registers for D2 steps: there a block is at most eight tokens, columns 0 .. 7 of one product their upper and
